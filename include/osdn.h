@@ -1,7 +1,8 @@
 /*
  * osdn.h - C ABI of libosdn.so: the Online Scaled DeltaNet (OSDN) forward, its
  * backward (gradients for training) and single-token decode on NVIDIA B200
- * (sm_100a).
+ * (sm_100a); with it what a layer needs next to them: a gated linear recurrence, the
+ * norms of queries and keys with the position rotation, and the rotation alone.
  *
  * Method: "OSDN: Improving Delta Rule with Provable Online Preconditioning in
  * Linear Attention" (gist.science technical summary).
@@ -396,6 +397,171 @@ int osdn_fwd_host(const osdn_params *p,
  * `groups` (as in osdn_fwd_host), written to *bytes.
  * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED. */
 int osdn_fwd_host_buffer_size(const osdn_params *p, int groups, size_t *bytes);
+
+/* Gated linear recurrence over the tokens of every channel (a token mixer with a
+ * vector state, beside the matrix states above):
+ *     h_t = a_t h_{t-1} + s_t x_t            for each of D channels,
+ *     a_t = gate (OSDN_GATE_DECAY), exp(gate) (OSDN_GATE_LOG) or
+ *           1 / (1 + exp(-gate)) (OSDN_GATE_LOGIT);
+ *     s_t = 1 (OSDN_INPUT_NONE), 1 - a_t (OSDN_INPUT_COMPLEMENT) or
+ *           sqrt(1 - a_t^2) (OSDN_INPUT_NORM; a_t in [0, 1]).
+ * a_t = 0 (gate 0, or -infinity in the other forms) starts a new document. 1 - a
+ * is formed from the gate without cancellation; products, states and sums are
+ * fp32. A non-finite state stays non-finite (0 times infinity is NaN). */
+typedef enum { OSDN_GATE_DECAY = 0, OSDN_GATE_LOG = 1, OSDN_GATE_LOGIT = 2 } osdn_gate_form;
+typedef enum { OSDN_INPUT_NONE = 0, OSDN_INPUT_COMPLEMENT = 1, OSDN_INPUT_NORM = 2 } osdn_input_scale;
+
+/* Tokens between the states that osdn_recur_fwd saves for osdn_recur_bwd. */
+#define OSDN_RECUR_CHECKPOINT 64
+
+typedef struct {
+    uint32_t struct_size;   /* must be sizeof(osdn_recur_params) */
+    int32_t B;              /* sequences, >= 1 */
+    int32_t T;              /* tokens per sequence, 0 .. 2^30 (osdn_recur_step: ignored) */
+    int32_t D;              /* channels, 1 .. 2^24 */
+    int32_t dtype;          /* osdn_dtype of x and h (and dh, dx) */
+    int32_t gate_dtype;     /* osdn_dtype of gate (and dgate): dtype, or OSDN_FP32 */
+    int32_t gate_form;      /* osdn_gate_form */
+    int32_t input_scale;    /* osdn_input_scale */
+    /* Element strides of x, gate and h over (b, t); the channels are contiguous.
+     * Both zero: dense [B, T, D]. Otherwise 0 .. 2^38; those of h keep its rows
+     * apart. stride_h is also the stride of dh in the backward; dx and dgate are
+     * dense. osdn_recur_step reads the b strides alone. */
+    int64_t stride_x[2];
+    int64_t stride_gate[2];
+    int64_t stride_h[2];
+} osdn_recur_params;
+
+/* Forward. x, gate [B, T, D]; h0 [B, D] fp32 (NULL: zeros); lengths [B] int32 in
+ * device memory (NULL: T each; a value is taken as 0 .. T): tokens from a
+ * sequence's length on are not read, and their rows of h are left as they were.
+ * h [B, T, D] (NULL: not written); final_h [B, D] fp32, the state after each
+ * sequence's last token (h0 for length 0; nullable); checkpoints
+ * [B, ceil(T / 64), D] fp32, the state before every 64th token, for the backward
+ * (nullable). Any D, T and element-aligned x, gate and h are accepted (16-byte
+ * aligned rows with D a multiple of 4 run fastest); fp32 states are 16-byte
+ * aligned. h must not overlap x or gate. No workspace; bitwise reproducible.
+ * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */
+int osdn_recur_fwd(const osdn_recur_params *p, const void *x, const void *gate, const float *h0,
+                   const int32_t *lengths, void *h, float *final_h, float *checkpoints, void *cuda_stream);
+
+/* Gradients of L = <dh, h> + <dfinal_h, final_h>: dx [B, T, D] in dtype, dgate
+ * [B, T, D] in gate_dtype (dense, required when T > 0), dh0 [B, D] fp32 (nullable).
+ * The derivative is with respect to the gate as given. dh has stride_h; dfinal_h
+ * [B, D] fp32 (NULL: 0). checkpoints: what osdn_recur_fwd wrote for the same x, gate,
+ * h0 and lengths, or NULL: the call runs the forward again for them, in a workspace
+ * of osdn_recur_bwd_workspace_size() bytes (unused, and nullable, with checkpoints).
+ * Where s_t = 0 in OSDN_INPUT_NORM (a_t = 1) the root's unbounded slope counts as
+ * 0. Rows of dx and dgate from a sequence's length on are left as they were. Bitwise
+ * reproducible. dx and dgate must not overlap an input.
+ * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */
+int osdn_recur_bwd_workspace_size(const osdn_recur_params *p, size_t *bytes);
+
+int osdn_recur_bwd(const osdn_recur_params *p, const void *x, const void *gate, const float *h0,
+                   const int32_t *lengths, const void *dh, const float *dfinal_h, const float *checkpoints,
+                   void *dx, void *dgate, float *dh0, void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* One decode token: state [B, D] fp32 is updated in place, h [B, D] receives it in
+ * dtype. x, gate [B, D] (rows at the b strides). p->T is ignored.
+ * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */
+int osdn_recur_step(const osdn_recur_params *p, const void *x, const void *gate, float *state, void *h,
+                    void *cuda_stream);
+
+/* Norms of queries and keys for each head, with the position rotation in the same
+ * pass: what the delta rule's q and k go through before osdn_fwd. For every row x
+ * (one token and head, `width` features):
+ *     y = scale x / sqrt(sum x^2 + eps)           (OSDN_NORM_L2)
+ *     y = scale w x / sqrt(mean x^2 + eps)        (OSDN_NORM_RMS; w NULL: ones)
+ *     y = scale x                                 (OSDN_NORM_NONE)
+ * (w also applies under OSDN_NORM_L2), then on the first rot_dim features the pairs
+ * (i, j) = (i, i + rot_dim / 2) (OSDN_ROPE_HALF) or (2 i, 2 i + 1)
+ * (OSDN_ROPE_INTERLEAVED) turn:
+ *     (y_i, y_j) <- amplitude (y_i cos - y_j sin, y_j cos + y_i sin),
+ *     angle = position freqs[pair], formed in 64 bits.
+ * Sums are fp32; a row whose sum and eps are both 0 gives zeros. */
+typedef enum { OSDN_NORM_NONE = 0, OSDN_NORM_L2 = 1, OSDN_NORM_RMS = 2 } osdn_norm;
+typedef enum { OSDN_ROPE_HALF = 0, OSDN_ROPE_INTERLEAVED = 1 } osdn_rope_layout;
+
+typedef struct {
+    uint32_t struct_size;   /* must be sizeof(osdn_qk_params) */
+    int32_t B;              /* sequences, >= 1 */
+    int32_t T;              /* tokens per sequence, >= 0 */
+    int32_t Hq, Hk;         /* heads of q and of k (Hk = 0: no k) */
+    int32_t width;          /* features of a head: a multiple of 8 up to 256 */
+    int32_t dtype;          /* osdn_dtype of q, k and their outputs and gradients */
+    int32_t norm;           /* osdn_norm */
+    int32_t layout;         /* osdn_rope_layout */
+    int32_t rot_dim;        /* rotated features: even, 0 (none) .. width; OSDN_ROPE_HALF: a multiple of 16 */
+    float eps;              /* >= 0 */
+    float amplitude;        /* factor on the rotated features (1: a pure rotation) */
+    float scale_q, scale_k; /* factors on q and k */
+    int64_t pos0;           /* position of token 0 where positions is NULL */
+    /* Element strides over (b, t, h), as in osdn_params: all zero for dense
+     * [B, T, H, width], else non-negative multiples of 8; those of outputs keep
+     * the rows apart. out_q and out_k: q_out and k_out in the forward, the
+     * upstream gradients dq_out and dk_out in the backward. */
+    int64_t stride_q[3];
+    int64_t stride_k[3];
+    int64_t stride_out_q[3];
+    int64_t stride_out_k[3];
+} osdn_qk_params;
+
+/* Forward: q [B, T, Hq, width] to q_out, k [B, T, Hk, width] to k_out. wq, wk [width]
+ * fp32 (NULL: ones; not with OSDN_NORM_NONE). positions [B, T] int64, any sign
+ * (NULL: pos0 + t); freqs [rot_dim / 2] fp64 in device memory (osdn_rope_freqs).
+ * lengths [B] int32 (NULL: T each): tokens from a sequence's length on are not read
+ * and their output rows are left as they were. q_out may be q itself, and k_out k, with
+ * the same strides; else the outputs must not overlap the inputs. All pointers
+ * 16-byte aligned. k, wk, k_out are ignored when Hk = 0.
+ * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */
+int osdn_qk_fwd(const osdn_qk_params *p, const void *q, const void *k, const float *wq, const float *wk,
+                const int64_t *positions, const double *freqs, const int32_t *lengths, void *q_out, void *k_out,
+                void *cuda_stream);
+
+/* Gradients of L = <dq_out, q_out> + <dk_out, k_out>: dq, dk (dense, input dtype) and
+ * dwq, dwk [width] fp32 (nullable each; sums over every live token and head in a
+ * fixed order, so results are bitwise reproducible on one device). Same inputs
+ * as the forward; rows of dq and dk from a sequence's length on are left as they
+ * were. workspace: osdn_qk_bwd_workspace_size() bytes, 16-byte aligned, no
+ * initialisation (nullable when dwq and dwk both are).
+ * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */
+int osdn_qk_bwd_workspace_size(const osdn_qk_params *p, size_t *bytes);
+
+int osdn_qk_bwd(const osdn_qk_params *p, const void *q, const void *k, const float *wq, const float *wk,
+                const int64_t *positions, const double *freqs, const int32_t *lengths, const void *dq_out,
+                const void *dk_out, void *dq, void *dk, float *dwq, float *dwk, void *workspace,
+                size_t workspace_bytes, void *cuda_stream);
+
+/* The rotation alone on one tensor x [B, T, Hq, width] (strides stride_q, output
+ * stride_out_q; Hk and scale_k are ignored): out = scale_q times the rotated x. inverse != 0
+ * turns back by the same angles with the same amplitude, the transpose: it takes
+ * the gradient of out to that of x. p->norm must be OSDN_NORM_NONE and rot_dim > 0. out may
+ * be x with the same strides. Other arguments as osdn_qk_fwd.
+ * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */
+int osdn_rope(const osdn_qk_params *p, const void *x, const int64_t *positions, const double *freqs,
+              const int32_t *lengths, void *out, int inverse, void *cuda_stream);
+
+/* Frequencies of the rotation, freqs[i] = base^(-2 i / rot_dim) for i < rot_dim / 2, scaled
+ * for contexts `factor` times longer than the original_length trained on:
+ *   OSDN_ROPE_PLAIN       as they are;
+ *   OSDN_ROPE_LINEAR      freqs / factor (position interpolation);
+ *   OSDN_ROPE_NTK         base * factor^(rot_dim / (rot_dim - 2)) in place of base: the
+ *                         fastest pair unchanged, the slowest divided by factor;
+ *   OSDN_ROPE_YARN        pairs that turn more than high_turns times over original_length
+ *                         unchanged, fewer than low_turns divided by factor, a linear ramp
+ *                         over the pair's index between (its ends rounded outwards to whole
+ *                         indices); amplitude 0.1 ln(factor) + 1;
+ *   OSDN_ROPE_WAVELENGTH  the same with the ramp linear in the number of turns:
+ *                         freq ((1 - m) / factor + m), m = (turns - low_turns) /
+ *                         (high_turns - low_turns) held in [0, 1].
+ * Writes rot_dim / 2 doubles to HOST memory freqs and the amplitude (1 except YARN) to
+ * *amplitude (nullable). Runs on the host; needs no GPU.
+ * Errors: OSDN_ERR_INVALID_ARG. */
+typedef enum { OSDN_ROPE_PLAIN = 0, OSDN_ROPE_LINEAR = 1, OSDN_ROPE_NTK = 2, OSDN_ROPE_YARN = 3,
+               OSDN_ROPE_WAVELENGTH = 4 } osdn_rope_scaling;
+
+int osdn_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, int64_t original_length,
+                    double low_turns, double high_turns, double *freqs, double *amplitude);
 
 /* Waits for the work queued on cuda_stream, then reports whether any bounded
  * device-side wait of the library's kernels gave up since the last call

@@ -8,6 +8,11 @@ wrappers that allocate outputs and workspace with PyTorch:
     grads = backward(q, k, v, beta, dout, r=None, d0=None, S0=None, eta=1e-2)
     o = step(q, k, v, beta, S, d, r=None, eta=1e-2)      # S, d updated in place
 
+Next to them stand what a layer needs around them: the gated linear recurrence
+(``recurrence``, ``recurrence_backward``, ``recurrence_step``), the norms of queries and
+keys with the position rotation (``qk_norm``, ``qk_norm_backward``) and the rotation
+alone (``rope``, ``rope_frequencies``).
+
 All tensors must be CUDA tensors; there is no CPU path.
 """
 from __future__ import annotations
@@ -20,14 +25,23 @@ from ._binding import (OSDN_BF16, OSDN_ERR_CUDA, OSDN_ERR_INVALID_ARG, OSDN_ERR_
                        osdn_fwd_workspace_size, osdn_fwd_segments, osdn_fwd_launches, osdn_params, osdn_set_wait_limit_ns, osdn_step, osdn_step_ex,
                        osdn_fwd_gated, osdn_fwd_chunk_gated, osdn_step_gated,
                        osdn_bwd, osdn_bwd_gated, osdn_bwd_workspace_size, osdn_sync_status,
-                       osdn_fwd_host, osdn_fwd_host_buffer_size)
+                       osdn_fwd_host, osdn_fwd_host_buffer_size,
+                       osdn_recur_params, osdn_recur_fwd, osdn_recur_bwd, osdn_recur_bwd_workspace_size,
+                       osdn_recur_step, osdn_qk_params, osdn_qk_fwd, osdn_qk_bwd, osdn_qk_bwd_workspace_size,
+                       osdn_rope, osdn_rope_freqs)
+from ._layer import (qk_norm, qk_norm_backward, recurrence, recurrence_backward, recurrence_step, rope,
+                     rope_frequencies)
 
 __all__ = ["forward", "backward", "step", "osdn_bwd", "osdn_bwd_gated", "osdn_bwd_workspace_size", "residual_ratio", "osdn_fwd_scan_diag", "osdn_fwd", "osdn_fwd_scan", "osdn_fwd_chunk", "osdn_step", "osdn_fwd_workspace_size", "osdn_fwd_segments", "osdn_fwd_launches", "osdn_sync_status",
            "osdn_set_wait_limit_ns", "osdn_step_ex",
            "osdn_fwd_gated", "osdn_fwd_chunk_gated", "osdn_step_gated", "osdn_fwd_host", "osdn_fwd_host_buffer_size",
            "forward_host", "osdn_params", "make_params", "get_last_error", "OsdnError", "build", "LIB_PATH",
            "OSDN_OK", "OSDN_ERR_INVALID_ARG", "OSDN_ERR_UNSUPPORTED", "OSDN_ERR_CUDA", "OSDN_ERR_TIMEOUT",
-           "OSDN_BF16", "OSDN_FP32"]
+           "OSDN_BF16", "OSDN_FP32",
+           "recurrence", "recurrence_backward", "recurrence_step", "qk_norm", "qk_norm_backward", "rope",
+           "rope_frequencies", "osdn_recur_params", "osdn_recur_fwd", "osdn_recur_bwd",
+           "osdn_recur_bwd_workspace_size", "osdn_recur_step", "osdn_qk_params", "osdn_qk_fwd", "osdn_qk_bwd",
+           "osdn_qk_bwd_workspace_size", "osdn_rope", "osdn_rope_freqs"]
 
 
 def forward(q, k, v, beta, r=None, d0=None, S0=None, eta=1e-2, chunk=64, workspace=None, stream=None,

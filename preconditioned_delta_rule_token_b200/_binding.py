@@ -22,6 +22,12 @@ LIB_PATH = os.path.join(_PKG, "libosdn.so")
 OSDN_OK, OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA, OSDN_ERR_TIMEOUT = range(5)
 OSDN_BF16, OSDN_FP32 = 0, 1
 OSDN_NOALLOC_SCRATCH_BYTES = 32 << 20
+OSDN_RECUR_CHECKPOINT = 64
+GATE_FORMS = {"decay": 0, "log": 1, "logit": 2}
+INPUT_SCALES = {"none": 0, "complement": 1, "norm": 2}
+NORMS = {"none": 0, "l2": 1, "rms": 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "-cudart", "static", "--expt-relaxed-constexpr"]
@@ -33,6 +39,23 @@ class osdn_params(ctypes.Structure):
                 ("chunk", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eta", ctypes.c_float),
                 ("apf_anchor", ctypes.c_int32), ("stride_q", ctypes.c_int64 * 3), ("stride_k", ctypes.c_int64 * 3),
                 ("stride_v", ctypes.c_int64 * 3), ("stride_o", ctypes.c_int64 * 3)]
+
+
+class osdn_recur_params(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("B", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32),
+                ("gate_form", ctypes.c_int32), ("input_scale", ctypes.c_int32), ("stride_x", ctypes.c_int64 * 2),
+                ("stride_gate", ctypes.c_int64 * 2), ("stride_h", ctypes.c_int64 * 2)]
+
+
+class osdn_qk_params(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("B", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("layout", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("amplitude", ctypes.c_float), ("scale_q", ctypes.c_float),
+                ("scale_k", ctypes.c_float), ("pos0", ctypes.c_int64), ("stride_q", ctypes.c_int64 * 3),
+                ("stride_k", ctypes.c_int64 * 3), ("stride_out_q", ctypes.c_int64 * 3),
+                ("stride_out_k", ctypes.c_int64 * 3)]
 
 
 class OsdnError(RuntimeError):
@@ -115,6 +138,17 @@ def lib():
         L.osdn_bwd.restype = ctypes.c_int
         L.osdn_bwd_gated.argtypes = [P] + [vp] * 20 + [sz, vp]
         L.osdn_bwd_gated.restype = ctypes.c_int
+        R, Q = ctypes.POINTER(osdn_recur_params), ctypes.POINTER(osdn_qk_params)
+        psz, dbl, pdbl = ctypes.POINTER(sz), ctypes.c_double, ctypes.POINTER(ctypes.c_double)
+        for name, args in (("osdn_recur_fwd", [R] + [vp] * 8), ("osdn_recur_bwd_workspace_size", [R, psz]),
+                           ("osdn_recur_bwd", [R] + [vp] * 11 + [sz, vp]), ("osdn_recur_step", [R] + [vp] * 5),
+                           ("osdn_qk_fwd", [Q] + [vp] * 10), ("osdn_qk_bwd_workspace_size", [Q, psz]),
+                           ("osdn_qk_bwd", [Q] + [vp] * 14 + [sz, vp]),
+                           ("osdn_rope", [Q] + [vp] * 5 + [ctypes.c_int, vp]),
+                           ("osdn_rope_freqs", [ctypes.c_int32, dbl, ctypes.c_int32, dbl, ctypes.c_int64, dbl, dbl,
+                                                pdbl, pdbl])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = ctypes.c_int
         L.osdn_sync_status.argtypes = [vp]
         L.osdn_sync_status.restype = ctypes.c_int
         L.osdn_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
@@ -331,6 +365,72 @@ def osdn_bwd_gated(params, q, k, v, beta, r, alpha, d0, S0, dout, dS_final, dd_f
                                 _ptr(d0), _ptr(S0), _ptr(dout), _ptr(dS_final), _ptr(dd_final), _ptr(dq), _ptr(dk),
                                 _ptr(dv), _ptr(dbeta), _ptr(dr), _ptr(dalpha), _ptr(dd0), _ptr(dS0), _ptr(workspace),
                                 ctypes.c_size_t(_ws_bytes(workspace)), _stream(stream)))
+
+
+def _address(t):
+    """Device address of a tensor (None: NULL); its layout is in the parameter block."""
+    return None if t is None else t.data_ptr()
+
+
+def osdn_recur_fwd(params, x, gate, h0, lengths, h, final_h, checkpoints, stream=None):
+    """Raw C-ABI call of the gated linear recurrence (every tensor preallocated; strides in params)."""
+    _check(lib().osdn_recur_fwd(params, _address(x), _address(gate), _address(h0), _address(lengths), _address(h),
+                                _address(final_h), _address(checkpoints), _stream(stream)))
+
+
+def osdn_recur_bwd_workspace_size(params: osdn_recur_params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().osdn_recur_bwd_workspace_size(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def osdn_recur_bwd(params, x, gate, h0, lengths, dh, dfinal_h, checkpoints, dx, dgate, dh0, workspace, stream=None):
+    """Raw C-ABI call of the recurrence's backward."""
+    _check(lib().osdn_recur_bwd(params, _address(x), _address(gate), _address(h0), _address(lengths), _address(dh),
+                                _address(dfinal_h), _address(checkpoints), _address(dx), _address(dgate),
+                                _address(dh0), _address(workspace), _ws_bytes(workspace), _stream(stream)))
+
+
+def osdn_recur_step(params, x, gate, state, h, stream=None):
+    """Raw C-ABI call: one token of the recurrence, state updated in place."""
+    _check(lib().osdn_recur_step(params, _address(x), _address(gate), _address(state), _address(h), _stream(stream)))
+
+
+def osdn_qk_fwd(params, q, k, wq, wk, positions, freqs, lengths, q_out, k_out, stream=None):
+    """Raw C-ABI call of the query and key norms with the rotation (strides in params)."""
+    _check(lib().osdn_qk_fwd(params, _address(q), _address(k), _address(wq), _address(wk), _address(positions),
+                             _address(freqs), _address(lengths), _address(q_out), _address(k_out), _stream(stream)))
+
+
+def osdn_qk_bwd_workspace_size(params: osdn_qk_params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().osdn_qk_bwd_workspace_size(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def osdn_qk_bwd(params, q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
+                stream=None):
+    """Raw C-ABI call of the backward of osdn_qk_fwd."""
+    _check(lib().osdn_qk_bwd(params, _address(q), _address(k), _address(wq), _address(wk), _address(positions),
+                             _address(freqs), _address(lengths), _address(dq_out), _address(dk_out), _address(dq),
+                             _address(dk), _address(dwq), _address(dwk), _address(workspace), _ws_bytes(workspace),
+                             _stream(stream)))
+
+
+def osdn_rope(params, x, positions, freqs, lengths, out, inverse=False, stream=None):
+    """Raw C-ABI call of the rotation alone."""
+    _check(lib().osdn_rope(params, _address(x), _address(positions), _address(freqs), _address(lengths),
+                           _address(out), 1 if inverse else 0, _stream(stream)))
+
+
+def osdn_rope_freqs(rot_dim, base, scaling, factor, original_length, low_turns, high_turns):
+    """The rotation's frequencies (a list of rot_dim / 2 floats, computed on the host) and the amplitude."""
+    if rot_dim < 2 or rot_dim > 256:
+        raise OsdnError(OSDN_ERR_INVALID_ARG, "rot_dim must be even, 2 .. 256 (got %d)" % rot_dim)
+    out, amplitude = (ctypes.c_double * (rot_dim // 2))(), ctypes.c_double(0.0)
+    _check(lib().osdn_rope_freqs(rot_dim, base, scaling, factor, original_length, low_turns, high_turns, out,
+                                 ctypes.byref(amplitude)))
+    return list(out), amplitude.value
 
 
 def osdn_sync_status(stream=None) -> int:

@@ -1,0 +1,286 @@
+"""What a layer needs next to the delta rule: the gated linear recurrence, the norms of
+queries and keys with the position rotation, and the rotation alone.
+
+Wrappers that check shapes, types and devices, allocate the outputs and call the C ABI.
+`stream` is a torch.cuda.Stream of the tensors' device (default: that device's current
+stream); outputs and workspaces are allocated on it. All tensors must be on one CUDA
+device; there is no CPU path.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from functools import lru_cache
+
+import torch
+
+from . import _binding as B
+from ._binding import OSDN_BF16, OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_FP32, OsdnError
+
+_DTYPES = {torch.bfloat16: OSDN_BF16, torch.float32: OSDN_FP32}
+_HERE = contextlib.nullcontext()
+
+
+def _bad(msg, code=OSDN_ERR_INVALID_ARG):
+    raise OsdnError(code, msg)
+
+
+def _scope(dev, stream):
+    """Makes `stream` (None: the current one) of device `dev` current for allocations and the launch."""
+    if stream is not None:
+        if stream.device != dev:
+            _bad("the stream is of %s, the tensors are on %s" % (stream.device, dev))
+        return torch.cuda.stream(stream)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _choice(name, value, table):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        _bad("%s is one of %s (got %r)" % (name, ", ".join(table), value))
+
+
+def _dtype(name, t):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        _bad("%s must be bfloat16 or float32 (got %s)" % (name, t.dtype), OSDN_ERR_UNSUPPORTED)
+    return code
+
+
+def _held(dev, name, t, shape, dtype, dense=True):
+    """Checks one tensor: on `dev`, of this shape and type, dense where asked."""
+    if t is None:
+        return
+    if t.device != dev or not t.is_cuda:
+        _bad("%s is on %s, not on %s (the library has no CPU path)" % (name, t.device, dev))
+    if t.shape != shape:
+        _bad("%s must be %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        _bad("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if dense and not t.is_contiguous():
+        _bad("%s is not contiguous" % name)
+
+
+def _strides(name, t, n):
+    """The first n strides of a token tensor whose last dimension is contiguous (zeros: dense)."""
+    if t is None or t.is_contiguous():
+        return (0,) * n
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] != 1:
+        _bad("the last dimension of %s must be contiguous" % name)
+    if not any(st[:n]):
+        _bad("%s has strides of 0 in every dimension: expand it into memory" % name)
+    return st[:n]
+
+
+@lru_cache(maxsize=256)
+def _recur_params(nB, T, D, dtype, gate_dtype, gate_form, input_scale, sx, sg, sh):
+    p = B.osdn_recur_params()
+    p.struct_size = ctypes.sizeof(p)
+    p.B, p.T, p.D, p.dtype, p.gate_dtype, p.gate_form, p.input_scale = nB, T, D, dtype, gate_dtype, gate_form, input_scale
+    p.stride_x[:], p.stride_gate[:], p.stride_h[:] = sx, sg, sh
+    return p
+
+
+def _recur_inputs(x, gate, gate_form, input_scale, h0, lengths, h, h_name):
+    if x.dim() != 3:
+        _bad("x is [B, T, D] (got %s)" % (tuple(x.shape),))
+    nB, T, D = x.shape
+    if not x.is_cuda:
+        _bad("x is on %s (the library has no CPU path)" % x.device)
+    dev = x.device
+    code, gcode = _dtype("x", x), _dtype("gate", gate)
+    _held(dev, "gate", gate, x.shape, gate.dtype, dense=False)
+    _held(dev, "h0", h0, (nB, D), torch.float32)
+    _held(dev, "lengths", lengths, (nB,), torch.int32)
+    _held(dev, h_name, h, x.shape, x.dtype, dense=False)
+    p = _recur_params(nB, T, D, code, gcode, _choice("gate_form", gate_form, B.GATE_FORMS),
+                      _choice("input_scale", input_scale, B.INPUT_SCALES), _strides("x", x, 2),
+                      _strides("gate", gate, 2), _strides(h_name, h, 2))
+    return p, dev, nB, T, D
+
+
+def recurrence(x, gate, h0=None, lengths=None, gate_form="decay", input_scale="none", checkpoints=False, h=None,
+               stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + s_t x_t of every channel.
+
+    x, gate [B,T,D] (x bf16 or fp32; gate of x's type or fp32; the channels contiguous, e.g. column
+    slices of one projection). gate_form: a = gate ("decay"), exp(gate) ("log") or sigmoid(gate) ("logit");
+    a = 0 starts a new document. input_scale: s = 1 ("none"), 1 - a ("complement") or sqrt(1 - a^2) ("norm").
+    h0 [B,D] fp32 or None (zeros). lengths [B] int32 (None: T each): tokens from a sequence's length
+    on are not read; their rows of h are zeros (left as they were when `h` is given).
+    Returns (h [B,T,D] in x's type, final_h [B,D] fp32), and with checkpoints=True the states
+    [B,ceil(T/64),D] fp32 that recurrence_backward takes."""
+    p, dev, nB, T, D = _recur_inputs(x, gate, gate_form, input_scale, h0, lengths, h, "h")
+    with _scope(dev, stream):
+        if h is None:
+            h = (torch.empty if lengths is None else torch.zeros)((nB, T, D), dtype=x.dtype, device=dev)
+        final_h = torch.empty((nB, D), dtype=torch.float32, device=dev)
+        marks = None
+        if checkpoints:
+            marks = torch.empty((nB, (T + B.OSDN_RECUR_CHECKPOINT - 1) // B.OSDN_RECUR_CHECKPOINT, D),
+                                dtype=torch.float32, device=dev)
+        B.osdn_recur_fwd(p, x, gate, h0, lengths, h, final_h, marks)
+    return (h, final_h, marks) if checkpoints else (h, final_h)
+
+
+def recurrence_backward(x, gate, dh, h0=None, dfinal_h=None, lengths=None, checkpoints=None, gate_form="decay",
+                        input_scale="none", workspace=None, stream=None):
+    """Gradients of L = sum(dh * h) + sum(dfinal_h * final_h) for the recurrence() of the same inputs.
+
+    dh [B,T,D] in x's type; dfinal_h [B,D] fp32 or None (= 0). checkpoints: the states that
+    recurrence(..., checkpoints=True) returned for the same inputs; None runs the forward again for them.
+    Returns a dict with dx (x's type), dgate (the gate's type; with respect to the gate as given) and
+    dh0 [B,D] fp32. Rows from a sequence's length on are zeros."""
+    p, dev, nB, T, D = _recur_inputs(x, gate, gate_form, input_scale, h0, lengths, dh, "dh")
+    _held(dev, "dfinal_h", dfinal_h, (nB, D), torch.float32)
+    _held(dev, "checkpoints", checkpoints,
+          (nB, (T + B.OSDN_RECUR_CHECKPOINT - 1) // B.OSDN_RECUR_CHECKPOINT, D), torch.float32)
+    with _scope(dev, stream):
+        new = torch.empty if lengths is None else torch.zeros
+        g = {"dx": new((nB, T, D), dtype=x.dtype, device=dev), "dgate": new((nB, T, D), dtype=gate.dtype, device=dev),
+             "dh0": torch.empty((nB, D), dtype=torch.float32, device=dev)}
+        if checkpoints is None and workspace is None:
+            workspace = torch.empty(B.osdn_recur_bwd_workspace_size(p), dtype=torch.uint8, device=dev)
+        B.osdn_recur_bwd(p, x, gate, h0, lengths, dh, dfinal_h, checkpoints, g["dx"], g["dgate"], g["dh0"], workspace)
+    return g
+
+
+def recurrence_step(x, gate, state, gate_form="decay", input_scale="none", out=None, stream=None):
+    """One decode token of the recurrence: x, gate [B,D]; state [B,D] fp32, updated in place.
+    Returns the new state in x's type [B,D] (`out` if given)."""
+    if x.dim() != 2:
+        _bad("x is [B, D] (got %s)" % (tuple(x.shape),))
+    if not x.is_cuda:
+        _bad("x is on %s (the library has no CPU path)" % x.device)
+    (nB, D), dev = x.shape, x.device
+    code, gcode = _dtype("x", x), _dtype("gate", gate)
+    _held(dev, "gate", gate, x.shape, gate.dtype, dense=False)
+    _held(dev, "state", state, x.shape, torch.float32)
+    _held(dev, "out", out, x.shape, x.dtype, dense=False)
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((nB, D), dtype=x.dtype, device=dev)
+        p = _recur_params(nB, 1, D, code, gcode, _choice("gate_form", gate_form, B.GATE_FORMS),
+                          _choice("input_scale", input_scale, B.INPUT_SCALES), _strides("x", x, 1) + (0,),
+                          _strides("gate", gate, 1) + (0,), _strides("out", out, 1) + (0,))
+        B.osdn_recur_step(p, x, gate, state, out)
+    return out
+
+
+@lru_cache(maxsize=256)
+def _qk_params(nB, T, Hq, Hk, width, dtype, norm, layout, rot, eps, amplitude, scale_q, scale_k, pos0, sq, sk, soq, sok):
+    p = B.osdn_qk_params()
+    p.struct_size = ctypes.sizeof(p)
+    p.B, p.T, p.Hq, p.Hk, p.width, p.dtype, p.norm, p.layout, p.rot_dim = nB, T, Hq, Hk, width, dtype, norm, layout, rot
+    p.eps, p.amplitude, p.scale_q, p.scale_k, p.pos0 = eps, amplitude, scale_q, scale_k, pos0
+    p.stride_q[:], p.stride_k[:], p.stride_out_q[:], p.stride_out_k[:] = sq, sk, soq, sok
+    return p
+
+
+def _heads_inputs(q, k, freqs, positions, lengths, norm, layout, wq, wk, out_q, out_k, eps, amplitude, scale_q, scale_k,
+                  pos0, names):
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        _bad("%s are [B, T, H, width]" % " and ".join(names[:2]))
+    if not q.is_cuda:
+        _bad("%s is on %s (the library has no CPU path)" % (names[0], q.device))
+    (nB, T, Hq, width), dev = q.shape, q.device
+    Hk = 0 if k is None else k.shape[2]
+    code = _dtype(names[0], q)
+    if k is not None:
+        _held(dev, names[1], k, (nB, T, Hk, width), q.dtype, dense=False)
+    _held(dev, "positions", positions, (nB, T), torch.int64)
+    _held(dev, "lengths", lengths, (nB,), torch.int32)
+    _held(dev, "wq", wq, (width,), torch.float32)
+    _held(dev, "wk", wk, (width,), torch.float32)
+    rot = 0
+    if freqs is not None:
+        _held(dev, "freqs", freqs, (freqs.numel(),), torch.float64)
+        rot = 2 * freqs.numel()
+    _held(dev, names[2], out_q, q.shape, q.dtype, dense=False)
+    if k is not None:
+        _held(dev, names[3], out_k, k.shape, q.dtype, dense=False)
+    p = _qk_params(nB, T, Hq, Hk, width, code, _choice("norm", norm, B.NORMS),
+                   _choice("layout", layout, B.ROPE_LAYOUTS), rot, eps, amplitude, scale_q, scale_k, pos0,
+                   _strides(names[0], q, 3), _strides(names[1], k, 3), _strides(names[2], out_q, 3),
+                   _strides(names[3], out_k, 3))
+    return p, dev
+
+
+def qk_norm(q, k, freqs=None, positions=None, norm="l2", eps=1e-6, wq=None, wk=None, layout="half", amplitude=1.0,
+            scale_q=1.0, scale_k=1.0, pos0=0, lengths=None, q_out=None, k_out=None, stream=None):
+    """Norm of every query and key head, then the position rotation, in one pass.
+
+    q [B,T,Hq,width], k [B,T,Hk,width] or None (bf16 or fp32; column slices of a fused projection are
+    read in place). norm: "l2" (x / sqrt(sum x^2 + eps), as the delta rule wants its keys), "rms"
+    (x / sqrt(mean x^2 + eps)) or "none"; wq, wk [width] fp32 multiply after it, scale_q and scale_k too.
+    freqs [rot/2] fp64 (rope_frequencies; None: no rotation) turns the first rot features: pairs
+    (i, i + rot/2) for layout "half" (rot a multiple of 16), (2i, 2i+1) for "interleaved". positions
+    [B,T] int64 (None: pos0 + t). lengths [B] int32: tokens from a sequence's length on give zeros
+    (rows of a given q_out, k_out stay as they were). q_out may be q, k_out may be k.
+    Returns (q_out, k_out)."""
+    p, dev = _heads_inputs(q, k, freqs, positions, lengths, norm, layout, wq, wk, q_out, k_out, float(eps),
+                           float(amplitude), float(scale_q), float(scale_k), int(pos0), ("q", "k", "q_out", "k_out"))
+    with _scope(dev, stream):
+        new = torch.empty if lengths is None else torch.zeros
+        if q_out is None:
+            q_out = new(q.shape, dtype=q.dtype, device=dev)
+        if k is not None and k_out is None:
+            k_out = new(k.shape, dtype=k.dtype, device=dev)
+        B.osdn_qk_fwd(p, q, k, wq, wk, positions, freqs, lengths, q_out, k_out)
+    return q_out, k_out
+
+
+def qk_norm_backward(q, k, dq_out, dk_out, freqs=None, positions=None, norm="l2", eps=1e-6, wq=None, wk=None,
+                     layout="half", amplitude=1.0, scale_q=1.0, scale_k=1.0, pos0=0, lengths=None, workspace=None,
+                     stream=None):
+    """Gradients of L = sum(dq_out * q_out) + sum(dk_out * k_out) for the qk_norm() of the same inputs.
+    Returns a dict with dq, dk (the inputs' type; zeros from a sequence's length on) and dwq, dwk
+    [width] fp32 (None without the weight)."""
+    if (k is None) != (dk_out is None):
+        _bad("k and dk_out go together")
+    p, dev = _heads_inputs(q, k, freqs, positions, lengths, norm, layout, wq, wk, dq_out, dk_out, float(eps),
+                           float(amplitude), float(scale_q), float(scale_k), int(pos0), ("q", "k", "dq_out", "dk_out"))
+    with _scope(dev, stream):
+        new = torch.empty if lengths is None else torch.zeros
+        g = {"dq": new(q.shape, dtype=q.dtype, device=dev),
+             "dk": None if k is None else new(k.shape, dtype=k.dtype, device=dev),
+             "dwq": None if wq is None else torch.empty_like(wq),
+             "dwk": None if wk is None or k is None else torch.empty_like(wk)}
+        if workspace is None and (g["dwq"] is not None or g["dwk"] is not None):
+            workspace = torch.empty(B.osdn_qk_bwd_workspace_size(p), dtype=torch.uint8, device=dev)
+        B.osdn_qk_bwd(p, q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, g["dq"], g["dk"], g["dwq"],
+                      g["dwk"], workspace)
+    return g
+
+
+def rope(x, freqs, positions=None, layout="half", amplitude=1.0, scale=1.0, pos0=0, inverse=False, lengths=None,
+         out=None, stream=None):
+    """The position rotation alone on x [B,T,H,width]: see qk_norm for freqs, positions, layout and lengths.
+    inverse=True turns back with the same amplitude: it takes the gradient of the result to that of x.
+    `out` may be x. Returns the rotated tensor."""
+    if freqs is None:
+        _bad("freqs is needed")
+    p, dev = _heads_inputs(x, None, freqs, positions, lengths, "none", layout, None, None, out, None, 0.0,
+                           float(amplitude), float(scale), 1.0, int(pos0), ("x", "k", "out", "k_out"))
+    with _scope(dev, stream):
+        if out is None:
+            out = (torch.empty if lengths is None else torch.zeros)(x.shape, dtype=x.dtype, device=dev)
+        B.osdn_rope(p, x, positions, freqs, lengths, out, inverse)
+    return out
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=0, low_turns=1.0,
+                     high_turns=None, device="cuda"):
+    """Frequencies of the rotation of rot_dim features as a fp64 tensor [rot_dim/2], and its amplitude.
+
+    scaling, for contexts `factor` times longer than original_length: "none"; "linear" (all divided by
+    factor); "ntk" (a larger base); "yarn" (pairs with more than high_turns turns over original_length
+    kept, fewer than low_turns divided, a ramp over the pairs between; amplitude 0.1 ln(factor) + 1);
+    "wavelength" (the ramp over the number of turns). high_turns defaults to 32 ("yarn") or 4."""
+    if high_turns is None:
+        high_turns = 32.0 if scaling == "yarn" else 4.0
+    f, amplitude = B.osdn_rope_freqs(int(rot_dim), float(base), _choice("scaling", scaling, B.ROPE_SCALINGS),
+                                     float(factor), int(original_length), float(low_turns), float(high_turns))
+    return torch.tensor(f, dtype=torch.float64, device=device), amplitude

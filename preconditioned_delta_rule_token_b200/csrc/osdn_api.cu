@@ -5,7 +5,9 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstddef>
 #include <cstdarg>
 #include <cstdio>
@@ -20,6 +22,8 @@
 #include "bwd.cuh"
 #include "chunk_ffma.cuh"
 #include "chunk_wy.cuh"
+#include "heads.cuh"
+#include "recurrence.cuh"
 #include "scan_ws.cuh"
 #include "scan_seq.cuh"
 #include "segments.cuh"
@@ -1399,6 +1403,488 @@ int osdn_fwd_host(const osdn_params* p, const void* q, const void* k, const void
     } while (false);
     for (int i = 0; i < nev; ++i) cudaEventDestroy(ev[i]);
     return rc;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------- gated linear recurrence
+namespace {
+
+// True when the rows (of `width` contiguous elements) that these extents and strides address do not
+// overlap: taken in the order of their strides, each dimension steps over all that the smaller ones span.
+template <int N> bool rows_apart(const int64_t (&extent)[N], const int64_t (&stride)[N], int64_t width) {
+    int order[N];
+    for (int i = 0; i < N; ++i) order[i] = i;
+    std::sort(order, order + N, [&](int a, int b) { return stride[a] < stride[b]; });
+    __int128 span = width;   // an extent times a stride may pass 64 bits
+    for (int i : order) {
+        if (extent[i] <= 1) continue;
+        if (stride[i] < span) return false;
+        span += (__int128)stride[i] * (extent[i] - 1);
+    }
+    return true;
+}
+
+struct Str2 {
+    int64_t b, t;
+};
+Str2 recur_strides(const osdn_recur_params* p, const int64_t (&s)[2]) {
+    if (!(s[0] | s[1])) return {(int64_t)p->T * p->D, (int64_t)p->D};
+    return {s[0], s[1]};
+}
+
+int check_recur(const osdn_recur_params* p, bool step) {
+    if (!p) return fail(OSDN_ERR_INVALID_ARG, "params is NULL");
+    if (p->struct_size != sizeof(osdn_recur_params))
+        return fail(OSDN_ERR_INVALID_ARG, "params.struct_size is %u, expected %zu", p->struct_size,
+                    sizeof(osdn_recur_params));
+    if (p->B < 1) return fail(OSDN_ERR_INVALID_ARG, "B must be >= 1 (got %d)", p->B);
+    if (p->D < 1 || p->D > (1 << 24)) return fail(OSDN_ERR_INVALID_ARG, "D must be 1 .. 2^24 (got %d)", p->D);
+    if (!step && (p->T < 0 || p->T > (1 << 30)))
+        return fail(OSDN_ERR_INVALID_ARG, "T must be 0 .. 2^30 (got %d)", p->T);
+    if (p->dtype != OSDN_BF16 && p->dtype != OSDN_FP32)
+        return fail(OSDN_ERR_INVALID_ARG, "unknown dtype %d", p->dtype);
+    if (p->gate_dtype != OSDN_BF16 && p->gate_dtype != OSDN_FP32)
+        return fail(OSDN_ERR_INVALID_ARG, "unknown gate_dtype %d", p->gate_dtype);
+    if (p->gate_dtype != p->dtype && p->gate_dtype != OSDN_FP32)
+        return fail(OSDN_ERR_UNSUPPORTED, "gate_dtype must be dtype or fp32");
+    if (p->gate_form < OSDN_GATE_DECAY || p->gate_form > OSDN_GATE_LOGIT)
+        return fail(OSDN_ERR_INVALID_ARG, "unknown gate_form %d", p->gate_form);
+    if (p->input_scale < OSDN_INPUT_NONE || p->input_scale > OSDN_INPUT_NORM)
+        return fail(OSDN_ERR_INVALID_ARG, "unknown input_scale %d", p->input_scale);
+    for (const int64_t* st : {p->stride_x, p->stride_gate, p->stride_h})
+        for (int i = 0; i < 2; ++i)
+            if (st[i] < 0 || st[i] > ((int64_t)1 << 38))
+                return fail(OSDN_ERR_INVALID_ARG, "strides must be 0 .. 2^38 (got %lld)", (long long)st[i]);
+    if ((double)p->B * (step ? 1 : p->T) * p->D > 9.0e18)
+        return fail(OSDN_ERR_INVALID_ARG, "tensor sizes overflow 64-bit indexing");
+    if ((double)p->B * ((p->D + 31) / 32) * 16 > 2147483647.0)
+        return fail(OSDN_ERR_INVALID_ARG, "B * D exceeds the grid limit");
+    return OSDN_OK;
+}
+
+int check_h_rows(const osdn_recur_params* p, bool step) {
+    const Str2 s = recur_strides(p, p->stride_h);
+    if (!rows_apart<2>({p->B, step ? 1 : p->T}, {s.b, s.t}, p->D))
+        return fail(OSDN_ERR_INVALID_ARG, "stride_h makes rows of h overlap");
+    return OSDN_OK;
+}
+
+osdn::recur::Args recur_args(const osdn_recur_params* p) {
+    osdn::recur::Args a{};
+    a.B = p->B; a.T = p->T; a.D = p->D; a.form = p->gate_form; a.scale = p->input_scale;
+    const Str2 x = recur_strides(p, p->stride_x), g = recur_strides(p, p->stride_gate),
+               h = recur_strides(p, p->stride_h);
+    a.xb = x.b; a.xt = x.t; a.gb = g.b; a.gt = g.t; a.hb = h.b; a.ht = h.t;
+    return a;
+}
+
+// Channels a thread takes: the most, up to 4, at which every row of every tensor starts on a whole
+// vector. `each` lists the token tensors with their element size.
+struct TokenPtr {
+    const void* ptr;
+    size_t elem;
+};
+int recur_vec(const osdn_recur_params* p, const osdn::recur::Args& a, std::initializer_list<TokenPtr> each) {
+    for (int v = 4; v > 1; v /= 2) {
+        bool ok = p->D % v == 0 && !((a.xb | a.xt | a.gb | a.gt | a.hb | a.ht) % v);
+        for (const TokenPtr& t : each) ok = ok && reinterpret_cast<uintptr_t>(t.ptr) % (v * t.elem) == 0;
+        if (ok) return v;
+    }
+    return 1;
+}
+
+// f(V, Tx, Tg) for the vector width and the types as constants.
+template <typename F> int recur_dispatch(const osdn_recur_params* p, int vec, F&& f) {
+    using bf = __nv_bfloat16;
+    auto types = [&](auto v) {
+        if (p->dtype == OSDN_FP32) return f(v, float{}, float{});
+        if (p->gate_dtype == OSDN_FP32) return f(v, bf{}, float{});
+        return f(v, bf{}, bf{});
+    };
+    if (vec == 4) return types(std::integral_constant<int, 4>{});
+    if (vec == 2) return types(std::integral_constant<int, 2>{});
+    return types(std::integral_constant<int, 1>{});
+}
+
+bool element_aligned(const void* p, size_t elem) { return reinterpret_cast<uintptr_t>(p) % elem == 0; }
+
+int launch_recur_fwd(const osdn_recur_params* p, osdn::recur::Args a, cudaStream_t st) {
+    const size_t ex = elem_size(p->dtype), eg = elem_size(p->gate_dtype);
+    return recur_dispatch(p, recur_vec(p, a, {{a.x, ex}, {a.gate, eg}, {a.h, ex}}), [&](auto v, auto tx, auto tg) {
+        a.cblocks = (p->D + 32 * v - 1) / (32 * v);
+        osdn::recur::fwd_kernel<v, decltype(tx), decltype(tg)>
+            <<<(unsigned)p->B * a.cblocks, osdn::recur::kThreads, 0, st>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "recurrence launch");
+    });
+}
+
+size_t recur_ckpt_bytes(const osdn_recur_params* p) {
+    const size_t tiles = ((size_t)p->T + OSDN_RECUR_CHECKPOINT - 1) / OSDN_RECUR_CHECKPOINT;
+    return (size_t)p->B * tiles * p->D * sizeof(float);
+}
+
+static_assert(osdn::recur::kTile == OSDN_RECUR_CHECKPOINT, "a saved state before each tile");
+
+}  // namespace
+
+extern "C" {
+
+int osdn_recur_fwd(const osdn_recur_params* p, const void* x, const void* gate, const float* h0,
+                   const int32_t* lengths, void* h, float* final_h, float* checkpoints, void* cuda_stream) {
+    t_last_error.clear();
+    int rc = check_recur(p, false);
+    if (rc) return rc;
+    if (p->T > 0 && (!x || !gate)) return fail(OSDN_ERR_INVALID_ARG, "a required pointer (x, gate) is NULL");
+    if (h && (rc = check_h_rows(p, false))) return rc;
+    if (!element_aligned(x, elem_size(p->dtype)) || !element_aligned(h, elem_size(p->dtype)) ||
+        !element_aligned(gate, elem_size(p->gate_dtype)) || !element_aligned(lengths, 4))
+        return fail(OSDN_ERR_INVALID_ARG, "x, gate, h and lengths must be aligned to their elements");
+    if (!aligned16(h0) || !aligned16(final_h) || !aligned16(checkpoints))
+        return fail(OSDN_ERR_INVALID_ARG, "h0, final_h and checkpoints must be 16-byte aligned");
+    if (h && (h == x || h == gate)) return fail(OSDN_ERR_INVALID_ARG, "h must not be x or gate");
+    osdn::recur::Args a = recur_args(p);
+    a.x = x; a.gate = gate; a.h0 = h0; a.lengths = lengths; a.h = h; a.final_h = final_h; a.ckpt = checkpoints;
+    return launch_recur_fwd(p, a, reinterpret_cast<cudaStream_t>(cuda_stream));
+}
+
+int osdn_recur_bwd_workspace_size(const osdn_recur_params* p, size_t* bytes) {
+    t_last_error.clear();
+    int rc = check_recur(p, false);
+    if (rc) return rc;
+    if (!bytes) return fail(OSDN_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = round_up(recur_ckpt_bytes(p), 256);
+    return OSDN_OK;
+}
+
+int osdn_recur_bwd(const osdn_recur_params* p, const void* x, const void* gate, const float* h0,
+                   const int32_t* lengths, const void* dh, const float* dfinal_h, const float* checkpoints,
+                   void* dx, void* dgate, float* dh0, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+    t_last_error.clear();
+    int rc = check_recur(p, false);
+    if (rc) return rc;
+    if (p->T > 0 && (!x || !gate || !dh || !dx || !dgate))
+        return fail(OSDN_ERR_INVALID_ARG, "a required pointer (x, gate, dh, dx, dgate) is NULL");
+    const size_t ex = elem_size(p->dtype), eg = elem_size(p->gate_dtype);
+    if (!element_aligned(x, ex) || !element_aligned(dh, ex) || !element_aligned(gate, eg) ||
+        !element_aligned(lengths, 4))
+        return fail(OSDN_ERR_INVALID_ARG, "x, gate, dh and lengths must be aligned to their elements");
+    for (const void* q : {(const void*)h0, (const void*)dfinal_h, (const void*)checkpoints, (const void*)dx,
+                          (const void*)dgate, (const void*)dh0, (const void*)workspace})
+        if (!aligned16(q))
+            return fail(OSDN_ERR_INVALID_ARG,
+                        "h0, dfinal_h, checkpoints, dx, dgate, dh0 and workspace must be 16-byte aligned");
+    for (const void* q : {x, gate, dh})
+        if (q && (dx == q || dgate == q)) return fail(OSDN_ERR_INVALID_ARG, "dx and dgate must not be an input");
+    if (p->T > 0 && dx == dgate) return fail(OSDN_ERR_INVALID_ARG, "dx and dgate are the same pointer");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    osdn::recur::Args a = recur_args(p);
+    a.x = x; a.gate = gate; a.h0 = h0; a.lengths = lengths;
+    if (!checkpoints && p->T > 0) {
+        const size_t need = recur_ckpt_bytes(p);
+        if (!workspace) return fail(OSDN_ERR_INVALID_ARG, "workspace is NULL and no checkpoints are given");
+        if (workspace_bytes < need)
+            return fail(OSDN_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+        a.ckpt = static_cast<float*>(workspace);
+        if ((rc = launch_recur_fwd(p, a, st))) return rc;
+        checkpoints = a.ckpt;
+        a.ckpt = nullptr;
+    }
+    a.dh = dh; a.dfinal = dfinal_h; a.ckpt_in = checkpoints; a.dx = dx; a.dgate = dgate; a.dh0 = dh0;
+    return recur_dispatch(p, recur_vec(p, a, {{x, ex}, {gate, eg}, {dh, ex}}), [&](auto v, auto tx, auto tg) {
+        a.cblocks = (p->D + 32 * v - 1) / (32 * v);
+        osdn::recur::bwd_kernel<v, decltype(tx), decltype(tg)>
+            <<<(unsigned)p->B * a.cblocks, osdn::recur::kThreads, 0, st>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "recurrence backward launch");
+    });
+}
+
+int osdn_recur_step(const osdn_recur_params* p, const void* x, const void* gate, float* state, void* h,
+                    void* cuda_stream) {
+    t_last_error.clear();
+    int rc = check_recur(p, true);
+    if (rc) return rc;
+    osdn_recur_params q = *p;
+    q.T = 1;
+    if (!x || !gate || !state || !h)
+        return fail(OSDN_ERR_INVALID_ARG, "a required pointer (x, gate, state, h) is NULL");
+    const size_t ex = elem_size(p->dtype), eg = elem_size(p->gate_dtype);
+    if (!element_aligned(x, ex) || !element_aligned(h, ex) || !element_aligned(gate, eg))
+        return fail(OSDN_ERR_INVALID_ARG, "x, gate and h must be aligned to their elements");
+    if (!aligned16(state)) return fail(OSDN_ERR_INVALID_ARG, "state must be 16-byte aligned");
+    if (h == x || h == gate || h == state) return fail(OSDN_ERR_INVALID_ARG, "h must not be x, gate or state");
+    if ((rc = check_h_rows(&q, true))) return rc;
+    osdn::recur::Args a = recur_args(&q);
+    a.xt = a.gt = a.ht = 0;   // one token: these strides are not used
+    a.x = x; a.gate = gate; a.h = h; a.final_h = state;
+    return recur_dispatch(&q, recur_vec(&q, a, {{x, ex}, {gate, eg}, {h, ex}}), [&](auto v, auto tx, auto tg) {
+        const int64_t n = (int64_t)q.B * (q.D / v), blocks = (n + 255) / 256;
+        osdn::recur::step_kernel<v, decltype(tx), decltype(tg)>
+            <<<(unsigned)std::min<int64_t>(blocks, 148 * 8), 256, 0,
+               reinterpret_cast<cudaStream_t>(cuda_stream)>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "recurrence step launch");
+    });
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------- norms of queries and keys, rotation
+namespace {
+
+osdn::Tok3 qk_strides(const osdn_qk_params* p, const int64_t (&s)[3], int H) {
+    if (all_zero(s)) return {(int64_t)p->T * H * p->width, (int64_t)H * p->width, (int64_t)p->width};
+    return {s[0], s[1], s[2]};
+}
+
+int check_qk(const osdn_qk_params* p) {
+    if (!p) return fail(OSDN_ERR_INVALID_ARG, "params is NULL");
+    if (p->struct_size != sizeof(osdn_qk_params))
+        return fail(OSDN_ERR_INVALID_ARG, "params.struct_size is %u, expected %zu", p->struct_size,
+                    sizeof(osdn_qk_params));
+    if (p->B < 1 || p->Hq < 1 || p->Hk < 0 || p->T < 0)
+        return fail(OSDN_ERR_INVALID_ARG, "B and Hq must be >= 1, T and Hk >= 0 (got %d, %d, %d, %d)", p->B, p->Hq,
+                    p->T, p->Hk);
+    if (p->Hq > (1 << 16) || p->Hk > (1 << 16)) return fail(OSDN_ERR_INVALID_ARG, "Hq and Hk must be at most 2^16");
+    if (p->width < 1) return fail(OSDN_ERR_INVALID_ARG, "width must be positive (got %d)", p->width);
+    if (p->width % 8 || p->width > osdn::heads::kMaxWidth)
+        return fail(OSDN_ERR_UNSUPPORTED, "width must be a multiple of 8 up to 256 (got %d)", p->width);
+    if (p->dtype != OSDN_BF16 && p->dtype != OSDN_FP32)
+        return fail(OSDN_ERR_INVALID_ARG, "unknown dtype %d", p->dtype);
+    if (p->norm < OSDN_NORM_NONE || p->norm > OSDN_NORM_RMS) return fail(OSDN_ERR_INVALID_ARG, "unknown norm %d", p->norm);
+    if (p->layout != OSDN_ROPE_HALF && p->layout != OSDN_ROPE_INTERLEAVED)
+        return fail(OSDN_ERR_INVALID_ARG, "unknown layout %d", p->layout);
+    if (p->rot_dim < 0 || p->rot_dim > p->width || p->rot_dim % 2)
+        return fail(OSDN_ERR_INVALID_ARG, "rot_dim must be even, 0 .. width (got %d)", p->rot_dim);
+    if (p->layout == OSDN_ROPE_HALF && p->rot_dim % 16)
+        return fail(OSDN_ERR_UNSUPPORTED, "the half layout takes rot_dim in multiples of 16 (got %d)", p->rot_dim);
+    if (!(p->eps >= 0.f)) return fail(OSDN_ERR_INVALID_ARG, "eps must be >= 0");
+    if (!(std::isfinite(p->amplitude) && std::isfinite(p->scale_q) && std::isfinite(p->scale_k)))
+        return fail(OSDN_ERR_INVALID_ARG, "amplitude, scale_q and scale_k must be finite");
+    for (const int64_t* st : {p->stride_q, p->stride_k, p->stride_out_q, p->stride_out_k})
+        for (int i = 0; i < 3; ++i)
+            if (st[i] < 0 || (st[i] & 7) || st[i] > ((int64_t)1 << 38))
+                return fail(OSDN_ERR_INVALID_ARG,
+                            "strides must be non-negative multiples of 8 elements below 2^38 (got %lld)",
+                            (long long)st[i]);
+    const double tokens = (double)p->B * p->T;
+    if (tokens * std::max(p->Hq, p->Hk) * p->width > 9.0e18)
+        return fail(OSDN_ERR_INVALID_ARG, "tensor sizes overflow 64-bit indexing");
+    if (tokens > 2147483647.0) return fail(OSDN_ERR_INVALID_ARG, "B * T exceeds the grid limit");
+    return OSDN_OK;
+}
+
+// Tokens a CTA takes at a time, and its grid: forward as many CTAs as there are such groups; the
+// backward at most four to an SM, since each leaves a row of partial weight gradients.
+int qk_tok(const osdn_qk_params* p) { return (int64_t)p->B * p->T >= 4096 ? 4 : 1; }
+unsigned qk_grid(const osdn_qk_params* p, bool backward) {
+    const int64_t tokens = (int64_t)p->B * p->T, tok = qk_tok(p), n = (tokens + tok - 1) / tok;
+    return (unsigned)(backward ? std::min<int64_t>(n, 4 * sm_count()) : n);
+}
+
+template <bool kBackward> int launch_heads(const osdn_qk_params* p, const osdn::heads::Args& a, cudaStream_t st) {
+    using bf = __nv_bfloat16;
+    const int tok = qk_tok(p);
+    auto go = [&](auto g, auto k, auto tx) {
+        osdn::heads::heads_kernel<g, k, kBackward, decltype(tx)>
+            <<<qk_grid(p, kBackward), osdn::heads::kThreads, sizeof(float2) * k * (a.rot / 2), st>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "head norm and rotation launch");
+    };
+    auto types = [&](auto g, auto k) { return p->dtype == OSDN_FP32 ? go(g, k, float{}) : go(g, k, bf{}); };
+    auto toks = [&](auto g) {
+        return tok == 4 ? types(g, std::integral_constant<int, 4>{}) : types(g, std::integral_constant<int, 1>{});
+    };
+    if (p->width <= 64) return toks(std::integral_constant<int, 8>{});
+    if (p->width <= 128) return toks(std::integral_constant<int, 16>{});
+    return toks(std::integral_constant<int, 32>{});
+}
+
+osdn::heads::Args heads_args(const osdn_qk_params* p, const int64_t* positions, const double* freqs,
+                             const int32_t* lengths) {
+    osdn::heads::Args a{};
+    a.positions = reinterpret_cast<const long long*>(positions);
+    a.freqs = freqs;
+    a.lengths = lengths;
+    a.pos0 = p->pos0;
+    a.tokens = (long long)p->B * p->T;
+    a.T = p->T; a.width = p->width; a.rot = p->rot_dim; a.norm = p->norm; a.layout = p->layout;
+    a.eps = p->eps; a.amplitude = p->amplitude;
+    a.side[0].H = p->Hq; a.side[0].scale = p->scale_q;
+    a.side[1].H = p->Hk; a.side[1].scale = p->scale_k;
+    a.side[0].sx = qk_strides(p, p->stride_q, p->Hq);
+    a.side[1].sx = qk_strides(p, p->stride_k, p->Hk);
+    a.side[0].so = qk_strides(p, p->stride_out_q, p->Hq);
+    a.side[1].so = qk_strides(p, p->stride_out_k, p->Hk);
+    a.side[0].sd = {(int64_t)p->T * p->Hq * p->width, (int64_t)p->Hq * p->width, p->width};
+    a.side[1].sd = {(int64_t)p->T * p->Hk * p->width, (int64_t)p->Hk * p->width, p->width};
+    return a;
+}
+
+int check_qk_pointers(const osdn_qk_params* p, std::initializer_list<const void*> all, const int64_t* positions,
+                      const double* freqs, const int32_t* lengths) {
+    for (const void* q : all)
+        if (!aligned16(q)) return fail(OSDN_ERR_INVALID_ARG, "every pointer must be 16-byte aligned");
+    if (!element_aligned(positions, 8) || !element_aligned(freqs, 8) || !element_aligned(lengths, 4))
+        return fail(OSDN_ERR_INVALID_ARG, "positions, freqs and lengths must be aligned to their elements");
+    if (p->T > 0 && p->rot_dim > 0 && !freqs) return fail(OSDN_ERR_INVALID_ARG, "freqs is NULL with rot_dim > 0");
+    return OSDN_OK;
+}
+
+// An output that may be its input in place: the same pointer needs the same strides; rows stay apart.
+int check_qk_out(const osdn_qk_params* p, const osdn::heads::Side& s, const void* x, const void* out) {
+    if (!rows_apart<3>({p->B, p->T, s.H}, {s.so.b, s.so.t, s.so.h}, p->width))
+        return fail(OSDN_ERR_INVALID_ARG, "the output strides make rows overlap");
+    if (out == x && (s.so.b != s.sx.b || s.so.t != s.sx.t || s.so.h != s.sx.h))
+        return fail(OSDN_ERR_INVALID_ARG, "an output in place of its input needs the input's strides");
+    return OSDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int osdn_qk_fwd(const osdn_qk_params* p, const void* q, const void* k, const float* wq, const float* wk,
+                const int64_t* positions, const double* freqs, const int32_t* lengths, void* q_out, void* k_out,
+                void* cuda_stream) {
+    t_last_error.clear();
+    int rc = check_qk(p);
+    if (rc) return rc;
+    if (!p->Hk) k = nullptr, wk = nullptr, k_out = nullptr;
+    if (p->norm == OSDN_NORM_NONE && (wq || wk)) return fail(OSDN_ERR_INVALID_ARG, "weights need a norm");
+    if (p->T > 0 && (!q || !q_out || (p->Hk && (!k || !k_out))))
+        return fail(OSDN_ERR_INVALID_ARG, "a required pointer (q, k, q_out, k_out) is NULL");
+    if ((rc = check_qk_pointers(p, {q, k, wq, wk, q_out, k_out}, positions, freqs, lengths))) return rc;
+    osdn::heads::Args a = heads_args(p, positions, freqs, lengths);
+    if (p->T > 0 && ((rc = check_qk_out(p, a.side[0], q, q_out)) ||
+                     (p->Hk && (rc = check_qk_out(p, a.side[1], k, k_out)))))
+        return rc;
+    if (p->T > 0 && p->Hk && (q_out == k || k_out == q || q_out == k_out))
+        return fail(OSDN_ERR_INVALID_ARG, "q_out and k_out must not be each other's tensors");
+    if (p->T == 0) return OSDN_OK;
+    a.side[0].x = q; a.side[0].w = wq; a.side[0].out = q_out;
+    a.side[1].x = k; a.side[1].w = wk; a.side[1].out = k_out;
+    return launch_heads<false>(p, a, reinterpret_cast<cudaStream_t>(cuda_stream));
+}
+
+int osdn_qk_bwd_workspace_size(const osdn_qk_params* p, size_t* bytes) {
+    t_last_error.clear();
+    int rc = check_qk(p);
+    if (rc) return rc;
+    if (!bytes) return fail(OSDN_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = round_up((size_t)2 * qk_grid(p, true) * p->width * sizeof(float), 256);
+    return OSDN_OK;
+}
+
+int osdn_qk_bwd(const osdn_qk_params* p, const void* q, const void* k, const float* wq, const float* wk,
+                const int64_t* positions, const double* freqs, const int32_t* lengths, const void* dq_out,
+                const void* dk_out, void* dq, void* dk, float* dwq, float* dwk, void* workspace,
+                size_t workspace_bytes, void* cuda_stream) {
+    t_last_error.clear();
+    int rc = check_qk(p);
+    if (rc) return rc;
+    if (!p->Hk) k = nullptr, wk = nullptr, dk_out = nullptr, dk = nullptr, dwk = nullptr;
+    if (p->norm == OSDN_NORM_NONE && (wq || wk || dwq || dwk))
+        return fail(OSDN_ERR_INVALID_ARG, "weights need a norm");
+    if (p->T > 0 && (!q || !dq_out || !dq || (p->Hk && (!k || !dk_out || !dk))))
+        return fail(OSDN_ERR_INVALID_ARG, "a required pointer (q, k, dq_out, dk_out, dq, dk) is NULL");
+    if ((rc = check_qk_pointers(p, {q, k, wq, wk, dq_out, dk_out, dq, dk, dwq, dwk, workspace}, positions, freqs,
+                                lengths)))
+        return rc;
+    if (p->T > 0)
+        for (const void* in : {q, k, dq_out, dk_out})
+            if (in && (dq == in || dk == in)) return fail(OSDN_ERR_INVALID_ARG, "dq and dk must not be an input");
+    if (p->T > 0 && p->Hk && dq == dk) return fail(OSDN_ERR_INVALID_ARG, "dq and dk are the same pointer");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    cudaError_t e;
+    if (p->T == 0) {
+        for (float* w : {dwq, dwk})
+            if (w && (e = cudaMemsetAsync(w, 0, p->width * sizeof(float), st)) != cudaSuccess)
+                return cuda_fail(e, "weight gradient");
+        return OSDN_OK;
+    }
+    const unsigned grid = qk_grid(p, true);
+    const size_t part = (size_t)grid * p->width;
+    float* ws = static_cast<float*>(workspace);
+    if (dwq || dwk) {
+        if (!ws) return fail(OSDN_ERR_INVALID_ARG, "workspace is NULL");
+        if (workspace_bytes < 2 * part * sizeof(float))
+            return fail(OSDN_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes,
+                        2 * part * sizeof(float));
+    }
+    osdn::heads::Args a = heads_args(p, positions, freqs, lengths);
+    a.side[0].x = q; a.side[0].w = wq; a.side[0].dout = dq_out; a.side[0].out = dq; a.side[0].dw = dwq ? ws : nullptr;
+    a.side[1].x = k; a.side[1].w = wk; a.side[1].dout = dk_out; a.side[1].out = dk;
+    a.side[1].dw = dwk ? ws + part : nullptr;
+    if ((rc = launch_heads<true>(p, a, st))) return rc;
+    if (dwq || dwk) {
+        osdn::heads::dw_kernel<<<dim3((p->width + 31) / 32, 2), 256, 0, st>>>(ws, ws + part, dwq, dwk, (int)grid,
+                                                                              p->width);
+        if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "weight gradient launch");
+    }
+    return OSDN_OK;
+}
+
+int osdn_rope(const osdn_qk_params* p, const void* x, const int64_t* positions, const double* freqs,
+              const int32_t* lengths, void* out, int inverse, void* cuda_stream) {
+    t_last_error.clear();
+    if (p && p->struct_size == sizeof(osdn_qk_params) && p->norm != OSDN_NORM_NONE)
+        return fail(OSDN_ERR_INVALID_ARG, "the rotation alone takes OSDN_NORM_NONE");
+    int rc = check_qk(p);
+    if (rc) return rc;
+    if (p->rot_dim == 0) return fail(OSDN_ERR_INVALID_ARG, "rot_dim must be positive");
+    osdn_qk_params one = *p;
+    one.Hk = 0;
+    if (p->T > 0 && (!x || !out)) return fail(OSDN_ERR_INVALID_ARG, "a required pointer (x, out) is NULL");
+    if ((rc = check_qk_pointers(&one, {x, out}, positions, freqs, lengths))) return rc;
+    osdn::heads::Args a = heads_args(&one, positions, freqs, lengths);
+    if (p->T > 0 && (rc = check_qk_out(&one, a.side[0], x, out))) return rc;
+    if (p->T == 0) return OSDN_OK;
+    a.side[0].x = x; a.side[0].out = out;
+    a.inverse = inverse != 0;
+    return launch_heads<false>(&one, a, reinterpret_cast<cudaStream_t>(cuda_stream));
+}
+
+int osdn_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, int64_t original_length,
+                    double low_turns, double high_turns, double* freqs, double* amplitude) {
+    t_last_error.clear();
+    if (!freqs) return fail(OSDN_ERR_INVALID_ARG, "freqs is NULL");
+    if (rot_dim < 2 || rot_dim % 2 || rot_dim > osdn::heads::kMaxWidth)
+        return fail(OSDN_ERR_INVALID_ARG, "rot_dim must be even, 2 .. 256 (got %d)", rot_dim);
+    if (!(base > 1.0) || !std::isfinite(base)) return fail(OSDN_ERR_INVALID_ARG, "base must be finite and above 1");
+    if (scaling < OSDN_ROPE_PLAIN || scaling > OSDN_ROPE_WAVELENGTH)
+        return fail(OSDN_ERR_INVALID_ARG, "unknown scaling %d", scaling);
+    if (scaling != OSDN_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+        return fail(OSDN_ERR_INVALID_ARG, "factor must be finite and >= 1");
+    if (scaling == OSDN_ROPE_NTK && rot_dim < 4) return fail(OSDN_ERR_INVALID_ARG, "NTK scaling needs rot_dim >= 4");
+    const bool ramped = scaling == OSDN_ROPE_YARN || scaling == OSDN_ROPE_WAVELENGTH;
+    if (ramped && original_length < 1) return fail(OSDN_ERR_INVALID_ARG, "original_length must be >= 1");
+    if (ramped && (!(low_turns > 0.0) || !(high_turns > low_turns) || !std::isfinite(high_turns)))
+        return fail(OSDN_ERR_INVALID_ARG, "0 < low_turns < high_turns is needed");
+    constexpr double kTwoPi = 6.283185307179586477;
+    const int n = rot_dim / 2;
+    if (scaling == OSDN_ROPE_NTK) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+    auto pair_of = [&](double turns) {   // the index whose pair turns that often over original_length
+        return rot_dim * std::log((double)original_length / (turns * kTwoPi)) / (2.0 * std::log(base));
+    };
+    double low = 0, high = 0;
+    if (scaling == OSDN_ROPE_YARN) {
+        low = std::max(std::floor(pair_of(high_turns)), 0.0);
+        high = std::min(std::ceil(pair_of(low_turns)), (double)rot_dim - 1);
+    }
+    for (int i = 0; i < n; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot_dim);
+        double keep = 1.0;                // share of the unscaled frequency
+        if (scaling == OSDN_ROPE_LINEAR) keep = 0.0;
+        if (scaling == OSDN_ROPE_YARN) keep = 1.0 - std::min(std::max((i - low) / std::max(high - low, 1e-3), 0.0), 1.0);
+        if (scaling == OSDN_ROPE_WAVELENGTH)
+            keep = std::min(std::max((original_length * f / kTwoPi - low_turns) / (high_turns - low_turns), 0.0), 1.0);
+        freqs[i] = keep == 1.0 ? f : f * ((1.0 - keep) / factor + keep);
+    }
+    if (amplitude) *amplitude = scaling == OSDN_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    return OSDN_OK;
 }
 
 }  // extern "C"
