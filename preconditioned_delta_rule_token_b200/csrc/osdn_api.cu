@@ -1479,44 +1479,92 @@ osdn::recur::Args recur_args(const osdn_recur_params* p) {
     return a;
 }
 
-// Channels a thread takes: the most, up to 4, at which every row of every tensor starts on a whole
-// vector. `each` lists the token tensors with their element size.
+// How a call runs: channels a thread takes (two where every row of every tensor starts on such a pair),
+// whether tiles come in by 16-byte copies (rows and widths in whole 16 bytes), CTAs of a cluster.
+// `each` lists the token tensors that are read or written at the strides, with their element size.
 struct TokenPtr {
     const void* ptr;
     size_t elem;
 };
-int recur_vec(const osdn_recur_params* p, const osdn::recur::Args& a, std::initializer_list<TokenPtr> each) {
-    for (int v = 4; v > 1; v /= 2) {
-        bool ok = p->D % v == 0 && !((a.xb | a.xt | a.gb | a.gt | a.hb | a.ht) % v);
-        for (const TokenPtr& t : each) ok = ok && reinterpret_cast<uintptr_t>(t.ptr) % (v * t.elem) == 0;
-        if (ok) return v;
-    }
-    return 1;
+struct RecurPlan {
+    int vec;
+    bool async;
+    int R;
+};
+RecurPlan recur_plan(const osdn_recur_params* p, const osdn::recur::Args& a, std::initializer_list<TokenPtr> each) {
+    auto whole = [&](int bytes, int elems) {
+        const int64_t strides = a.xb | a.xt | a.gb | a.gt | a.hb | a.ht | p->D;
+        for (const TokenPtr& t : each) {
+            const int n = bytes ? bytes / (int)t.elem : elems;
+            if (strides % n || reinterpret_cast<uintptr_t>(t.ptr) % (n * t.elem)) return false;
+        }
+        return true;
+    };
+    RecurPlan pl;
+    pl.vec = whole(0, 2) ? 2 : 1;
+    pl.async = whole(16, 0);
+    const int64_t units = (int64_t)p->B * ((p->D + 32 * pl.vec - 1) / (32 * pl.vec));
+    const int64_t tiles = ((int64_t)p->T + osdn::recur::kTile - 1) / osdn::recur::kTile;
+    pl.R = 1;
+    static const int64_t want = getenv("RECUR_CTAS") ? atoi(getenv("RECUR_CTAS")) : 296;
+    while (pl.R < osdn::recur::kMaxCluster && units * pl.R < want && pl.R < tiles) pl.R *= 2;
+    return pl;
 }
 
-// f(V, Tx, Tg) for the vector width and the types as constants.
-template <typename F> int recur_dispatch(const osdn_recur_params* p, int vec, F&& f) {
+// f(V, async, Tx, Tg) for the plan and the types as constants.
+template <typename F> int recur_dispatch(const osdn_recur_params* p, const RecurPlan& pl, F&& f) {
     using bf = __nv_bfloat16;
-    auto types = [&](auto v) {
-        if (p->dtype == OSDN_FP32) return f(v, float{}, float{});
-        if (p->gate_dtype == OSDN_FP32) return f(v, bf{}, float{});
-        return f(v, bf{}, bf{});
+    auto types = [&](auto v, auto as) {
+        if (p->dtype == OSDN_FP32) return f(v, as, float{}, float{});
+        if (p->gate_dtype == OSDN_FP32) return f(v, as, bf{}, float{});
+        return f(v, as, bf{}, bf{});
     };
-    if (vec == 4) return types(std::integral_constant<int, 4>{});
-    if (vec == 2) return types(std::integral_constant<int, 2>{});
-    return types(std::integral_constant<int, 1>{});
+    if (pl.async) return types(std::integral_constant<int, 2>{}, std::true_type{});
+    if (pl.vec == 2) return types(std::integral_constant<int, 2>{}, std::false_type{});
+    return types(std::integral_constant<int, 1>{}, std::false_type{});
+}
+
+// Launch of `kern` in clusters of R CTAs with `smem` bytes of dynamic shared memory.
+int launch_recur(void (*kern)(osdn::recur::Args), const osdn::recur::Args& a, unsigned grid, int smem, int max_smem,
+                 std::atomic<uint64_t>& ready, cudaStream_t st, const char* what) {
+    cudaError_t e;
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "current device");
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {   // once a device: the kernel's limits
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+            return cuda_fail(e, what);
+        if (dev < 64) ready.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(osdn::recur::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = a.R;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = a.R > 1 ? 1 : 0;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, a)) != cudaSuccess) return cuda_fail(e, what);
+    return OSDN_OK;
 }
 
 bool element_aligned(const void* p, size_t elem) { return reinterpret_cast<uintptr_t>(p) % elem == 0; }
 
 int launch_recur_fwd(const osdn_recur_params* p, osdn::recur::Args a, cudaStream_t st) {
     const size_t ex = elem_size(p->dtype), eg = elem_size(p->gate_dtype);
-    return recur_dispatch(p, recur_vec(p, a, {{a.x, ex}, {a.gate, eg}, {a.h, ex}}), [&](auto v, auto tx, auto tg) {
+    const RecurPlan pl = recur_plan(p, a, {{a.x, ex}, {a.gate, eg}, {a.h, ex}});
+    return recur_dispatch(p, pl, [&](auto v, auto as, auto tx, auto tg) {
+        using namespace osdn::recur;
+        static std::atomic<uint64_t> ready{0};
         a.cblocks = (p->D + 32 * v - 1) / (32 * v);
-        osdn::recur::fwd_kernel<v, decltype(tx), decltype(tg)>
-            <<<(unsigned)p->B * a.cblocks, osdn::recur::kThreads, 0, st>>>(a);
-        const cudaError_t e = cudaGetLastError();
-        return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "recurrence launch");
+        a.R = pl.R;
+        constexpr int stages = fwd_slots<v, as, decltype(tx), decltype(tg)>();
+        return launch_recur(fwd_kernel<v, as, decltype(tx), decltype(tg)>, a, (unsigned)p->B * a.cblocks * a.R,
+                            stages + slot_bytes<v>(a.R), stages + slot_bytes<v>(kMaxCluster), ready, st,
+                            "recurrence launch");
     });
 }
 
@@ -1592,12 +1640,16 @@ int osdn_recur_bwd(const osdn_recur_params* p, const void* x, const void* gate, 
         a.ckpt = nullptr;
     }
     a.dh = dh; a.dfinal = dfinal_h; a.ckpt_in = checkpoints; a.dx = dx; a.dgate = dgate; a.dh0 = dh0;
-    return recur_dispatch(p, recur_vec(p, a, {{x, ex}, {gate, eg}, {dh, ex}}), [&](auto v, auto tx, auto tg) {
+    const RecurPlan pl = recur_plan(p, a, {{x, ex}, {gate, eg}, {dh, ex}});
+    return recur_dispatch(p, pl, [&](auto v, auto as, auto tx, auto tg) {
+        using namespace osdn::recur;
+        static std::atomic<uint64_t> ready{0};
         a.cblocks = (p->D + 32 * v - 1) / (32 * v);
-        osdn::recur::bwd_kernel<v, decltype(tx), decltype(tg)>
-            <<<(unsigned)p->B * a.cblocks, osdn::recur::kThreads, 0, st>>>(a);
-        const cudaError_t e = cudaGetLastError();
-        return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "recurrence backward launch");
+        a.R = pl.R;
+        constexpr int stages = bwd_slots<v, as, decltype(tx), decltype(tg)>();
+        return launch_recur(bwd_kernel<v, as, decltype(tx), decltype(tg)>, a, (unsigned)p->B * a.cblocks * a.R,
+                            stages + slot_bytes<v>(a.R), stages + slot_bytes<v>(kMaxCluster), ready, st,
+                            "recurrence backward launch");
     });
 }
 
@@ -1619,14 +1671,24 @@ int osdn_recur_step(const osdn_recur_params* p, const void* x, const void* gate,
     osdn::recur::Args a = recur_args(&q);
     a.xt = a.gt = a.ht = 0;   // one token: these strides are not used
     a.x = x; a.gate = gate; a.h = h; a.final_h = state;
-    return recur_dispatch(&q, recur_vec(&q, a, {{x, ex}, {gate, eg}, {h, ex}}), [&](auto v, auto tx, auto tg) {
+    const size_t each[3] = {ex, eg, ex};
+    const void* ptrs[3] = {x, gate, h};
+    bool four = q.D % 4 == 0 && !((a.xb | a.gb | a.hb) % 4);   // four channels a thread where all rows allow it
+    for (int i = 0; i < 3; ++i) four = four && element_aligned(ptrs[i], 4 * each[i]);
+    auto go = [&](auto v, auto tx, auto tg) {
         const int64_t n = (int64_t)q.B * (q.D / v), blocks = (n + 255) / 256;
         osdn::recur::step_kernel<v, decltype(tx), decltype(tg)>
             <<<(unsigned)std::min<int64_t>(blocks, 148 * 8), 256, 0,
                reinterpret_cast<cudaStream_t>(cuda_stream)>>>(a);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "recurrence step launch");
-    });
+    };
+    auto types = [&](auto v) {
+        using bf = __nv_bfloat16;
+        if (q.dtype == OSDN_FP32) return go(v, float{}, float{});
+        return q.gate_dtype == OSDN_FP32 ? go(v, bf{}, float{}) : go(v, bf{}, bf{});
+    };
+    return four ? types(std::integral_constant<int, 4>{}) : types(std::integral_constant<int, 1>{});
 }
 
 }  // extern "C"

@@ -63,7 +63,7 @@ struct Args {
     const int* lengths;
     void *h, *dx, *dgate;
     float *final_h, *ckpt, *dh0;
-    int B, T, D, form, scale, cblocks;
+    int B, T, D, form, scale, cblocks, R;
     int64_t xb, xt, gb, gt, hb, ht;     // element strides of x, gate and h (or dh) over (b, t)
 };
 
@@ -82,35 +82,149 @@ __device__ __forceinline__ int length_of(const Args& p, int b) {
     return n < 0 ? 0 : n > p.T ? p.T : n;
 }
 
-// One CTA walks the tiles of one sequence and 32 V channels in order.
-template <int V, typename Tx, typename Tg>
+// ---- tiles in shared memory
+
+template <typename T> constexpr int kTileBytes(int V) { return kTile * 32 * V * (int)sizeof(T); }
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool read) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Starts the copy of tokens t0 .. t0 + 63 of 32 V channels (channel c0 on) into tile [64][32 V]; tokens
+// from len on and channels from D on are zeros and not read. All threads, 16 bytes each at a time.
+template <int V, typename T>
+__device__ __forceinline__ void fetch_tile(T* tile, const T* base, int64_t stride, int t0, int len, int c0, int D) {
+    constexpr int kPer = 16 / sizeof(T), kRow = 32 * V / kPer;   // elements of 16 bytes, such pieces of a row
+#pragma unroll
+    for (int i = 0; i < kTile * kRow / kThreads; ++i) {
+        const int k = threadIdx.x + i * kThreads, row = k / kRow, col = (k % kRow) * kPer;
+        const bool in = t0 + row < len && c0 + col < D;
+        cp_async16(tile + row * 32 * V + col, in ? base + (int64_t)(t0 + row) * stride + col : base, in);
+    }
+}
+
+// ---- joining the CTAs of a cluster
+
+__device__ __forceinline__ void store_remote(float2* local, int rank, float2 v) {
+    uint32_t a = (uint32_t)__cvta_generic_to_shared(local), r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(r), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The incoming value of each run of a tile, by one thread a channel. part[w] = (product, end from 0) of
+// run w, carry = the value before the cluster's tiles; the runs and the CTAs are taken in the order
+// of the walk (kUp: first to last). Writes in[w], returns through `entry` the value before this CTA's tile and
+// updates carry to the value behind all of the cluster's tiles.
+template <int V, bool kUp>
+__device__ __forceinline__ void join_runs(const float* partA, const float* partE, float* in, float2 (*slots)[32 * V],
+                                          int R, int rank, float& carry, float& entry) {
+    const int ch = threadIdx.x;
+    float A[kWarps], E[kWarps], a = 1.f, e = 0.f;
+    if (ch < 32 * V) {
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const int w = kUp ? i : kWarps - 1 - i;
+            A[i] = partA[w * 32 * V + ch];
+            E[i] = partE[w * 32 * V + ch];
+            e = fmaf(A[i], e, E[i]);
+            a *= A[i];
+        }
+        for (int r = 0; R > 1 && r < R; ++r) store_remote(&slots[rank][ch], r, make_float2(a, e));
+    }
+    if (R > 1) cluster_sync();
+    if (ch < 32 * V) {
+        entry = carry;
+        if (R > 1) {
+            for (int i = 0; i < R; ++i) {
+                const int r = kUp ? i : R - 1 - i;
+                const float2 s = slots[r][ch];
+                if (r == rank) entry = carry;
+                carry = fmaf(s.x, carry, s.y);
+            }
+        } else {
+            carry = fmaf(a, carry, e);
+        }
+        float v = entry;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            in[(kUp ? i : kWarps - 1 - i) * 32 * V + ch] = v;
+            v = fmaf(A[i], v, E[i]);
+        }
+    }
+}
+
+constexpr int kStages = 3;              // tiles in flight or in use
+constexpr int kMaxCluster = 16;
+
+// Dynamic shared memory: the stages, then the cluster's slots [2][R][32 V] (none for one CTA).
+template <int V, bool kAsync, typename Tx, typename Tg> constexpr int fwd_slots() {
+    return kAsync ? kStages * (kTileBytes<Tx>(V) + kTileBytes<Tg>(V)) : 0;
+}
+template <int V, bool kAsync, typename Tx, typename Tg> constexpr int bwd_slots() {
+    return kAsync ? kStages * (2 * kTileBytes<Tx>(V) + kTileBytes<Tg>(V)) : 0;
+}
+template <int V> constexpr int slot_bytes(int R) { return R > 1 ? 2 * R * 32 * V * (int)sizeof(float2) : 0; }
+
+// A cluster of R CTAs walks one sequence and 32 V channels, R tiles at a time.
+template <int V, bool kAsync, typename Tx, typename Tg>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const Args p) {
-    __shared__ float sA[2][kWarps][32 * V], sH[2][kWarps][32 * V];
+    constexpr int W = 32 * V;
+    extern __shared__ __align__(16) char dyn[];
+    Tx* bx = reinterpret_cast<Tx*>(dyn);                                        // [kStages][kTile][W]
+    Tg* bg = reinterpret_cast<Tg*>(dyn + kStages * kTileBytes<Tx>(V));
+    __shared__ float sA[kWarps][W], sE[kWarps][W], sIn[kWarps][W];
+    auto slots = reinterpret_cast<float2(*)[W]>(dyn + fwd_slots<V, kAsync, Tx, Tg>());   // [2][R][W]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.x / p.cblocks, c = (blockIdx.x % p.cblocks) * 32 * V + lane * V;
+    const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
+    const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * V;
     const bool on = c < p.D;
     const int len = length_of(p, b);
     const bool want_b = p.scale != kNone;
-    const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c;
-    const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c;
+    const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c0;
+    const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c0;
     Tx* h = p.h ? static_cast<Tx*>(p.h) + b * p.hb + c : nullptr;
     const int tiles = (len + kTile - 1) / kTile, all_tiles = (p.T + kTile - 1) / kTile;
+    const int steps = (tiles + R - 1) / R;
 
-    float carry[V];
+    const int ch = threadIdx.x;                     // channel whose runs this thread joins
+    const bool joins = ch < W && c0 + ch < p.D;
+    float carry = joins && p.h0 ? p.h0[(int64_t)b * p.D + c0 + ch] : 0.f, entry = 0.f;
+
+    auto fetch = [&](int i) {
+        if (kAsync && i < steps) {
+            const int t0 = (i * R + rank) * kTile;
+            fetch_tile<V>(bx + (i % kStages) * kTile * W, x, p.xt, t0, len, c0, p.D);
+            fetch_tile<V>(bg + (i % kStages) * kTile * W, gate, p.gt, t0, len, c0, p.D);
+        }
+        if (kAsync) cp_async_commit();
+    };
 #pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = 0.f;
-    if (on && p.h0) load_vec<V>(p.h0 + (int64_t)b * p.D + c, carry);
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    if (kAsync) cp_async_wait<kStages - 2>();
+    __syncthreads();
 
-    for (int tile = 0; tile < tiles; ++tile) {
-        const int t0 = tile * kTile + warp * kRun, par = tile & 1;
+    for (int i = 0; i < steps; ++i) {
+        const int t0 = (i * R + rank) * kTile + warp * kRun;
         float P[kRun][V], H[kRun][V];
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
             const bool in = on && t0 + j < len;
             float xv[V], gv[V];
-            if (in) {
-                load_vec<V>(x + (t0 + j) * p.xt, xv);
-                load_vec<V>(gate + (t0 + j) * p.gt, gv);
+            if (kAsync) {
+                const int at = ((i % kStages) * kTile + warp * kRun + j) * W + lane * V;
+                load_vec<V>(bx + at, xv);
+                load_vec<V>(bg + at, gv);
+            } else if (in) {
+                load_vec<V>(x + lane * V + (t0 + j) * p.xt, xv);
+                load_vec<V>(gate + lane * V + (t0 + j) * p.gt, gv);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -123,23 +237,18 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const Args p) {
                 H[j][v] = j ? fmaf(a, H[j ? j - 1 : 0][v], u) : u;
             }
         }
-        store_vec<V>(&sA[par][warp][lane * V], P[kRun - 1]);
-        store_vec<V>(&sH[par][warp][lane * V], H[kRun - 1]);
+        store_vec<V>(&sA[warp][lane * V], P[kRun - 1]);
+        store_vec<V>(&sE[warp][lane * V], H[kRun - 1]);
         __syncthreads();
-        float hin[V];
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp)
-#pragma unroll
-                for (int v = 0; v < V; ++v) hin[v] = carry[v];
-            float A[V], E[V];
-            load_vec<V>(&sA[par][w][lane * V], A);
-            load_vec<V>(&sH[par][w][lane * V], E);
-#pragma unroll
-            for (int v = 0; v < V; ++v) carry[v] = fmaf(A[v], carry[v], E[v]);
-        }
-        if (on && p.ckpt && warp == 0) store_vec<V>(p.ckpt + ((int64_t)b * all_tiles + tile) * p.D + c, hin);
+        fetch(i + kStages - 1);
+        join_runs<V, true>(&sA[0][0], &sE[0][0], &sIn[0][0], slots + (i & 1) * R, R, rank, carry, entry);
+        if (joins && p.ckpt && i * R + rank < tiles)
+            p.ckpt[((int64_t)b * all_tiles + i * R + rank) * p.D + c0 + ch] = entry;
+        if (kAsync) cp_async_wait<kStages - 2>();
+        __syncthreads();
         if (on && h) {
+            float hin[V];
+            load_vec<V>(&sIn[warp][lane * V], hin);
 #pragma unroll
             for (int j = 0; j < kRun; ++j)
                 if (t0 + j < len) {
@@ -150,106 +259,150 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const Args p) {
                 }
         }
     }
-    if (on && p.final_h && warp == 0) store_vec<V>(p.final_h + (int64_t)b * p.D + c, carry);
+    if (joins && p.final_h && rank == 0) p.final_h[(int64_t)b * p.D + c0 + ch] = carry;
 }
 
-// One CTA walks the tiles of one sequence and 32 V channels from the last to the first; the states
-// h_{t-1} are run again from the state that the forward saved at the tile's start.
-template <int V, typename Tx, typename Tg>
+// A cluster of R CTAs walks the tiles of one sequence and 32 V channels from the last to the first; the
+// states h_{t-1} are run again from the state that the forward saved at the tile's start.
+template <int V, bool kAsync, typename Tx, typename Tg>
 __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args p) {
-    __shared__ float sA[2][kWarps][32 * V], sH[2][kWarps][32 * V], sM[2][kWarps][32 * V];
+    constexpr int W = 32 * V;
+    extern __shared__ __align__(16) char dyn[];
+    Tx* bx = reinterpret_cast<Tx*>(dyn);                                        // [kStages][kTile][W]
+    Tx* bd = reinterpret_cast<Tx*>(dyn + kStages * kTileBytes<Tx>(V));
+    Tg* bg = reinterpret_cast<Tg*>(dyn + 2 * kStages * kTileBytes<Tx>(V));
+    __shared__ float sA[kWarps][W], sE[kWarps][W], sM[kWarps][W], sH[kWarps][W], sIn[kWarps][W];
+    auto slots = reinterpret_cast<float2(*)[W]>(dyn + bwd_slots<V, kAsync, Tx, Tg>());   // [2][R][W]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.x / p.cblocks, c = (blockIdx.x % p.cblocks) * 32 * V + lane * V;
+    const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
+    const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * V;
     const bool on = c < p.D;
     const int len = length_of(p, b);
     const bool want_b = p.scale != kNone;
-    const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c;
-    const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c;
-    const Tx* dh = static_cast<const Tx*>(p.dh) + b * p.hb + c;
+    const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c0;
+    const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c0;
+    const Tx* dh = static_cast<const Tx*>(p.dh) + b * p.hb + c0;
     Tx* dx = static_cast<Tx*>(p.dx) + (int64_t)b * p.T * p.D + c;
     Tg* dgate = static_cast<Tg*>(p.dgate) + (int64_t)b * p.T * p.D + c;
     const int tiles = (len + kTile - 1) / kTile, all_tiles = (p.T + kTile - 1) / kTile;
+    const int steps = (tiles + R - 1) / R;
 
-    float carry[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = 0.f;
-    if (on && p.dfinal) load_vec<V>(p.dfinal + (int64_t)b * p.D + c, carry);
+    const int ch = threadIdx.x;
+    const bool joins = ch < W && c0 + ch < p.D;
+    float carry = joins && p.dfinal ? p.dfinal[(int64_t)b * p.D + c0 + ch] : 0.f, entry = 0.f;
+    auto tile_of = [&](int i) { return (steps - 1 - i) * R + rank; };
 
-    for (int tile = tiles - 1; tile >= 0; --tile) {
-        const int t0 = tile * kTile + warp * kRun, par = tile & 1;
-        float a[kRun][V], bb[kRun][V], xv[kRun][V], dv[kRun][V], hin[V];
+    auto fetch = [&](int i) {
+        if (kAsync && i < steps) {
+            const int t0 = tile_of(i) * kTile, s = (i % kStages) * kTile * W;
+            fetch_tile<V>(bx + s, x, p.xt, t0, len, c0, p.D);
+            fetch_tile<V>(bg + s, gate, p.gt, t0, len, c0, p.D);
+            fetch_tile<V>(bd + s, dh, p.ht, t0, len, c0, p.D);
+        }
+        if (kAsync) cp_async_commit();
+    };
 #pragma unroll
-        for (int v = 0; v < V; ++v) hin[v] = 0.f;
-        if (on) load_vec<V>(p.ckpt_in + ((int64_t)b * all_tiles + tile) * p.D + c, hin);
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    if (kAsync) cp_async_wait<kStages - 2>();
+    __syncthreads();
+
+    for (int i = 0; i < steps; ++i) {
+        const int tile = tile_of(i), t0 = tile * kTile + warp * kRun;
+        const int at0 = ((i % kStages) * kTile + warp * kRun) * W + lane * V;
+        float start = joins && tile < tiles ? p.ckpt_in[((int64_t)b * all_tiles + tile) * p.D + c0 + ch] : 0.f;
+        float a[kRun][V], bb[kRun][V], xr[kAsync ? 1 : kRun][V], dr[kAsync ? 1 : kRun][V];
+        auto x_at = [&](int j, float* o) {          // x and dh of token j: again from the tile, or kept
+            if constexpr (kAsync) load_vec<V>(bx + at0 + j * W, o);
+            else
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = xr[j][v];
+        };
+        auto dh_at = [&](int j, float* o) {
+            if constexpr (kAsync) load_vec<V>(bd + at0 + j * W, o);
+            else
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = dr[j][v];
+        };
         float A[V], E[V], M[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) A[v] = 1.f, E[v] = M[v] = 0.f;
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
             const bool in = on && t0 + j < len;
-            float gv[V];
-            if (in) {
-                load_vec<V>(x + (t0 + j) * p.xt, xv[j]);
-                load_vec<V>(gate + (t0 + j) * p.gt, gv);
-                load_vec<V>(dh + (t0 + j) * p.ht, dv[j]);
+            float xv[V], gv[V];
+            if constexpr (kAsync) {
+                load_vec<V>(bg + at0 + j * W, gv);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) gv[v] = xr[j][v] = dr[j][v] = 0.f;
+                if (in) {
+                    load_vec<V>(x + lane * V + (t0 + j) * p.xt, xr[j]);
+                    load_vec<V>(gate + lane * V + (t0 + j) * p.gt, gv);
+                    load_vec<V>(dh + lane * V + (t0 + j) * p.ht, dr[j]);
+                }
             }
+            x_at(j, xv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
+                a[j][v] = 1.f;
+                bb[j][v] = 0.f;
                 if (in) {
                     float ds;
                     decay_of(gv[v], p.form, want_b, a[j][v], bb[j][v]);
-                    E[v] = fmaf(a[j][v], E[v], scale_of(a[j][v], bb[j][v], p.scale, ds) * xv[j][v]);
-                } else {
-                    a[j][v] = 1.f;
-                    bb[j][v] = xv[j][v] = dv[j][v] = 0.f;
+                    E[v] = fmaf(a[j][v], E[v], scale_of(a[j][v], bb[j][v], p.scale, ds) * xv[v]);
                 }
                 A[v] *= a[j][v];
             }
         }
 #pragma unroll
-        for (int j = kRun - 1; j >= 0; --j)
+        for (int j = kRun - 1; j >= 0; --j) {
+            float dv[V];
+            dh_at(j, dv);                            // zeros behind the length
 #pragma unroll
-            for (int v = 0; v < V; ++v) M[v] = a[j][v] * (dv[j][v] + M[v]);
-        store_vec<V>(&sA[par][warp][lane * V], A);
-        store_vec<V>(&sH[par][warp][lane * V], E);
-        store_vec<V>(&sM[par][warp][lane * V], M);
+            for (int v = 0; v < V; ++v) M[v] = a[j][v] * (dv[v] + M[v]);
+        }
+        store_vec<V>(&sA[warp][lane * V], A);
+        store_vec<V>(&sE[warp][lane * V], E);
+        store_vec<V>(&sM[warp][lane * V], M);
         __syncthreads();
-        float mu[V];
+        fetch(i + kStages - 1);
+        if (ch < W) {                                // the states before each run
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-            if (w == warp)
-#pragma unroll
-                for (int v = 0; v < V; ++v) mu[v] = carry[v];
-            load_vec<V>(&sA[par][w][lane * V], A);
-            load_vec<V>(&sM[par][w][lane * V], M);
-#pragma unroll
-            for (int v = 0; v < V; ++v) carry[v] = fmaf(A[v], carry[v], M[v]);
+            for (int w = 0; w < kWarps; ++w) {
+                sH[w][ch] = start;
+                start = fmaf(sA[w][ch], start, sE[w][ch]);
+            }
         }
-        for (int w = 0; w < warp; ++w) {
-            load_vec<V>(&sA[par][w][lane * V], A);
-            load_vec<V>(&sH[par][w][lane * V], E);
+        join_runs<V, false>(&sA[0][0], &sM[0][0], &sIn[0][0], slots + (i & 1) * R, R, rank, carry, entry);
+        if (kAsync) cp_async_wait<kStages - 2>();
+        __syncthreads();
+        float hin[V], mu[V];
+        load_vec<V>(&sH[warp][lane * V], hin);
+        load_vec<V>(&sIn[warp][lane * V], mu);
+        float before[kRun][V];                       // h_{t-1}
 #pragma unroll
-            for (int v = 0; v < V; ++v) hin[v] = fmaf(A[v], hin[v], E[v]);
-        }
-        float before[kRun][V];   // h_{t-1}
-#pragma unroll
-        for (int j = 0; j < kRun; ++j)
+        for (int j = 0; j < kRun; ++j) {
+            float xv[V];
+            x_at(j, xv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float ds;
                 before[j][v] = hin[v];
-                hin[v] = fmaf(a[j][v], hin[v], scale_of(a[j][v], bb[j][v], p.scale, ds) * xv[j][v]);
+                hin[v] = fmaf(a[j][v], hin[v], scale_of(a[j][v], bb[j][v], p.scale, ds) * xv[v]);
             }
+        }
 #pragma unroll
         for (int j = kRun - 1; j >= 0; --j) {
-            float ox[V], og[V];
+            float ox[V], og[V], xv[V], dv[V];
+            x_at(j, xv);
+            dh_at(j, dv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float ds;
-                const float lam = dv[j][v] + mu[v];
+                const float lam = dv[v] + mu[v];
                 const float s = scale_of(a[j][v], bb[j][v], p.scale, ds);
                 ox[v] = s * lam;
-                og[v] = lam * slope_of(a[j][v], bb[j][v], p.form) * fmaf(xv[j][v], ds, before[j][v]);
+                og[v] = lam * slope_of(a[j][v], bb[j][v], p.form) * fmaf(xv[v], ds, before[j][v]);
                 mu[v] = a[j][v] * lam;
             }
             if (on && t0 + j < len) {
@@ -258,7 +411,7 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args p) {
             }
         }
     }
-    if (on && p.dh0 && warp == 0) store_vec<V>(p.dh0 + (int64_t)b * p.D + c, carry);
+    if (joins && p.dh0 && rank == 0) p.dh0[(int64_t)b * p.D + c0 + ch] = carry;
 }
 
 // One token for every channel: state <- a state + s x in place, h = the new state.
