@@ -9,6 +9,8 @@
 // kTile tokens x 32 V channels, each warp runs its kRun tokens from 0, and the runs are joined
 // through shared memory in the order of the tokens.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace osdn {
@@ -22,39 +24,121 @@ constexpr int kRun = 8;                 // tokens of one run, held in registers
 constexpr int kTile = kWarps * kRun;    // 64: also the distance of the saved states
 constexpr int kThreads = 32 * kWarps;
 
-// a and b = 1 - a (b without the cancellation of 1 - a where a is a function of the gate).
-__device__ __forceinline__ void decay_of(float g, int form, bool want_b, float& a, float& b) {
-    if (form == kDecay) {
+// ---- two channels at a time: one instruction for both where sm_100a has it (fma, mul, add on f32x2)
+
+__device__ __forceinline__ uint64_t bits2(float2 a) { return *reinterpret_cast<uint64_t*>(&a); }
+__device__ __forceinline__ float2 pair2(uint64_t a) { return *reinterpret_cast<float2*>(&a); }
+__device__ __forceinline__ float2 all2(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float root(float x) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rroot(float x) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// a and b = 1 - a, each without the cancellation of taking it from the other where that one is near 1:
+// a product of thousands of decays near 1 shows any bias of a single one.
+//   log:   |g| < 0.2: b = -(g + g^2/2 + ... + g^6/720), the exponential's series (the next term is below
+//          2e-8 of b), a = 1 - b; else a = 2^(g log2 e) and b = 1 - a;
+//   logit: with e = exp(-|g|) and m = e / (1 + e) <= 1/2, a and b are m and 1 - m by the sign of g.
+template <int kForm> __device__ __forceinline__ void decay_of(float2 g, float2& a, float2& b) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    if constexpr (kForm == kDecay) {
         a = g;
-        b = 1.f - g;
-    } else if (form == kLog) {
-        a = expf(g);
-        b = want_b ? -expm1f(g) : 0.f;
+        b = add2(all2(1.f), neg2(g));
+    } else if constexpr (kForm == kLog) {
+        const float2 t = mul2(g, all2(kLog2e));
+        const float2 la = make_float2(ex2(t.x), ex2(t.y));
+        const float2 lb = add2(all2(1.f), neg2(la));
+        float2 s = fma2(g, all2(1.f / 720), all2(1.f / 120));
+        s = fma2(g, s, all2(1.f / 24));
+        s = fma2(g, s, all2(1.f / 6));
+        s = fma2(g, s, all2(0.5f));
+        s = fma2(g, s, all2(1.f));
+        const float2 ng = neg2(g), sb = mul2(ng, s), sa = fma2(g, s, all2(1.f));
+        const bool x = fabsf(g.x) < 0.2f, y = fabsf(g.y) < 0.2f;
+        a = make_float2(x ? sa.x : la.x, y ? sa.y : la.y);
+        b = make_float2(x ? sb.x : lb.x, y ? sb.y : lb.y);
     } else {
-        const float e = expf(-fabsf(g)), r = __fdividef(1.f, 1.f + e), er = e * r;
-        a = g >= 0.f ? r : er;
-        b = g >= 0.f ? er : r;
+        const float2 e = make_float2(ex2(-kLog2e * fabsf(g.x)), ex2(-kLog2e * fabsf(g.y)));
+        const float2 d = add2(e, all2(1.f));
+        const float2 m = mul2(e, make_float2(rcp(d.x), rcp(d.y)));
+        const float2 q = add2(all2(1.f), neg2(m));
+        a = make_float2(g.x >= 0.f ? q.x : m.x, g.y >= 0.f ? q.y : m.y);
+        b = make_float2(g.x >= 0.f ? m.x : q.x, g.y >= 0.f ? m.y : q.y);
     }
+}
+
+template <int kScale> __device__ __forceinline__ float2 scale_of(float2 a, float2 b) {
+    if constexpr (kScale == kNone) return all2(1.f);
+    if constexpr (kScale == kComplement) return b;
+    const float2 y = fma2(a, b, b);
+    return make_float2(root(y.x), root(y.y));
 }
 
 // s, and ds/da (0 where s = 0: the slope of the root is unbounded there).
-__device__ __forceinline__ float scale_of(float a, float b, int scale, float& ds) {
-    if (scale == kNone) {
-        ds = 0.f;
-        return 1.f;
+template <int kScale> __device__ __forceinline__ float2 scale_of(float2 a, float2 b, float2& ds) {
+    if constexpr (kScale == kNone) {
+        ds = all2(0.f);
+        return all2(1.f);
     }
-    if (scale == kComplement) {
-        ds = -1.f;
+    if constexpr (kScale == kComplement) {
+        ds = all2(-1.f);
         return b;
     }
-    const float y = b * (1.f + a);
-    const float r = y > 0.f ? rsqrtf(y) : 0.f;
-    ds = -a * r;
-    return y * r;
+    const float2 y = fma2(a, b, b);
+    const float2 r = make_float2(y.x > 0.f ? rroot(y.x) : 0.f, y.y > 0.f ? rroot(y.y) : 0.f);
+    ds = mul2(neg2(a), r);
+    return mul2(y, r);
 }
 
-__device__ __forceinline__ float slope_of(float a, float b, int form) {   // da / dgate
-    return form == kDecay ? 1.f : form == kLog ? a : a * b;
+template <int kForm> __device__ __forceinline__ float2 slope_of(float2 a, float2 b) {   // da / dgate
+    if constexpr (kForm == kDecay) return all2(1.f);
+    if constexpr (kForm == kLog) return a;
+    return mul2(a, b);
+}
+
+// f(form, scale) as constants: one branch for all that a thread does with them.
+template <typename F> __device__ __forceinline__ void with_kind(int form, int scale, F&& f) {
+    auto scales = [&](auto fo) {
+        if (scale == kNone) f(fo, std::integral_constant<int, kNone>{});
+        else if (scale == kComplement) f(fo, std::integral_constant<int, kComplement>{});
+        else f(fo, std::integral_constant<int, kNorm>{});
+    };
+    if (form == kDecay) scales(std::integral_constant<int, kDecay>{});
+    else if (form == kLog) scales(std::integral_constant<int, kLog>{});
+    else scales(std::integral_constant<int, kLogit>{});
 }
 
 struct Args {
@@ -67,13 +151,20 @@ struct Args {
     int64_t xb, xt, gb, gt, hb, ht;     // element strides of x, gate and h (or dh) over (b, t)
 };
 
-template <int V, typename T> __device__ __forceinline__ void load_vec(const T* p, float* o) {
-    if constexpr (V == 1) o[0] = to_f32(*p);
-    else VecIO<V, T>::load(p, o);
+// V (1 or 2) channels as a pair; the second of one channel is 0 and not stored.
+template <int V, typename T> __device__ __forceinline__ float2 load_pair(const T* p) {
+    if constexpr (V == 1) return make_float2(to_f32(*p), 0.f);
+    float o[2];
+    VecIO<2, T>::load(p, o);
+    return make_float2(o[0], o[1]);
 }
-template <int V, typename T> __device__ __forceinline__ void store_vec(T* p, const float* o) {
-    if constexpr (V == 1) *p = from_f32<T>(o[0]);
-    else VecIO<V, T>::store(p, o);
+template <int V, typename T> __device__ __forceinline__ void store_pair(T* p, float2 v) {
+    if constexpr (V == 1) {
+        *p = from_f32<T>(v.x);
+    } else {
+        const float o[2] = {v.x, v.y};
+        VecIO<2, T>::store(p, o);
+    }
 }
 
 __device__ __forceinline__ int length_of(const Args& p, int b) {
@@ -175,19 +266,18 @@ template <int V> constexpr int slot_bytes(int R) { return R > 1 ? 2 * R * 32 * V
 
 // A cluster of R CTAs walks one sequence and 32 V channels, R tiles at a time.
 template <int V, bool kAsync, typename Tx, typename Tg>
-__global__ void __launch_bounds__(kThreads) fwd_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, kAsync ? 3 : 2) fwd_kernel(const Args p) {
     constexpr int W = 32 * V;
     extern __shared__ __align__(16) char dyn[];
     Tx* bx = reinterpret_cast<Tx*>(dyn);                                        // [kStages][kTile][W]
     Tg* bg = reinterpret_cast<Tg*>(dyn + kStages * kTileBytes<Tx>(V));
-    __shared__ float sA[kWarps][W], sE[kWarps][W], sIn[kWarps][W];
     auto slots = reinterpret_cast<float2(*)[W]>(dyn + fwd_slots<V, kAsync, Tx, Tg>());   // [2][R][W]
+    __shared__ float sA[kWarps][W], sE[kWarps][W], sIn[kWarps][W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
     const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * V;
     const bool on = c < p.D;
     const int len = length_of(p, b);
-    const bool want_b = p.scale != kNone;
     const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c0;
     const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c0;
     Tx* h = p.h ? static_cast<Tx*>(p.h) + b * p.hb + c : nullptr;
@@ -213,32 +303,37 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const Args p) {
 
     for (int i = 0; i < steps; ++i) {
         const int t0 = (i * R + rank) * kTile + warp * kRun;
-        float P[kRun][V], H[kRun][V];
+        const int live = !on ? 0 : len - t0;        // tokens of this run inside the sequence
+        float2 P[kRun], H[kRun];
+        const int at0 = ((i % kStages) * kTile + warp * kRun) * W + lane * V;
+        with_kind(p.form, p.scale, [&](auto form, auto scale) {
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) {
-            const bool in = on && t0 + j < len;
-            float xv[V], gv[V];
-            if (kAsync) {
-                const int at = ((i % kStages) * kTile + warp * kRun + j) * W + lane * V;
-                load_vec<V>(bx + at, xv);
-                load_vec<V>(bg + at, gv);
-            } else if (in) {
-                load_vec<V>(x + lane * V + (t0 + j) * p.xt, xv);
-                load_vec<V>(gate + lane * V + (t0 + j) * p.gt, gv);
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float a = 1.f, bb, ds, u = 0.f;
-                if (in) {
-                    decay_of(gv[v], p.form, want_b, a, bb);
-                    u = scale_of(a, bb, p.scale, ds) * xv[v];
+            for (int j = 0; j < kRun; ++j) {
+                float2 xv = all2(0.f), gv = all2(0.f), a, bb;
+                if constexpr (kAsync) {
+                    xv = load_pair<V>(bx + at0 + j * W);
+                    gv = load_pair<V>(bg + at0 + j * W);
+                } else if (j < live) {
+                    xv = load_pair<V>(x + lane * V + (t0 + j) * p.xt);
+                    gv = load_pair<V>(gate + lane * V + (t0 + j) * p.gt);
                 }
-                P[j][v] = j ? a * P[j ? j - 1 : 0][v] : a;
-                H[j][v] = j ? fmaf(a, H[j ? j - 1 : 0][v], u) : u;
+                decay_of<form>(gv, a, bb);
+                H[j] = scale == kNone ? xv : mul2(scale_of<scale>(a, bb), xv);
+                P[j] = a;
             }
+        });
+        if (live < kRun) {                          // tokens behind the length change nothing
+#pragma unroll
+            for (int j = 0; j < kRun; ++j)
+                if (j >= live) P[j] = all2(1.f), H[j] = all2(0.f);
         }
-        store_vec<V>(&sA[warp][lane * V], P[kRun - 1]);
-        store_vec<V>(&sE[warp][lane * V], H[kRun - 1]);
+#pragma unroll
+        for (int j = 1; j < kRun; ++j) {
+            H[j] = fma2(P[j], H[j - 1], H[j]);
+            P[j] = mul2(P[j], P[j - 1]);
+        }
+        store_pair<V>(&sA[warp][lane * V], P[kRun - 1]);
+        store_pair<V>(&sE[warp][lane * V], H[kRun - 1]);
         __syncthreads();
         fetch(i + kStages - 1);
         join_runs<V, true>(&sA[0][0], &sE[0][0], &sIn[0][0], slots + (i & 1) * R, R, rank, carry, entry);
@@ -246,17 +341,17 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const Args p) {
             p.ckpt[((int64_t)b * all_tiles + i * R + rank) * p.D + c0 + ch] = entry;
         if (kAsync) cp_async_wait<kStages - 2>();
         __syncthreads();
-        if (on && h) {
-            float hin[V];
-            load_vec<V>(&sIn[warp][lane * V], hin);
+        if (h && live > 0) {
+            const float2 hin = load_pair<V>(&sIn[warp][lane * V]);
+            Tx* o = h + t0 * p.ht;
+            if (live >= kRun) {
 #pragma unroll
-            for (int j = 0; j < kRun; ++j)
-                if (t0 + j < len) {
-                    float o[V];
+                for (int j = 0; j < kRun; ++j, o += p.ht) store_pair<V>(o, fma2(P[j], hin, H[j]));
+            } else {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) o[v] = fmaf(P[j][v], hin[v], H[j][v]);
-                    store_vec<V>(h + (t0 + j) * p.ht, o);
-                }
+                for (int j = 0; j < kRun; ++j, o += p.ht)
+                    if (j < live) store_pair<V>(o, fma2(P[j], hin, H[j]));
+            }
         }
     }
     if (joins && p.final_h && rank == 0) p.final_h[(int64_t)b * p.D + c0 + ch] = carry;
@@ -265,20 +360,19 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const Args p) {
 // A cluster of R CTAs walks the tiles of one sequence and 32 V channels from the last to the first; the
 // states h_{t-1} are run again from the state that the forward saved at the tile's start.
 template <int V, bool kAsync, typename Tx, typename Tg>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p) {
     constexpr int W = 32 * V;
     extern __shared__ __align__(16) char dyn[];
     Tx* bx = reinterpret_cast<Tx*>(dyn);                                        // [kStages][kTile][W]
     Tx* bd = reinterpret_cast<Tx*>(dyn + kStages * kTileBytes<Tx>(V));
     Tg* bg = reinterpret_cast<Tg*>(dyn + 2 * kStages * kTileBytes<Tx>(V));
-    __shared__ float sA[kWarps][W], sE[kWarps][W], sM[kWarps][W], sH[kWarps][W], sIn[kWarps][W];
     auto slots = reinterpret_cast<float2(*)[W]>(dyn + bwd_slots<V, kAsync, Tx, Tg>());   // [2][R][W]
+    __shared__ float sA[kWarps][W], sE[kWarps][W], sM[kWarps][W], sH[kWarps][W], sIn[kWarps][W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
     const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * V;
     const bool on = c < p.D;
     const int len = length_of(p, b);
-    const bool want_b = p.scale != kNone;
     const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c0;
     const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c0;
     const Tx* dh = static_cast<const Tx*>(p.dh) + b * p.hb + c0;
@@ -308,62 +402,45 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args p) {
 
     for (int i = 0; i < steps; ++i) {
         const int tile = tile_of(i), t0 = tile * kTile + warp * kRun;
+        const int live = !on ? 0 : len - t0;
         const int at0 = ((i % kStages) * kTile + warp * kRun) * W + lane * V;
         float start = joins && tile < tiles ? p.ckpt_in[((int64_t)b * all_tiles + tile) * p.D + c0 + ch] : 0.f;
-        float a[kRun][V], bb[kRun][V], xr[kAsync ? 1 : kRun][V], dr[kAsync ? 1 : kRun][V];
-        auto x_at = [&](int j, float* o) {          // x and dh of token j: again from the tile, or kept
-            if constexpr (kAsync) load_vec<V>(bx + at0 + j * W, o);
-            else
-#pragma unroll
-                for (int v = 0; v < V; ++v) o[v] = xr[j][v];
+        float2 a[kRun], bb[kRun], xr[kAsync ? 1 : kRun] = {}, dr[kAsync ? 1 : kRun] = {};
+        auto x_at = [&](int j) {                     // x and dh of token j: again from the tile, or kept
+            if constexpr (kAsync) return load_pair<V>(bx + at0 + j * W);
+            else return xr[j];
         };
-        auto dh_at = [&](int j, float* o) {
-            if constexpr (kAsync) load_vec<V>(bd + at0 + j * W, o);
-            else
-#pragma unroll
-                for (int v = 0; v < V; ++v) o[v] = dr[j][v];
+        auto dh_at = [&](int j) {
+            if constexpr (kAsync) return load_pair<V>(bd + at0 + j * W);
+            else return dr[j];
         };
-        float A[V], E[V], M[V];
+        float2 A = all2(1.f), E = all2(0.f), M = all2(0.f);
+        with_kind(p.form, p.scale, [&](auto form, auto scale) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = 1.f, E[v] = M[v] = 0.f;
-#pragma unroll
-        for (int j = 0; j < kRun; ++j) {
-            const bool in = on && t0 + j < len;
-            float xv[V], gv[V];
-            if constexpr (kAsync) {
-                load_vec<V>(bg + at0 + j * W, gv);
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v) gv[v] = xr[j][v] = dr[j][v] = 0.f;
-                if (in) {
-                    load_vec<V>(x + lane * V + (t0 + j) * p.xt, xr[j]);
-                    load_vec<V>(gate + lane * V + (t0 + j) * p.gt, gv);
-                    load_vec<V>(dh + lane * V + (t0 + j) * p.ht, dr[j]);
+            for (int j = 0; j < kRun; ++j) {
+                float2 gv = all2(0.f);
+                if constexpr (kAsync) {
+                    gv = load_pair<V>(bg + at0 + j * W);
+                } else {
+                    xr[j] = dr[j] = all2(0.f);       // what lies behind the length is not read
+                    if (j < live) {
+                        xr[j] = load_pair<V>(x + lane * V + (t0 + j) * p.xt);
+                        gv = load_pair<V>(gate + lane * V + (t0 + j) * p.gt);
+                        dr[j] = load_pair<V>(dh + lane * V + (t0 + j) * p.ht);
+                    }
                 }
+                decay_of<form>(gv, a[j], bb[j]);
+                if (live < kRun && j >= live) a[j] = all2(1.f), bb[j] = all2(0.f);
+                const float2 xv = x_at(j);
+                E = fma2(a[j], E, scale == kNone ? xv : mul2(scale_of<scale>(a[j], bb[j]), xv));
+                A = mul2(A, a[j]);
             }
-            x_at(j, xv);
+        });
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                a[j][v] = 1.f;
-                bb[j][v] = 0.f;
-                if (in) {
-                    float ds;
-                    decay_of(gv[v], p.form, want_b, a[j][v], bb[j][v]);
-                    E[v] = fmaf(a[j][v], E[v], scale_of(a[j][v], bb[j][v], p.scale, ds) * xv[v]);
-                }
-                A[v] *= a[j][v];
-            }
-        }
-#pragma unroll
-        for (int j = kRun - 1; j >= 0; --j) {
-            float dv[V];
-            dh_at(j, dv);                            // zeros behind the length
-#pragma unroll
-            for (int v = 0; v < V; ++v) M[v] = a[j][v] * (dv[v] + M[v]);
-        }
-        store_vec<V>(&sA[warp][lane * V], A);
-        store_vec<V>(&sE[warp][lane * V], E);
-        store_vec<V>(&sM[warp][lane * V], M);
+        for (int j = kRun - 1; j >= 0; --j) M = mul2(a[j], add2(dh_at(j), M));
+        store_pair<V>(&sA[warp][lane * V], A);
+        store_pair<V>(&sE[warp][lane * V], E);
+        store_pair<V>(&sM[warp][lane * V], M);
         __syncthreads();
         fetch(i + kStages - 1);
         if (ch < W) {                                // the states before each run
@@ -376,39 +453,31 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args p) {
         join_runs<V, false>(&sA[0][0], &sM[0][0], &sIn[0][0], slots + (i & 1) * R, R, rank, carry, entry);
         if (kAsync) cp_async_wait<kStages - 2>();
         __syncthreads();
-        float hin[V], mu[V];
-        load_vec<V>(&sH[warp][lane * V], hin);
-        load_vec<V>(&sIn[warp][lane * V], mu);
-        float before[kRun][V];                       // h_{t-1}
+        if (live > 0) {
+            float2 before[kRun], state = load_pair<V>(&sH[warp][lane * V]), mu = load_pair<V>(&sIn[warp][lane * V]);
+            with_kind(p.form, p.scale, [&](auto form, auto scale) {
+                float2 ds;
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) {
-            float xv[V];
-            x_at(j, xv);
+                for (int j = 0; j < kRun; ++j) {
+                    const float2 xv = x_at(j);
+                    before[j] = state;               // h_{t-1}
+                    state = fma2(a[j], state, scale == kNone ? xv : mul2(scale_of<scale>(a[j], bb[j]), xv));
+                }
+                Tx* ox = dx + (int64_t)(t0 + kRun - 1) * p.D;
+                Tg* og = dgate + (int64_t)(t0 + kRun - 1) * p.D;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float ds;
-                before[j][v] = hin[v];
-                hin[v] = fmaf(a[j][v], hin[v], scale_of(a[j][v], bb[j][v], p.scale, ds) * xv[v]);
-            }
-        }
-#pragma unroll
-        for (int j = kRun - 1; j >= 0; --j) {
-            float ox[V], og[V], xv[V], dv[V];
-            x_at(j, xv);
-            dh_at(j, dv);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float ds;
-                const float lam = dv[v] + mu[v];
-                const float s = scale_of(a[j][v], bb[j][v], p.scale, ds);
-                ox[v] = s * lam;
-                og[v] = lam * slope_of(a[j][v], bb[j][v], p.form) * fmaf(xv[v], ds, before[j][v]);
-                mu[v] = a[j][v] * lam;
-            }
-            if (on && t0 + j < len) {
-                store_vec<V>(dx + (int64_t)(t0 + j) * p.D, ox);
-                store_vec<V>(dgate + (int64_t)(t0 + j) * p.D, og);
-            }
+                for (int j = kRun - 1; j >= 0; --j, ox -= p.D, og -= p.D) {
+                    const float2 lam = add2(dh_at(j), mu);
+                    const float2 s = scale_of<scale>(a[j], bb[j], ds);
+                    float2 g = scale == kNone ? before[j] : fma2(x_at(j), ds, before[j]);
+                    g = mul2(form == kDecay ? lam : mul2(lam, slope_of<form>(a[j], bb[j])), g);
+                    mu = mul2(a[j], lam);
+                    if (j < live) {
+                        store_pair<V>(ox, scale == kNone ? lam : mul2(s, lam));
+                        store_pair<V>(og, g);
+                    }
+                }
+            });
         }
     }
     if (joins && p.dh0 && rank == 0) p.dh0[(int64_t)b * p.D + c0 + ch] = carry;
@@ -417,23 +486,39 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args p) {
 // One token for every channel: state <- a state + s x in place, h = the new state.
 template <int V, typename Tx, typename Tg>
 __global__ void __launch_bounds__(256) step_kernel(const Args p) {
+    constexpr int kPairs = V == 4 ? 2 : 1;
     const int per = p.D / V;
     const int64_t n = (int64_t)p.B * per;
-    const bool want_b = p.scale != kNone;
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t b = i / per, c = (i - b * per) * V;
-        float xv[V], gv[V], st[V];
-        load_vec<V>(static_cast<const Tx*>(p.x) + b * p.xb + c, xv);
-        load_vec<V>(static_cast<const Tg*>(p.gate) + b * p.gb + c, gv);
-        load_vec<V>(p.final_h + b * p.D + c, st);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float a, bb, ds;
-            decay_of(gv[v], p.form, want_b, a, bb);
-            st[v] = fmaf(a, st[v], scale_of(a, bb, p.scale, ds) * xv[v]);
+        float xv[4] = {}, gv[4] = {}, st[4] = {};
+        if constexpr (V == 4) {
+            VecIO<4, Tx>::load(static_cast<const Tx*>(p.x) + b * p.xb + c, xv);
+            VecIO<4, Tg>::load(static_cast<const Tg*>(p.gate) + b * p.gb + c, gv);
+            VecIO<4, float>::load(p.final_h + b * p.D + c, st);
+        } else {
+            xv[0] = to_f32(static_cast<const Tx*>(p.x)[b * p.xb + c]);
+            gv[0] = to_f32(static_cast<const Tg*>(p.gate)[b * p.gb + c]);
+            st[0] = p.final_h[b * p.D + c];
         }
-        store_vec<V>(p.final_h + b * p.D + c, st);
-        store_vec<V>(static_cast<Tx*>(p.h) + b * p.hb + c, st);
+        with_kind(p.form, p.scale, [&](auto form, auto scale) {
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) {
+                float2 a, bb;
+                decay_of<form>(make_float2(gv[2 * k], gv[2 * k + 1]), a, bb);
+                const float2 u = mul2(scale_of<scale>(a, bb), make_float2(xv[2 * k], xv[2 * k + 1]));
+                const float2 r = fma2(a, make_float2(st[2 * k], st[2 * k + 1]), u);
+                st[2 * k] = r.x;
+                st[2 * k + 1] = r.y;
+            }
+        });
+        if constexpr (V == 4) {
+            VecIO<4, float>::store(p.final_h + b * p.D + c, st);
+            VecIO<4, Tx>::store(static_cast<Tx*>(p.h) + b * p.hb + c, st);
+        } else {
+            p.final_h[b * p.D + c] = st[0];
+            static_cast<Tx*>(p.h)[b * p.hb + c] = from_f32<Tx>(st[0]);
+        }
     }
 }
 
