@@ -1475,20 +1475,22 @@ osdn::recur::Args recur_args(const osdn_recur_params* p) {
     a.B = p->B; a.T = p->T; a.D = p->D; a.form = p->gate_form; a.scale = p->input_scale;
     const Str2 x = recur_strides(p, p->stride_x), g = recur_strides(p, p->stride_gate),
                h = recur_strides(p, p->stride_h);
-    a.xb = x.b; a.xt = x.t; a.gb = g.b; a.gt = g.t; a.hb = h.b; a.ht = h.t;
+    if (p->B > 1) a.xb = x.b, a.gb = g.b, a.hb = h.b;   // a stride over one element is not used: 0
+    if (p->T > 1) a.xt = x.t, a.gt = g.t, a.ht = h.t;
+    a.wait_limit_ns = g_wait_limit_ns.load();
     return a;
 }
 
 // How a call runs: channels a thread takes (two where every row of every tensor starts on such a pair),
-// whether tiles come in by 16-byte copies (rows and widths in whole 16 bytes), CTAs of a cluster.
-// `each` lists the token tensors that are read or written at the strides, with their element size.
+// whether tiles go by tensor maps (rows and widths in whole 16 bytes, no stride of 0), CTAs of a
+// cluster. `each` lists the token tensors that are read or written at the strides, with their element size.
 struct TokenPtr {
     const void* ptr;
     size_t elem;
 };
 struct RecurPlan {
     int vec;
-    bool async;
+    bool tma;
     int R;
 };
 RecurPlan recur_plan(const osdn_recur_params* p, const osdn::recur::Args& a, std::initializer_list<TokenPtr> each) {
@@ -1502,7 +1504,8 @@ RecurPlan recur_plan(const osdn_recur_params* p, const osdn::recur::Args& a, std
     };
     RecurPlan pl;
     pl.vec = whole(0, 2) ? 2 : 1;
-    pl.async = whole(16, 0);
+    pl.tma = whole(16, 0) && (p->B == 1 || (a.xb && a.gb && a.hb)) && (p->T == 1 || (a.xt && a.gt && a.ht));
+    for (int64_t st : {a.xb, a.xt, a.gb, a.gt, a.hb, a.ht}) pl.tma = pl.tma && st < ((int64_t)1 << 37);
     const int64_t units = (int64_t)p->B * ((p->D + 32 * pl.vec - 1) / (32 * pl.vec));
     const int64_t tiles = ((int64_t)p->T + osdn::recur::kTile - 1) / osdn::recur::kTile;
     pl.R = 1;
@@ -1511,7 +1514,7 @@ RecurPlan recur_plan(const osdn_recur_params* p, const osdn::recur::Args& a, std
     return pl;
 }
 
-// f(V, async, Tx, Tg) for the plan and the types as constants.
+// f(V, tma, Tx, Tg) for the plan and the types as constants.
 template <typename F> int recur_dispatch(const osdn_recur_params* p, const RecurPlan& pl, F&& f) {
     using bf = __nv_bfloat16;
     auto types = [&](auto v, auto as) {
@@ -1519,13 +1522,32 @@ template <typename F> int recur_dispatch(const osdn_recur_params* p, const Recur
         if (p->gate_dtype == OSDN_FP32) return f(v, as, bf{}, float{});
         return f(v, as, bf{}, bf{});
     };
-    if (pl.async) return types(std::integral_constant<int, 2>{}, std::true_type{});
+    if (pl.tma) return types(std::integral_constant<int, 2>{}, std::true_type{});
     if (pl.vec == 2) return types(std::integral_constant<int, 2>{}, std::false_type{});
     return types(std::integral_constant<int, 1>{}, std::false_type{});
 }
 
+// Tensor map of [B, T, D] (a stride of 0: one sequence or token, never stepped over) with boxes of
+// `rows` tokens x 64 channels.
+int make_rows_map(CUtensorMap* m, const void* base, const osdn_recur_params* p, int dtype, int64_t sb, int64_t st,
+                  int rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return fail(OSDN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t es = elem_size(dtype);
+    const cuuint64_t dims[3] = {(cuuint64_t)p->D, (cuuint64_t)p->T, (cuuint64_t)p->B};
+    const cuuint64_t strides[2] = {(cuuint64_t)(st ? st : p->D) * es, (cuuint64_t)(sb ? sb : p->D) * es};
+    const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(m, dtype == OSDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                     const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(OSDN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return OSDN_OK;
+}
+
 // Launch of `kern` in clusters of R CTAs with `smem` bytes of dynamic shared memory.
-int launch_recur(void (*kern)(osdn::recur::Args), const osdn::recur::Args& a, unsigned grid, int smem, int max_smem,
+int launch_recur(void (*kern)(osdn::recur::Args, osdn::recur::Maps), const osdn::recur::Args& a,
+                 const osdn::recur::Maps& maps, unsigned grid, int smem, int max_smem,
                  std::atomic<uint64_t>& ready, cudaStream_t st, const char* what) {
     cudaError_t e;
     int dev = 0;
@@ -1547,7 +1569,7 @@ int launch_recur(void (*kern)(osdn::recur::Args), const osdn::recur::Args& a, un
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = a.R > 1 ? 1 : 0;
-    if ((e = cudaLaunchKernelEx(&cfg, kern, a)) != cudaSuccess) return cuda_fail(e, what);
+    if ((e = cudaLaunchKernelEx(&cfg, kern, a, maps)) != cudaSuccess) return cuda_fail(e, what);
     return OSDN_OK;
 }
 
@@ -1562,7 +1584,14 @@ int launch_recur_fwd(const osdn_recur_params* p, osdn::recur::Args a, cudaStream
         a.cblocks = (p->D + 32 * v - 1) / (32 * v);
         a.R = pl.R;
         constexpr int stages = fwd_slots<v, as, decltype(tx), decltype(tg)>();
-        return launch_recur(fwd_kernel<v, as, decltype(tx), decltype(tg)>, a, (unsigned)p->B * a.cblocks * a.R,
+        Maps maps{};
+        int rc = OSDN_OK;
+        if (as && p->T > 0)
+            (void)((rc = make_rows_map(&maps.x, a.x, p, p->dtype, a.xb, a.xt, kTile)) ||
+                   (rc = make_rows_map(&maps.gate, a.gate, p, p->gate_dtype, a.gb, a.gt, kTile)) ||
+                   (a.h && (rc = make_rows_map(&maps.o0, a.h, p, p->dtype, a.hb, a.ht, kRun))));
+        if (rc) return rc;
+        return launch_recur(fwd_kernel<v, as, decltype(tx), decltype(tg)>, a, maps, (unsigned)p->B * a.cblocks * a.R,
                             stages + slot_bytes<v>(a.R), stages + slot_bytes<v>(kMaxCluster), ready, st,
                             "recurrence launch");
     });
@@ -1647,7 +1676,17 @@ int osdn_recur_bwd(const osdn_recur_params* p, const void* x, const void* gate, 
         a.cblocks = (p->D + 32 * v - 1) / (32 * v);
         a.R = pl.R;
         constexpr int stages = bwd_slots<v, as, decltype(tx), decltype(tg)>();
-        return launch_recur(bwd_kernel<v, as, decltype(tx), decltype(tg)>, a, (unsigned)p->B * a.cblocks * a.R,
+        Maps maps{};
+        int rc = OSDN_OK;
+        const int64_t db = p->B > 1 ? (int64_t)p->T * p->D : 0, dt = p->T > 1 ? p->D : 0;
+        if (as && p->T > 0)
+            (void)((rc = make_rows_map(&maps.x, x, p, p->dtype, a.xb, a.xt, kTile)) ||
+                   (rc = make_rows_map(&maps.gate, gate, p, p->gate_dtype, a.gb, a.gt, kTile)) ||
+                   (rc = make_rows_map(&maps.dh, dh, p, p->dtype, a.hb, a.ht, kTile)) ||
+                   (rc = make_rows_map(&maps.o0, dx, p, p->dtype, db, dt, kRun)) ||
+                   (rc = make_rows_map(&maps.o1, dgate, p, p->gate_dtype, db, dt, kRun)));
+        if (rc) return rc;
+        return launch_recur(bwd_kernel<v, as, decltype(tx), decltype(tg)>, a, maps, (unsigned)p->B * a.cblocks * a.R,
                             stages + slot_bytes<v>(a.R), stages + slot_bytes<v>(kMaxCluster), ready, st,
                             "recurrence backward launch");
     });

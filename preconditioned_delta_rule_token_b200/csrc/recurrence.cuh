@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace osdn {
 namespace recur {
@@ -44,7 +45,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
     return pair2(r);
 }
-__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ float2 less1(float2 a) { return fma2(a, all2(-1.f), all2(1.f)); }   // 1 - a
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -76,17 +77,17 @@ template <int kForm> __device__ __forceinline__ void decay_of(float2 g, float2& 
     constexpr float kLog2e = 1.4426950408889634f;
     if constexpr (kForm == kDecay) {
         a = g;
-        b = add2(all2(1.f), neg2(g));
+        b = less1(g);
     } else if constexpr (kForm == kLog) {
         const float2 t = mul2(g, all2(kLog2e));
         const float2 la = make_float2(ex2(t.x), ex2(t.y));
-        const float2 lb = add2(all2(1.f), neg2(la));
-        float2 s = fma2(g, all2(1.f / 720), all2(1.f / 120));
-        s = fma2(g, s, all2(1.f / 24));
-        s = fma2(g, s, all2(1.f / 6));
-        s = fma2(g, s, all2(0.5f));
-        s = fma2(g, s, all2(1.f));
-        const float2 ng = neg2(g), sb = mul2(ng, s), sa = fma2(g, s, all2(1.f));
+        const float2 lb = less1(la);
+        float2 s = fma2(g, all2(-1.f / 720), all2(-1.f / 120));
+        s = fma2(g, s, all2(-1.f / 24));
+        s = fma2(g, s, all2(-1.f / 6));
+        s = fma2(g, s, all2(-0.5f));
+        s = fma2(g, s, all2(-1.f));
+        const float2 sb = mul2(g, s), sa = less1(sb);
         const bool x = fabsf(g.x) < 0.2f, y = fabsf(g.y) < 0.2f;
         a = make_float2(x ? sa.x : la.x, y ? sa.y : la.y);
         b = make_float2(x ? sb.x : lb.x, y ? sb.y : lb.y);
@@ -94,7 +95,7 @@ template <int kForm> __device__ __forceinline__ void decay_of(float2 g, float2& 
         const float2 e = make_float2(ex2(-kLog2e * fabsf(g.x)), ex2(-kLog2e * fabsf(g.y)));
         const float2 d = add2(e, all2(1.f));
         const float2 m = mul2(e, make_float2(rcp(d.x), rcp(d.y)));
-        const float2 q = add2(all2(1.f), neg2(m));
+        const float2 q = less1(m);
         a = make_float2(g.x >= 0.f ? q.x : m.x, g.y >= 0.f ? q.y : m.y);
         b = make_float2(g.x >= 0.f ? m.x : q.x, g.y >= 0.f ? m.y : q.y);
     }
@@ -119,7 +120,7 @@ template <int kScale> __device__ __forceinline__ float2 scale_of(float2 a, float
     }
     const float2 y = fma2(a, b, b);
     const float2 r = make_float2(y.x > 0.f ? rroot(y.x) : 0.f, y.y > 0.f ? rroot(y.y) : 0.f);
-    ds = mul2(neg2(a), r);
+    ds = mul2(a, mul2(r, all2(-1.f)));
     return mul2(y, r);
 }
 
@@ -148,6 +149,7 @@ struct Args {
     void *h, *dx, *dgate;
     float *final_h, *ckpt, *dh0;
     int B, T, D, form, scale, cblocks, R;
+    unsigned long long wait_limit_ns;
     int64_t xb, xt, gb, gt, hb, ht;     // element strides of x, gate and h (or dh) over (b, t)
 };
 
@@ -173,105 +175,150 @@ __device__ __forceinline__ int length_of(const Args& p, int b) {
     return n < 0 ? 0 : n > p.T ? p.T : n;
 }
 
-// ---- tiles in shared memory
+// ---- tiles in shared memory, by the tensor memory accelerator
+
+constexpr int kStages = 3;              // tiles in flight or in use
+constexpr int kMaxCluster = 16;
 
 template <typename T> constexpr int kTileBytes(int V) { return kTile * 32 * V * (int)sizeof(T); }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool read) {
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(read ? 16 : 0) : "memory");
+// Tensor maps over [B, T, D] (innermost first: channels, tokens, sequences): loads of 64 x 32 V, stores of
+// one run, 8 x 32 V.
+struct Maps {
+    CUtensorMap x, gate, dh;            // loads
+    CUtensorMap o0, o1;                 // stores: h, or dx and dgate
+};
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c, int t, int b, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(t), "r"(b), "r"(tc::smem_u32(bar))
+        : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c, int t, int b) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(tc::smem_u32(src)), "r"(c), "r"(t), "r"(b)
+                 : "memory");
 }
 
-// Starts the copy of tokens t0 .. t0 + 63 of 32 V channels (channel c0 on) into tile [64][32 V]; tokens
-// from len on and channels from D on are zeros and not read. All threads, 16 bytes each at a time.
-template <int V, typename T>
-__device__ __forceinline__ void fetch_tile(T* tile, const T* base, int64_t stride, int t0, int len, int c0, int D) {
-    constexpr int kPer = 16 / sizeof(T), kRow = 32 * V / kPer;   // elements of 16 bytes, such pieces of a row
-#pragma unroll
-    for (int i = 0; i < kTile * kRow / kThreads; ++i) {
-        const int k = threadIdx.x + i * kThreads, row = k / kRow, col = (k % kRow) * kPer;
-        const bool in = t0 + row < len && c0 + col < D;
-        cp_async16(tile + row * 32 * V + col, in ? base + (int64_t)(t0 + row) * stride + col : base, in);
+// The stages' barriers: one phase a use, waited for by every thread. A wait that passes the limit
+// sets the library's status word; later waits of that thread are then skipped, so the kernel still ends.
+struct Pipe {
+    uint64_t* full;                     // [kStages]
+    unsigned long long limit_ns;
+    bool failed;
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
+        if (!failed && !tc::mbar_wait(bar, parity, limit_ns)) {
+            failed = true;
+            atomicOr(&g_osdn_status, kStatusTimeout);
+        }
     }
-}
+    __device__ __forceinline__ void wait(int i) { wait(full + i % kStages, (i / kStages) & 1); }
+    // Copies that were started and not waited for, before the block leaves (only after a failed wait).
+    __device__ __forceinline__ void drain(int from, int to) {
+        if (!failed) return;
+        for (int i = from; i < to; ++i) tc::mbar_wait(full + i % kStages, (i / kStages) & 1, 1000000000ull);
+    }
+};
 
 // ---- joining the CTAs of a cluster
 
-__device__ __forceinline__ void store_remote(float2* local, int rank, float2 v) {
-    uint32_t a = (uint32_t)__cvta_generic_to_shared(local), r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(r), "f"(v.x), "f"(v.y) : "memory");
+__device__ __forceinline__ uint32_t at_rank(const void* local, int rank) {   // the same address in CTA `rank`
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(local)), "r"(rank));
+    return r;
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+
+// What the CTAs of a cluster tell one another each step: (product, end from 0) of their tile, a pair a
+// channel, stored into every CTA's slots with the bytes counted on that CTA's barrier, so a step needs no
+// fence and only the joining threads wait. Two sets by the step's parity: a CTA sends for step i + 2 after it
+// has step i + 1 from all, and they sent that after reading step i.
+template <int V> struct Exchange {
+    static constexpr int W = 32 * V;
+    float2 (*slots)[W];                 // [2][R][W]
+    uint64_t* bar;                      // [2]
+    int R, rank;
+    __device__ __forceinline__ void init() {
+        if (R == 1) return;
+        if (threadIdx.x == 0) {
+            tc::mbar_init(bar, 1);
+            tc::mbar_init(bar + 1, 1);
+            tc::fence_mbar_init();
+        }
+        cluster_sync();
+    }
+    __device__ __forceinline__ void send(int i, int ch, float2 v) {
+        if (ch == 0) tc::mbar_arrive_expect_tx(bar + (i & 1), R * W * (int)sizeof(float2));
+        float2* slot = &slots[(i & 1) * R + rank][ch];
+        for (int r = 0; r < R; ++r)
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                             at_rank(slot, r)),
+                         "f"(v.x), "f"(v.y), "r"(at_rank(bar + (i & 1), r))
+                         : "memory");
+    }
+};
 
 // The incoming value of each run of a tile, by one thread a channel. part[w] = (product, end from 0) of
 // run w, carry = the value before the cluster's tiles; the runs and the CTAs are taken in the order
 // of the walk (kUp: first to last). Writes in[w], returns through `entry` the value before this CTA's tile and
 // updates carry to the value behind all of the cluster's tiles.
 template <int V, bool kUp>
-__device__ __forceinline__ void join_runs(const float* partA, const float* partE, float* in, float2 (*slots)[32 * V],
-                                          int R, int rank, float& carry, float& entry) {
+__device__ __forceinline__ void join_runs(const float* partA, const float* partE, float* in, Exchange<V>& ex, Pipe& pipe,
+                                          int i, float& carry, float& entry) {
     const int ch = threadIdx.x;
+    if (ch >= 32 * V) return;
     float A[kWarps], E[kWarps], a = 1.f, e = 0.f;
-    if (ch < 32 * V) {
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const int w = kUp ? i : kWarps - 1 - i;
-            A[i] = partA[w * 32 * V + ch];
-            E[i] = partE[w * 32 * V + ch];
-            e = fmaf(A[i], e, E[i]);
-            a *= A[i];
-        }
-        for (int r = 0; R > 1 && r < R; ++r) store_remote(&slots[rank][ch], r, make_float2(a, e));
+    for (int k = 0; k < kWarps; ++k) {
+        const int w = kUp ? k : kWarps - 1 - k;
+        A[k] = partA[w * 32 * V + ch];
+        E[k] = partE[w * 32 * V + ch];
+        e = fmaf(A[k], e, E[k]);
+        a *= A[k];
     }
-    if (R > 1) cluster_sync();
-    if (ch < 32 * V) {
-        entry = carry;
-        if (R > 1) {
-            for (int i = 0; i < R; ++i) {
-                const int r = kUp ? i : R - 1 - i;
-                const float2 s = slots[r][ch];
-                if (r == rank) entry = carry;
-                carry = fmaf(s.x, carry, s.y);
-            }
-        } else {
-            carry = fmaf(a, carry, e);
+    entry = carry;
+    if (ex.R > 1) {
+        ex.send(i, ch, make_float2(a, e));
+        pipe.wait(ex.bar + (i & 1), (i >> 1) & 1);
+        for (int k = 0; k < ex.R; ++k) {
+            const int r = kUp ? k : ex.R - 1 - k;
+            const float2 s = ex.slots[(i & 1) * ex.R + r][ch];
+            if (r == ex.rank) entry = carry;
+            carry = fmaf(s.x, carry, s.y);
         }
-        float v = entry;
+    } else {
+        carry = fmaf(a, carry, e);
+    }
+    float v = entry;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            in[(kUp ? i : kWarps - 1 - i) * 32 * V + ch] = v;
-            v = fmaf(A[i], v, E[i]);
-        }
+    for (int k = 0; k < kWarps; ++k) {
+        in[(kUp ? k : kWarps - 1 - k) * 32 * V + ch] = v;
+        v = fmaf(A[k], v, E[k]);
     }
 }
 
-constexpr int kStages = 3;              // tiles in flight or in use
-constexpr int kMaxCluster = 16;
-
-// Dynamic shared memory: the stages, then the cluster's slots [2][R][32 V] (none for one CTA).
-template <int V, bool kAsync, typename Tx, typename Tg> constexpr int fwd_slots() {
-    return kAsync ? kStages * (kTileBytes<Tx>(V) + kTileBytes<Tg>(V)) : 0;
+// Dynamic shared memory: the stages (128-byte aligned), then the cluster's slots [2][R][32 V] (none for one CTA).
+template <int V, bool kTma, typename Tx, typename Tg> constexpr int fwd_slots() {
+    return kTma ? kStages * (kTileBytes<Tx>(V) + kTileBytes<Tg>(V)) : 0;
 }
-template <int V, bool kAsync, typename Tx, typename Tg> constexpr int bwd_slots() {
-    return kAsync ? kStages * (2 * kTileBytes<Tx>(V) + kTileBytes<Tg>(V)) : 0;
+template <int V, bool kTma, typename Tx, typename Tg> constexpr int bwd_slots() {
+    return kTma ? kStages * (2 * kTileBytes<Tx>(V) + kTileBytes<Tg>(V)) : 0;
 }
 template <int V> constexpr int slot_bytes(int R) { return R > 1 ? 2 * R * 32 * V * (int)sizeof(float2) : 0; }
 
 // A cluster of R CTAs walks one sequence and 32 V channels, R tiles at a time.
-template <int V, bool kAsync, typename Tx, typename Tg>
-__global__ void __launch_bounds__(kThreads, kAsync ? 3 : 2) fwd_kernel(const Args p) {
+template <int V, bool kTma, typename Tx, typename Tg>
+__global__ void __launch_bounds__(kThreads, kTma ? 3 : 2) fwd_kernel(const Args p, const __grid_constant__ Maps maps) {
     constexpr int W = 32 * V;
-    extern __shared__ __align__(16) char dyn[];
+    extern __shared__ __align__(128) char dyn[];
     Tx* bx = reinterpret_cast<Tx*>(dyn);                                        // [kStages][kTile][W]
     Tg* bg = reinterpret_cast<Tg*>(dyn + kStages * kTileBytes<Tx>(V));
-    auto slots = reinterpret_cast<float2(*)[W]>(dyn + fwd_slots<V, kAsync, Tx, Tg>());   // [2][R][W]
+    auto slots = reinterpret_cast<float2(*)[W]>(dyn + fwd_slots<V, kTma, Tx, Tg>());   // [2][R][W]
     __shared__ float sA[kWarps][W], sE[kWarps][W], sIn[kWarps][W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
@@ -288,29 +335,39 @@ __global__ void __launch_bounds__(kThreads, kAsync ? 3 : 2) fwd_kernel(const Arg
     const bool joins = ch < W && c0 + ch < p.D;
     float carry = joins && p.h0 ? p.h0[(int64_t)b * p.D + c0 + ch] : 0.f, entry = 0.f;
 
-    auto fetch = [&](int i) {
-        if (kAsync && i < steps) {
-            const int t0 = (i * R + rank) * kTile;
-            fetch_tile<V>(bx + (i % kStages) * kTile * W, x, p.xt, t0, len, c0, p.D);
-            fetch_tile<V>(bg + (i % kStages) * kTile * W, gate, p.gt, t0, len, c0, p.D);
+    __shared__ uint64_t full[kStages];
+    Pipe pipe{full, p.wait_limit_ns, false};
+    __shared__ uint64_t joined[2];
+    Exchange<V> ex{slots, joined, R, rank};
+    ex.init();
+    auto fetch = [&](int i) {                       // starts the copies of this CTA's i-th tile (thread 0)
+        if (kTma && threadIdx.x == 0 && i < steps) {
+            const int t0 = (i * R + rank) * kTile, s = i % kStages;
+            tc::mbar_arrive_expect_tx(full + s, kTileBytes<Tx>(V) + kTileBytes<Tg>(V));
+            tma_load_3d(bx + s * kTile * W, &maps.x, c0, t0, b, full + s);
+            tma_load_3d(bg + s * kTile * W, &maps.gate, c0, t0, b, full + s);
         }
-        if (kAsync) cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i);
-    if (kAsync) cp_async_wait<kStages - 2>();
-    __syncthreads();
+    if (kTma) {
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < kStages; ++s) tc::mbar_init(full + s, 1);
+            tc::fence_mbar_init();
+        }
+        __syncthreads();
+        for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    }
 
     for (int i = 0; i < steps; ++i) {
         const int t0 = (i * R + rank) * kTile + warp * kRun;
-        const int live = !on ? 0 : len - t0;        // tokens of this run inside the sequence
+        const int live = kTma || on ? len - t0 : 0;   // tokens of this run inside the sequence
         float2 P[kRun], H[kRun];
+        if (kTma) pipe.wait(i);
         const int at0 = ((i % kStages) * kTile + warp * kRun) * W + lane * V;
         with_kind(p.form, p.scale, [&](auto form, auto scale) {
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
                 float2 xv = all2(0.f), gv = all2(0.f), a, bb;
-                if constexpr (kAsync) {
+                if constexpr (kTma) {
                     xv = load_pair<V>(bx + at0 + j * W);
                     gv = load_pair<V>(bg + at0 + j * W);
                 } else if (j < live) {
@@ -334,14 +391,24 @@ __global__ void __launch_bounds__(kThreads, kAsync ? 3 : 2) fwd_kernel(const Arg
         }
         store_pair<V>(&sA[warp][lane * V], P[kRun - 1]);
         store_pair<V>(&sE[warp][lane * V], H[kRun - 1]);
+        if (kTma && lane == 0) tc::bulk_wait_read<0>();   // the last tile has left: its stage is free
         __syncthreads();
         fetch(i + kStages - 1);
-        join_runs<V, true>(&sA[0][0], &sE[0][0], &sIn[0][0], slots + (i & 1) * R, R, rank, carry, entry);
+        join_runs<V, true>(&sA[0][0], &sE[0][0], &sIn[0][0], ex, pipe, i, carry, entry);
         if (joins && p.ckpt && i * R + rank < tiles)
             p.ckpt[((int64_t)b * all_tiles + i * R + rank) * p.D + c0 + ch] = entry;
-        if (kAsync) cp_async_wait<kStages - 2>();
         __syncthreads();
-        if (h && live > 0) {
+        if (kTma && h && live >= kRun) {            // a whole run: over its own x in the tile, and out from there
+            const float2 hin = load_pair<V>(&sIn[warp][lane * V]);
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) store_pair<V>(bx + at0 + j * W, fma2(P[j], hin, H[j]));
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_3d(&maps.o0, bx + at0, c0, t0, b);
+                tc::bulk_commit();
+            }
+        } else if (h && on && live > 0) {
             const float2 hin = load_pair<V>(&sIn[warp][lane * V]);
             Tx* o = h + t0 * p.ht;
             if (live >= kRun) {
@@ -355,18 +422,23 @@ __global__ void __launch_bounds__(kThreads, kAsync ? 3 : 2) fwd_kernel(const Arg
         }
     }
     if (joins && p.final_h && rank == 0) p.final_h[(int64_t)b * p.D + c0 + ch] = carry;
+    if (kTma) {
+        pipe.drain(0, steps);
+        if (lane == 0) tc::bulk_wait_read<0>();
+    }
+    if (R > 1) cluster_sync();   // no CTA leaves while another may still store to it
 }
 
 // A cluster of R CTAs walks the tiles of one sequence and 32 V channels from the last to the first; the
 // states h_{t-1} are run again from the state that the forward saved at the tile's start.
-template <int V, bool kAsync, typename Tx, typename Tg>
-__global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p) {
+template <int V, bool kTma, typename Tx, typename Tg>
+__global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __grid_constant__ Maps maps) {
     constexpr int W = 32 * V;
-    extern __shared__ __align__(16) char dyn[];
+    extern __shared__ __align__(128) char dyn[];
     Tx* bx = reinterpret_cast<Tx*>(dyn);                                        // [kStages][kTile][W]
     Tx* bd = reinterpret_cast<Tx*>(dyn + kStages * kTileBytes<Tx>(V));
     Tg* bg = reinterpret_cast<Tg*>(dyn + 2 * kStages * kTileBytes<Tx>(V));
-    auto slots = reinterpret_cast<float2(*)[W]>(dyn + bwd_slots<V, kAsync, Tx, Tg>());   // [2][R][W]
+    auto slots = reinterpret_cast<float2(*)[W]>(dyn + bwd_slots<V, kTma, Tx, Tg>());   // [2][R][W]
     __shared__ float sA[kWarps][W], sE[kWarps][W], sM[kWarps][W], sH[kWarps][W], sIn[kWarps][W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
@@ -386,40 +458,50 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p) {
     float carry = joins && p.dfinal ? p.dfinal[(int64_t)b * p.D + c0 + ch] : 0.f, entry = 0.f;
     auto tile_of = [&](int i) { return (steps - 1 - i) * R + rank; };
 
+    __shared__ uint64_t full[kStages];
+    Pipe pipe{full, p.wait_limit_ns, false};
+    __shared__ uint64_t joined[2];
+    Exchange<V> ex{slots, joined, R, rank};
+    ex.init();
     auto fetch = [&](int i) {
-        if (kAsync && i < steps) {
-            const int t0 = tile_of(i) * kTile, s = (i % kStages) * kTile * W;
-            fetch_tile<V>(bx + s, x, p.xt, t0, len, c0, p.D);
-            fetch_tile<V>(bg + s, gate, p.gt, t0, len, c0, p.D);
-            fetch_tile<V>(bd + s, dh, p.ht, t0, len, c0, p.D);
+        if (kTma && threadIdx.x == 0 && i < steps) {
+            const int t0 = tile_of(i) * kTile, s = i % kStages;
+            tc::mbar_arrive_expect_tx(full + s, 2 * kTileBytes<Tx>(V) + kTileBytes<Tg>(V));
+            tma_load_3d(bx + s * kTile * W, &maps.x, c0, t0, b, full + s);
+            tma_load_3d(bg + s * kTile * W, &maps.gate, c0, t0, b, full + s);
+            tma_load_3d(bd + s * kTile * W, &maps.dh, c0, t0, b, full + s);
         }
-        if (kAsync) cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i);
-    if (kAsync) cp_async_wait<kStages - 2>();
-    __syncthreads();
+    if (kTma) {
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < kStages; ++s) tc::mbar_init(full + s, 1);
+            tc::fence_mbar_init();
+        }
+        __syncthreads();
+        for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    }
 
     for (int i = 0; i < steps; ++i) {
         const int tile = tile_of(i), t0 = tile * kTile + warp * kRun;
-        const int live = !on ? 0 : len - t0;
+        const int live = kTma || on ? len - t0 : 0;
         const int at0 = ((i % kStages) * kTile + warp * kRun) * W + lane * V;
         float start = joins && tile < tiles ? p.ckpt_in[((int64_t)b * all_tiles + tile) * p.D + c0 + ch] : 0.f;
-        float2 a[kRun], bb[kRun], xr[kAsync ? 1 : kRun] = {}, dr[kAsync ? 1 : kRun] = {};
+        float2 a[kRun], bb[kRun], xr[kTma ? 1 : kRun] = {}, dr[kTma ? 1 : kRun] = {};
         auto x_at = [&](int j) {                     // x and dh of token j: again from the tile, or kept
-            if constexpr (kAsync) return load_pair<V>(bx + at0 + j * W);
+            if constexpr (kTma) return load_pair<V>(bx + at0 + j * W);
             else return xr[j];
         };
         auto dh_at = [&](int j) {
-            if constexpr (kAsync) return load_pair<V>(bd + at0 + j * W);
+            if constexpr (kTma) return load_pair<V>(bd + at0 + j * W);
             else return dr[j];
         };
         float2 A = all2(1.f), E = all2(0.f), M = all2(0.f);
+        if (kTma) pipe.wait(i);
         with_kind(p.form, p.scale, [&](auto form, auto scale) {
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
                 float2 gv = all2(0.f);
-                if constexpr (kAsync) {
+                if constexpr (kTma) {
                     gv = load_pair<V>(bg + at0 + j * W);
                 } else {
                     xr[j] = dr[j] = all2(0.f);       // what lies behind the length is not read
@@ -431,16 +513,18 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p) {
                 }
                 decay_of<form>(gv, a[j], bb[j]);
                 if (live < kRun && j >= live) a[j] = all2(1.f), bb[j] = all2(0.f);
-                const float2 xv = x_at(j);
+                const float2 xv = j < live ? x_at(j) : all2(0.f);
                 E = fma2(a[j], E, scale == kNone ? xv : mul2(scale_of<scale>(a[j], bb[j]), xv));
                 A = mul2(A, a[j]);
             }
         });
 #pragma unroll
-        for (int j = kRun - 1; j >= 0; --j) M = mul2(a[j], add2(dh_at(j), M));
+        for (int j = kRun - 1; j >= 0; --j)
+            if (j < live) M = mul2(a[j], add2(dh_at(j), M));
         store_pair<V>(&sA[warp][lane * V], A);
         store_pair<V>(&sE[warp][lane * V], E);
         store_pair<V>(&sM[warp][lane * V], M);
+        if (kTma && lane == 0) tc::bulk_wait_read<0>();
         __syncthreads();
         fetch(i + kStages - 1);
         if (ch < W) {                                // the states before each run
@@ -450,16 +534,16 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p) {
                 start = fmaf(sA[w][ch], start, sE[w][ch]);
             }
         }
-        join_runs<V, false>(&sA[0][0], &sM[0][0], &sIn[0][0], slots + (i & 1) * R, R, rank, carry, entry);
-        if (kAsync) cp_async_wait<kStages - 2>();
+        join_runs<V, false>(&sA[0][0], &sM[0][0], &sIn[0][0], ex, pipe, i, carry, entry);
         __syncthreads();
+        const bool whole = kTma && live >= kRun;    // a whole run goes out over its own tile
         if (live > 0) {
             float2 before[kRun], state = load_pair<V>(&sH[warp][lane * V]), mu = load_pair<V>(&sIn[warp][lane * V]);
             with_kind(p.form, p.scale, [&](auto form, auto scale) {
                 float2 ds;
 #pragma unroll
                 for (int j = 0; j < kRun; ++j) {
-                    const float2 xv = x_at(j);
+                    const float2 xv = j < live ? x_at(j) : all2(0.f);
                     before[j] = state;               // h_{t-1}
                     state = fma2(a[j], state, scale == kNone ? xv : mul2(scale_of<scale>(a[j], bb[j]), xv));
                 }
@@ -467,20 +551,38 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p) {
                 Tg* og = dgate + (int64_t)(t0 + kRun - 1) * p.D;
 #pragma unroll
                 for (int j = kRun - 1; j >= 0; --j, ox -= p.D, og -= p.D) {
+                    if (j >= live) continue;
                     const float2 lam = add2(dh_at(j), mu);
                     const float2 s = scale_of<scale>(a[j], bb[j], ds);
                     float2 g = scale == kNone ? before[j] : fma2(x_at(j), ds, before[j]);
                     g = mul2(form == kDecay ? lam : mul2(lam, slope_of<form>(a[j], bb[j])), g);
                     mu = mul2(a[j], lam);
-                    if (j < live) {
+                    if (whole) {
+                        store_pair<V>(bx + at0 + j * W, scale == kNone ? lam : mul2(s, lam));
+                        store_pair<V>(bg + at0 + j * W, g);
+                    } else if (on) {
                         store_pair<V>(ox, scale == kNone ? lam : mul2(s, lam));
                         store_pair<V>(og, g);
                     }
                 }
             });
+            if (whole) {
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&maps.o0, bx + at0, c0, t0, b);
+                    tma_store_3d(&maps.o1, bg + at0, c0, t0, b);
+                    tc::bulk_commit();
+                }
+            }
         }
     }
     if (joins && p.dh0 && rank == 0) p.dh0[(int64_t)b * p.D + c0 + ch] = carry;
+    if (kTma) {
+        pipe.drain(0, steps);
+        if (lane == 0) tc::bulk_wait_read<0>();
+    }
+    if (R > 1) cluster_sync();   // no CTA leaves while another may still store to it
 }
 
 // One token for every channel: state <- a state + s x in place, h = the new state.
