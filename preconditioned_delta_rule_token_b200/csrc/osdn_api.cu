@@ -1482,8 +1482,7 @@ osdn::recur::Args recur_args(const osdn_recur_params* p) {
 }
 
 // How a call runs: channels a thread takes (two where every row of every tensor starts on such a pair),
-// whether tiles go by tensor maps (rows and widths in whole 16 bytes, no stride of 0), CTAs of a
-// cluster. `each` lists the token tensors that are read or written at the strides, with their element size.
+// and whether tiles go by tensor maps (rows and widths in whole 16 bytes, no stride of 0). `each` lists the token tensors that are read or written at the strides, with their element size.
 struct TokenPtr {
     const void* ptr;
     size_t elem;
@@ -1491,7 +1490,6 @@ struct TokenPtr {
 struct RecurPlan {
     int vec;
     bool tma;
-    int R;
 };
 RecurPlan recur_plan(const osdn_recur_params* p, const osdn::recur::Args& a, std::initializer_list<TokenPtr> each) {
     auto whole = [&](int bytes, int elems) {
@@ -1506,11 +1504,6 @@ RecurPlan recur_plan(const osdn_recur_params* p, const osdn::recur::Args& a, std
     pl.vec = whole(0, 2) ? 2 : 1;
     pl.tma = whole(16, 0) && (p->B == 1 || (a.xb && a.gb && a.hb)) && (p->T == 1 || (a.xt && a.gt && a.ht));
     for (int64_t st : {a.xb, a.xt, a.gb, a.gt, a.hb, a.ht}) pl.tma = pl.tma && st < ((int64_t)1 << 37);
-    const int64_t units = (int64_t)p->B * ((p->D + 32 * pl.vec - 1) / (32 * pl.vec));
-    const int64_t tiles = ((int64_t)p->T + osdn::recur::kTile - 1) / osdn::recur::kTile;
-    pl.R = 1;
-    static const int64_t want = getenv("RECUR_CTAS") ? atoi(getenv("RECUR_CTAS")) : 296;
-    while (pl.R < osdn::recur::kMaxCluster && units * pl.R < want && pl.R < tiles) pl.R *= 2;
     return pl;
 }
 
@@ -1545,30 +1538,63 @@ int make_rows_map(CUtensorMap* m, const void* base, const osdn_recur_params* p, 
     return OSDN_OK;
 }
 
-// Launch of `kern` in clusters of R CTAs with `smem` bytes of dynamic shared memory.
-int launch_recur(void (*kern)(osdn::recur::Args, osdn::recur::Maps), const osdn::recur::Args& a,
-                 const osdn::recur::Maps& maps, unsigned grid, int smem, int max_smem,
-                 std::atomic<uint64_t>& ready, cudaStream_t st, const char* what) {
+// What a recurrence kernel needs to know of a device: clusters of R CTAs that run at a time, 0 until asked.
+struct RecurRoom {
+    std::atomic<int> clusters[osdn::recur::kMaxCluster + 1];
+};
+
+// Launch of `kern`, with `stages` + slots(R) bytes of dynamic shared memory, on `units` walks (a sequence and
+// 32 V channels), each by a cluster of R CTAs: the most at which all clusters run at once, since the tokens
+// split over more CTAs and a second wave would wait for the first.
+int launch_recur(void (*kern)(osdn::recur::Args, osdn::recur::Maps), osdn::recur::Args& a,
+                 const osdn::recur::Maps& maps, int64_t units, int tile, int stages, int slot, RecurRoom (&room)[64],
+                 cudaStream_t st, const char* what) {
+    using osdn::recur::kMaxCluster;
     cudaError_t e;
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "current device");
-    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {   // once a device: the kernel's limits
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
-            return cuda_fail(e, what);
-        if (dev < 64) ready.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
-    }
+    if (dev < 0 || dev >= 64) return fail(OSDN_ERR_UNSUPPORTED, "device index %d above 63", dev);
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
-    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(osdn::recur::kThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = a.R;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = a.R > 1 ? 1 : 0;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    auto shape = [&](int R) {
+        cfg.dynamicSmemBytes = stages + (R > 1 ? R * slot : 0);
+        attr.val.clusterDim.x = R;
+        cfg.numAttrs = R > 1 ? 1 : 0;
+    };
+    if (!room[dev].clusters[1].load(std::memory_order_acquire)) {   // once a device: limits, then the room
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      stages + kMaxCluster * slot)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+            return cuda_fail(e, what);
+        for (int R = kMaxCluster; R >= 1; --R) {
+            int n = 0;
+            shape(R);
+            cfg.gridDim = dim3(R);
+            if (R > 1) {
+                if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return cuda_fail(e, what);
+            } else {
+                if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, osdn::recur::kThreads,
+                                                                       cfg.dynamicSmemBytes)) != cudaSuccess)
+                    return cuda_fail(e, what);
+                n = std::max(n, 1) * sm_count();
+            }
+            room[dev].clusters[R].store(n, std::memory_order_release);
+        }
+    }
+    const int64_t tiles = std::max<int64_t>(1, ((int64_t)a.T + tile - 1) / tile);
+    int R = (int)std::min<int64_t>(kMaxCluster, tiles);
+    static const int envR = getenv("RECUR_R") ? atoi(getenv("RECUR_R")) : 0;
+    if (envR) R = std::min(R, envR);
+    while (R > 1 && room[dev].clusters[R].load(std::memory_order_relaxed) < units) --R;
+    if (getenv("RECUR_V")) fprintf(stderr, "%s units %ld R %d room1 %d room2 %d room16 %d\n", what, (long)units, R, room[dev].clusters[1].load(), room[dev].clusters[2].load(), room[dev].clusters[16].load());
+    a.R = R;
+    shape(R);
+    cfg.gridDim = dim3((unsigned)(units * R));
     if ((e = cudaLaunchKernelEx(&cfg, kern, a, maps)) != cudaSuccess) return cuda_fail(e, what);
     return OSDN_OK;
 }
@@ -1580,20 +1606,18 @@ int launch_recur_fwd(const osdn_recur_params* p, osdn::recur::Args a, cudaStream
     const RecurPlan pl = recur_plan(p, a, {{a.x, ex}, {a.gate, eg}, {a.h, ex}});
     return recur_dispatch(p, pl, [&](auto v, auto as, auto tx, auto tg) {
         using namespace osdn::recur;
-        static std::atomic<uint64_t> ready{0};
+        static RecurRoom room[64];
         a.cblocks = (p->D + 32 * v - 1) / (32 * v);
-        a.R = pl.R;
         constexpr int stages = fwd_slots<v, as, decltype(tx), decltype(tg)>();
         Maps maps{};
         int rc = OSDN_OK;
         if (as && p->T > 0)
-            (void)((rc = make_rows_map(&maps.x, a.x, p, p->dtype, a.xb, a.xt, kTile)) ||
-                   (rc = make_rows_map(&maps.gate, a.gate, p, p->gate_dtype, a.gb, a.gt, kTile)) ||
-                   (a.h && (rc = make_rows_map(&maps.o0, a.h, p, p->dtype, a.hb, a.ht, kRun))));
+            (void)((rc = make_rows_map(&maps.x, a.x, p, p->dtype, a.xb, a.xt, (kWarps * fwd_run<as, decltype(tx), decltype(tg)>()))) ||
+                   (rc = make_rows_map(&maps.gate, a.gate, p, p->gate_dtype, a.gb, a.gt, (kWarps * fwd_run<as, decltype(tx), decltype(tg)>()))) ||
+                   (a.h && (rc = make_rows_map(&maps.o0, a.h, p, p->dtype, a.hb, a.ht, fwd_run<as, decltype(tx), decltype(tg)>()))));
         if (rc) return rc;
-        return launch_recur(fwd_kernel<v, as, decltype(tx), decltype(tg)>, a, maps, (unsigned)p->B * a.cblocks * a.R,
-                            stages + slot_bytes<v>(a.R), stages + slot_bytes<v>(kMaxCluster), ready, st,
-                            "recurrence launch");
+        return launch_recur(fwd_kernel<v, as, decltype(tx), decltype(tg)>, a, maps, (int64_t)p->B * a.cblocks, (kWarps * fwd_run<as, decltype(tx), decltype(tg)>()),
+                            stages, kSlotBytes, room, st, "recurrence launch");
     });
 }
 
@@ -1602,7 +1626,7 @@ size_t recur_ckpt_bytes(const osdn_recur_params* p) {
     return (size_t)p->B * tiles * p->D * sizeof(float);
 }
 
-static_assert(osdn::recur::kTile == OSDN_RECUR_CHECKPOINT, "a saved state before each tile");
+static_assert(osdn::recur::kSaved == OSDN_RECUR_CHECKPOINT, "a saved state before each tile");
 
 }  // namespace
 
@@ -1672,23 +1696,21 @@ int osdn_recur_bwd(const osdn_recur_params* p, const void* x, const void* gate, 
     const RecurPlan pl = recur_plan(p, a, {{x, ex}, {gate, eg}, {dh, ex}});
     return recur_dispatch(p, pl, [&](auto v, auto as, auto tx, auto tg) {
         using namespace osdn::recur;
-        static std::atomic<uint64_t> ready{0};
+        static RecurRoom room[64];
         a.cblocks = (p->D + 32 * v - 1) / (32 * v);
-        a.R = pl.R;
         constexpr int stages = bwd_slots<v, as, decltype(tx), decltype(tg)>();
         Maps maps{};
         int rc = OSDN_OK;
         const int64_t db = p->B > 1 ? (int64_t)p->T * p->D : 0, dt = p->T > 1 ? p->D : 0;
         if (as && p->T > 0)
-            (void)((rc = make_rows_map(&maps.x, x, p, p->dtype, a.xb, a.xt, kTile)) ||
-                   (rc = make_rows_map(&maps.gate, gate, p, p->gate_dtype, a.gb, a.gt, kTile)) ||
-                   (rc = make_rows_map(&maps.dh, dh, p, p->dtype, a.hb, a.ht, kTile)) ||
-                   (rc = make_rows_map(&maps.o0, dx, p, p->dtype, db, dt, kRun)) ||
-                   (rc = make_rows_map(&maps.o1, dgate, p, p->gate_dtype, db, dt, kRun)));
+            (void)((rc = make_rows_map(&maps.x, x, p, p->dtype, a.xb, a.xt, kWarps * kBwdRun)) ||
+                   (rc = make_rows_map(&maps.gate, gate, p, p->gate_dtype, a.gb, a.gt, kWarps * kBwdRun)) ||
+                   (rc = make_rows_map(&maps.dh, dh, p, p->dtype, a.hb, a.ht, kWarps * kBwdRun)) ||
+                   (rc = make_rows_map(&maps.o0, dx, p, p->dtype, db, dt, kBwdRun)) ||
+                   (rc = make_rows_map(&maps.o1, dgate, p, p->gate_dtype, db, dt, kBwdRun)));
         if (rc) return rc;
-        return launch_recur(bwd_kernel<v, as, decltype(tx), decltype(tg)>, a, maps, (unsigned)p->B * a.cblocks * a.R,
-                            stages + slot_bytes<v>(a.R), stages + slot_bytes<v>(kMaxCluster), ready, st,
-                            "recurrence backward launch");
+        return launch_recur(bwd_kernel<v, as, decltype(tx), decltype(tg)>, a, maps, (int64_t)p->B * a.cblocks, kWarps * kBwdRun,
+                            stages, kSlotBytes, room, st, "recurrence backward launch");
     });
 }
 

@@ -20,10 +20,14 @@ namespace recur {
 enum GateForm : int { kDecay = 0, kLog = 1, kLogit = 2 };      // a = g, exp(g), 1 / (1 + exp(-g))
 enum InputScale : int { kNone = 0, kComplement = 1, kNorm = 2 };  // s = 1, 1 - a, sqrt(1 - a^2)
 
-constexpr int kWarps = 8;               // runs of one tile
-constexpr int kRun = 8;                 // tokens of one run, held in registers
-constexpr int kTile = kWarps * kRun;    // 64: also the distance of the saved states
+constexpr int kSaved = 64;              // tokens between the saved states
+constexpr int kWarps = 8;               // runs of one tile, a warp each
 constexpr int kThreads = 32 * kWarps;
+// Tokens of one run, held in registers (forward, backward). More of them join fewer runs.
+template <bool kTma, typename Tx, typename Tg> constexpr int fwd_run() {
+    return !kTma || sizeof(Tx) + sizeof(Tg) > 6 ? 8 : 16;
+}
+constexpr int kBwdRun = 8;
 
 // ---- two channels at a time: one instruction for both where sm_100a has it (fma, mul, add on f32x2)
 
@@ -70,8 +74,8 @@ __device__ __forceinline__ float rroot(float x) {
 
 // a and b = 1 - a, each without the cancellation of taking it from the other where that one is near 1:
 // a product of thousands of decays near 1 shows any bias of a single one.
-//   log:   |g| < 0.2: b = -(g + g^2/2 + ... + g^6/720), the exponential's series (the next term is below
-//          2e-8 of b), a = 1 - b; else a = 2^(g log2 e) and b = 1 - a;
+//   log:   |g| < 0.2: b = -g q(g) with q the polynomial of degree 4 that meets (e^g - 1) / g at the
+//          Chebyshev points of that range (within 3e-8 of it), a = 1 - b; else a = 2^(g log2 e), b = 1 - a;
 //   logit: with e = exp(-|g|) and m = e / (1 + e) <= 1/2, a and b are m and 1 - m by the sign of g.
 template <int kForm> __device__ __forceinline__ void decay_of(float2 g, float2& a, float2& b) {
     constexpr float kLog2e = 1.4426950408889634f;
@@ -82,10 +86,9 @@ template <int kForm> __device__ __forceinline__ void decay_of(float2 g, float2& 
         const float2 t = mul2(g, all2(kLog2e));
         const float2 la = make_float2(ex2(t.x), ex2(t.y));
         const float2 lb = less1(la);
-        float2 s = fma2(g, all2(-1.f / 720), all2(-1.f / 120));
-        s = fma2(g, s, all2(-1.f / 24));
-        s = fma2(g, s, all2(-1.f / 6));
-        s = fma2(g, s, all2(-0.5f));
+        float2 s = fma2(g, all2(-0.00834326f), all2(-0.041736159f));
+        s = fma2(g, s, all2(-0.16666657f));
+        s = fma2(g, s, all2(-0.49999931f));
         s = fma2(g, s, all2(-1.f));
         const float2 sb = mul2(g, s), sa = less1(sb);
         const bool x = fabsf(g.x) < 0.2f, y = fabsf(g.y) < 0.2f;
@@ -155,10 +158,14 @@ struct Args {
 
 // V (1 or 2) channels as a pair; the second of one channel is 0 and not stored.
 template <int V, typename T> __device__ __forceinline__ float2 load_pair(const T* p) {
-    if constexpr (V == 1) return make_float2(to_f32(*p), 0.f);
-    float o[2];
-    VecIO<2, T>::load(p, o);
-    return make_float2(o[0], o[1]);
+    if constexpr (V == 1) {
+        return make_float2(to_f32(*p), 0.f);
+    } else if constexpr (sizeof(T) == 2) {          // bf16 is the upper half of fp32
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    } else {
+        return *reinterpret_cast<const float2*>(p);
+    }
 }
 template <int V, typename T> __device__ __forceinline__ void store_pair(T* p, float2 v) {
     if constexpr (V == 1) {
@@ -177,13 +184,11 @@ __device__ __forceinline__ int length_of(const Args& p, int b) {
 
 // ---- tiles in shared memory, by the tensor memory accelerator
 
-constexpr int kStages = 3;              // tiles in flight or in use
 constexpr int kMaxCluster = 16;
 
-template <typename T> constexpr int kTileBytes(int V) { return kTile * 32 * V * (int)sizeof(T); }
+template <typename T> constexpr int kTileBytes(int V, int run) { return kWarps * run * 32 * V * (int)sizeof(T); }
 
-// Tensor maps over [B, T, D] (innermost first: channels, tokens, sequences): loads of 64 x 32 V, stores of
-// one run, 8 x 32 V.
+// Tensor maps over [B, T, D] (innermost first: channels, tokens, sequences): loads of a tile, stores of a run.
 struct Maps {
     CUtensorMap x, gate, dh;            // loads
     CUtensorMap o0, o1;                 // stores: h, or dx and dgate
@@ -205,7 +210,7 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 
 // The stages' barriers: one phase a use, waited for by every thread. A wait that passes the limit
 // sets the library's status word; later waits of that thread are then skipped, so the kernel still ends.
-struct Pipe {
+template <int kStages> struct Pipe {
     uint64_t* full;                     // [kStages]
     unsigned long long limit_ns;
     bool failed;
@@ -234,13 +239,12 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// What the CTAs of a cluster tell one another each step: (product, end from 0) of their tile, a pair a
-// channel, stored into every CTA's slots with the bytes counted on that CTA's barrier, so a step needs no
-// fence and only the joining threads wait. Two sets by the step's parity: a CTA sends for step i + 2 after it
-// has step i + 1 from all, and they sent that after reading step i.
-template <int V> struct Exchange {
-    static constexpr int W = 32 * V;
-    float2 (*slots)[W];                 // [2][R][W]
+// What the CTAs of a cluster tell one another each step: (product, end from 0) of their tile for a lane's two
+// channels, stored into every CTA's slots with the bytes counted on that CTA's barrier, so a step needs no
+// fence. Two sets by the step's parity: a CTA sends for step i + 2 after all its warps have had step i + 1 from
+// every CTA, and those sent that after their warps had read step i.
+struct Exchange {
+    float4 (*slots)[32];                // [2][R]
     uint64_t* bar;                      // [2]
     int R, rank;
     __device__ __forceinline__ void init() {
@@ -252,74 +256,83 @@ template <int V> struct Exchange {
         }
         cluster_sync();
     }
-    __device__ __forceinline__ void send(int i, int ch, float2 v) {
-        if (ch == 0) tc::mbar_arrive_expect_tx(bar + (i & 1), R * W * (int)sizeof(float2));
-        float2* slot = &slots[(i & 1) * R + rank][ch];
+    __device__ __forceinline__ void send(int i, int lane, float2 a, float2 e) {   // one warp of the CTA
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar + (i & 1), R * 32 * (int)sizeof(float4));
+        const float4* slot = &slots[(i & 1) * R + rank][lane];
         for (int r = 0; r < R; ++r)
-            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
-                             at_rank(slot, r)),
-                         "f"(v.x), "f"(v.y), "r"(at_rank(bar + (i & 1), r))
-                         : "memory");
+            asm volatile(
+                "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                    at_rank(slot, r)),
+                "f"(a.x), "f"(a.y), "f"(e.x), "f"(e.y), "r"(at_rank(bar + (i & 1), r))
+                : "memory");
     }
 };
 
-// The incoming value of each run of a tile, by one thread a channel. part[w] = (product, end from 0) of
-// run w, carry = the value before the cluster's tiles; the runs and the CTAs are taken in the order
-// of the walk (kUp: first to last). Writes in[w], returns through `entry` the value before this CTA's tile and
-// updates carry to the value behind all of the cluster's tiles.
-template <int V, bool kUp>
-__device__ __forceinline__ void join_runs(const float* partA, const float* partE, float* in, Exchange<V>& ex, Pipe& pipe,
-                                          int i, float& carry, float& entry) {
-    const int ch = threadIdx.x;
-    if (ch >= 32 * V) return;
-    float A[kWarps], E[kWarps], a = 1.f, e = 0.f;
+// The value that comes into this warp's run. A[w], E[w] = (product, end from 0) of run w for the lane's
+// channels; carry = the value before the cluster's tiles, the same in every warp and CTA. Runs and CTAs are
+// taken in the order of the walk (kUp: first to last). entry = the value before this CTA's tile; carry
+// becomes the value behind all of the cluster's tiles.
+template <int V, bool kUp, typename P>
+__device__ __forceinline__ float2 join_runs(const float (*A)[32 * V], const float (*E)[32 * V], Exchange& ex, P& pipe,
+                                            int i, float2& carry, float2& entry) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float2 in = carry;
+    entry = carry;
+    if (ex.R == 1) {
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            const int w = kUp ? k : kWarps - 1 - k;
+            if (w == warp) in = carry;
+            carry = fma2(load_pair<V>(&A[w][lane * V]), carry, load_pair<V>(&E[w][lane * V]));
+        }
+        return in;
+    }
+    float2 a = all2(1.f), e = all2(0.f), pa = a, pe = e;
+    const bool sends = warp == (i & (kWarps - 1));   // in turn
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
         const int w = kUp ? k : kWarps - 1 - k;
-        A[k] = partA[w * 32 * V + ch];
-        E[k] = partE[w * 32 * V + ch];
-        e = fmaf(A[k], e, E[k]);
-        a *= A[k];
-    }
-    entry = carry;
-    if (ex.R > 1) {
-        ex.send(i, ch, make_float2(a, e));
-        pipe.wait(ex.bar + (i & 1), (i >> 1) & 1);
-        for (int k = 0; k < ex.R; ++k) {
-            const int r = kUp ? k : ex.R - 1 - k;
-            const float2 s = ex.slots[(i & 1) * ex.R + r][ch];
-            if (r == ex.rank) entry = carry;
-            carry = fmaf(s.x, carry, s.y);
+        if (w == warp) {
+            pa = a;
+            pe = e;
+            if (!sends) break;
         }
-    } else {
-        carry = fmaf(a, carry, e);
+        const float2 aw = load_pair<V>(&A[w][lane * V]);
+        e = fma2(aw, e, load_pair<V>(&E[w][lane * V]));
+        a = mul2(a, aw);
     }
-    float v = entry;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-        in[(kUp ? k : kWarps - 1 - k) * 32 * V + ch] = v;
-        v = fmaf(A[k], v, E[k]);
+    if (sends) ex.send(i, lane, a, e);
+    pipe.wait(ex.bar + (i & 1), (i >> 1) & 1);
+    for (int k = 0; k < ex.R; ++k) {
+        const int r = kUp ? k : ex.R - 1 - k;
+        const float4 s = ex.slots[(i & 1) * ex.R + r][lane];
+        if (r == ex.rank) entry = carry;
+        carry = fma2(make_float2(s.x, s.y), carry, make_float2(s.z, s.w));
     }
+    return fma2(pa, entry, pe);
 }
 
-// Dynamic shared memory: the stages (128-byte aligned), then the cluster's slots [2][R][32 V] (none for one CTA).
+// Dynamic shared memory: the stages (128-byte aligned), then the cluster's slots [2][R][32] (none for one CTA).
+template <typename Tx, typename Tg> constexpr int fwd_stages() { return sizeof(Tx) + sizeof(Tg) == 6 ? 2 : 3; }
+constexpr int kBwdStages = 3;
 template <int V, bool kTma, typename Tx, typename Tg> constexpr int fwd_slots() {
-    return kTma ? kStages * (kTileBytes<Tx>(V) + kTileBytes<Tg>(V)) : 0;
+    constexpr int run = fwd_run<kTma, Tx, Tg>();
+    return kTma ? fwd_stages<Tx, Tg>() * (kTileBytes<Tx>(V, run) + kTileBytes<Tg>(V, run)) : 0;
 }
 template <int V, bool kTma, typename Tx, typename Tg> constexpr int bwd_slots() {
-    return kTma ? kStages * (2 * kTileBytes<Tx>(V) + kTileBytes<Tg>(V)) : 0;
+    return kTma ? kBwdStages * (2 * kTileBytes<Tx>(V, kBwdRun) + kTileBytes<Tg>(V, kBwdRun)) : 0;
 }
-template <int V> constexpr int slot_bytes(int R) { return R > 1 ? 2 * R * 32 * V * (int)sizeof(float2) : 0; }
+constexpr int kSlotBytes = 2 * 32 * (int)sizeof(float4);   // each CTA's
 
 // A cluster of R CTAs walks one sequence and 32 V channels, R tiles at a time.
 template <int V, bool kTma, typename Tx, typename Tg>
-__global__ void __launch_bounds__(kThreads, kTma ? 3 : 2) fwd_kernel(const Args p, const __grid_constant__ Maps maps) {
-    constexpr int W = 32 * V;
+__global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const Args p, const __grid_constant__ Maps maps) {
+    constexpr int W = 32 * V, kRun = fwd_run<kTma, Tx, Tg>(), kStages = fwd_stages<Tx, Tg>(), kTile = kWarps * kRun;
     extern __shared__ __align__(128) char dyn[];
     Tx* bx = reinterpret_cast<Tx*>(dyn);                                        // [kStages][kTile][W]
-    Tg* bg = reinterpret_cast<Tg*>(dyn + kStages * kTileBytes<Tx>(V));
-    auto slots = reinterpret_cast<float2(*)[W]>(dyn + fwd_slots<V, kTma, Tx, Tg>());   // [2][R][W]
-    __shared__ float sA[kWarps][W], sE[kWarps][W], sIn[kWarps][W];
+    Tg* bg = reinterpret_cast<Tg*>(dyn + kStages * kTileBytes<Tx>(V, kRun));
+    auto slots = reinterpret_cast<float4(*)[32]>(dyn + fwd_slots<V, kTma, Tx, Tg>());   // [2][R]
+    __shared__ float sA[2][kWarps][W], sE[2][kWarps][W];   // by the step's parity
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
     const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * V;
@@ -328,22 +341,21 @@ __global__ void __launch_bounds__(kThreads, kTma ? 3 : 2) fwd_kernel(const Args 
     const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c0;
     const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c0;
     Tx* h = p.h ? static_cast<Tx*>(p.h) + b * p.hb + c : nullptr;
-    const int tiles = (len + kTile - 1) / kTile, all_tiles = (p.T + kTile - 1) / kTile;
+    const int tiles = (len + kTile - 1) / kTile, saved = (p.T + kSaved - 1) / kSaved;
     const int steps = (tiles + R - 1) / R;
 
-    const int ch = threadIdx.x;                     // channel whose runs this thread joins
-    const bool joins = ch < W && c0 + ch < p.D;
-    float carry = joins && p.h0 ? p.h0[(int64_t)b * p.D + c0 + ch] : 0.f, entry = 0.f;
+    float2 carry = all2(0.f), entry;
+    if (on && p.h0) carry = load_pair<V>(p.h0 + (int64_t)b * p.D + c);
 
     __shared__ uint64_t full[kStages];
-    Pipe pipe{full, p.wait_limit_ns, false};
+    Pipe<kStages> pipe{full, p.wait_limit_ns, false};
     __shared__ uint64_t joined[2];
-    Exchange<V> ex{slots, joined, R, rank};
+    Exchange ex{slots, joined, R, rank};
     ex.init();
     auto fetch = [&](int i) {                       // starts the copies of this CTA's i-th tile (thread 0)
         if (kTma && threadIdx.x == 0 && i < steps) {
             const int t0 = (i * R + rank) * kTile, s = i % kStages;
-            tc::mbar_arrive_expect_tx(full + s, kTileBytes<Tx>(V) + kTileBytes<Tg>(V));
+            tc::mbar_arrive_expect_tx(full + s, kTileBytes<Tx>(V, kRun) + kTileBytes<Tg>(V, kRun));
             tma_load_3d(bx + s * kTile * W, &maps.x, c0, t0, b, full + s);
             tma_load_3d(bg + s * kTile * W, &maps.gate, c0, t0, b, full + s);
         }
@@ -389,17 +401,15 @@ __global__ void __launch_bounds__(kThreads, kTma ? 3 : 2) fwd_kernel(const Args 
             H[j] = fma2(P[j], H[j - 1], H[j]);
             P[j] = mul2(P[j], P[j - 1]);
         }
-        store_pair<V>(&sA[warp][lane * V], P[kRun - 1]);
-        store_pair<V>(&sE[warp][lane * V], H[kRun - 1]);
+        store_pair<V>(&sA[i & 1][warp][lane * V], P[kRun - 1]);
+        store_pair<V>(&sE[i & 1][warp][lane * V], H[kRun - 1]);
         if (kTma && lane == 0) tc::bulk_wait_read<0>();   // the last tile has left: its stage is free
         __syncthreads();
         fetch(i + kStages - 1);
-        join_runs<V, true>(&sA[0][0], &sE[0][0], &sIn[0][0], ex, pipe, i, carry, entry);
-        if (joins && p.ckpt && i * R + rank < tiles)
-            p.ckpt[((int64_t)b * all_tiles + i * R + rank) * p.D + c0 + ch] = entry;
-        __syncthreads();
+        const float2 hin = join_runs<V, true>(sA[i & 1], sE[i & 1], ex, pipe, i, carry, entry);
+        if (warp % (kSaved / kRun) == 0 && on && p.ckpt && t0 < len)
+            store_pair<V>(p.ckpt + ((int64_t)b * saved + t0 / kSaved) * p.D + c, hin);
         if (kTma && h && live >= kRun) {            // a whole run: over its own x in the tile, and out from there
-            const float2 hin = load_pair<V>(&sIn[warp][lane * V]);
 #pragma unroll
             for (int j = 0; j < kRun; ++j) store_pair<V>(bx + at0 + j * W, fma2(P[j], hin, H[j]));
             tc::fence_proxy_async_smem();
@@ -409,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, kTma ? 3 : 2) fwd_kernel(const Args 
                 tc::bulk_commit();
             }
         } else if (h && on && live > 0) {
-            const float2 hin = load_pair<V>(&sIn[warp][lane * V]);
             Tx* o = h + t0 * p.ht;
             if (live >= kRun) {
 #pragma unroll
@@ -421,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, kTma ? 3 : 2) fwd_kernel(const Args 
             }
         }
     }
-    if (joins && p.final_h && rank == 0) p.final_h[(int64_t)b * p.D + c0 + ch] = carry;
+    if (warp == 0 && on && p.final_h && rank == 0) store_pair<V>(p.final_h + (int64_t)b * p.D + c, carry);
     if (kTma) {
         pipe.drain(0, steps);
         if (lane == 0) tc::bulk_wait_read<0>();
@@ -433,13 +442,13 @@ __global__ void __launch_bounds__(kThreads, kTma ? 3 : 2) fwd_kernel(const Args 
 // states h_{t-1} are run again from the state that the forward saved at the tile's start.
 template <int V, bool kTma, typename Tx, typename Tg>
 __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __grid_constant__ Maps maps) {
-    constexpr int W = 32 * V;
+    constexpr int W = 32 * V, kRun = kBwdRun, kStages = kBwdStages, kTile = kWarps * kRun;
     extern __shared__ __align__(128) char dyn[];
     Tx* bx = reinterpret_cast<Tx*>(dyn);                                        // [kStages][kTile][W]
-    Tx* bd = reinterpret_cast<Tx*>(dyn + kStages * kTileBytes<Tx>(V));
-    Tg* bg = reinterpret_cast<Tg*>(dyn + 2 * kStages * kTileBytes<Tx>(V));
-    auto slots = reinterpret_cast<float2(*)[W]>(dyn + bwd_slots<V, kTma, Tx, Tg>());   // [2][R][W]
-    __shared__ float sA[kWarps][W], sE[kWarps][W], sM[kWarps][W], sH[kWarps][W], sIn[kWarps][W];
+    Tx* bd = reinterpret_cast<Tx*>(dyn + kStages * kTileBytes<Tx>(V, kRun));
+    Tg* bg = reinterpret_cast<Tg*>(dyn + 2 * kStages * kTileBytes<Tx>(V, kRun));
+    auto slots = reinterpret_cast<float4(*)[32]>(dyn + bwd_slots<V, kTma, Tx, Tg>());   // [2][R]
+    __shared__ float sA[2][kWarps][W], sE[2][kWarps][W], sM[2][kWarps][W];   // by the step's parity
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
     const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * V;
@@ -451,22 +460,22 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __
     Tx* dx = static_cast<Tx*>(p.dx) + (int64_t)b * p.T * p.D + c;
     Tg* dgate = static_cast<Tg*>(p.dgate) + (int64_t)b * p.T * p.D + c;
     const int tiles = (len + kTile - 1) / kTile, all_tiles = (p.T + kTile - 1) / kTile;
+    static_assert(kTile == kSaved, "a saved state before each tile");
     const int steps = (tiles + R - 1) / R;
 
-    const int ch = threadIdx.x;
-    const bool joins = ch < W && c0 + ch < p.D;
-    float carry = joins && p.dfinal ? p.dfinal[(int64_t)b * p.D + c0 + ch] : 0.f, entry = 0.f;
+    float2 carry = all2(0.f), entry;
+    if (on && p.dfinal) carry = load_pair<V>(p.dfinal + (int64_t)b * p.D + c);
     auto tile_of = [&](int i) { return (steps - 1 - i) * R + rank; };
 
     __shared__ uint64_t full[kStages];
-    Pipe pipe{full, p.wait_limit_ns, false};
+    Pipe<kStages> pipe{full, p.wait_limit_ns, false};
     __shared__ uint64_t joined[2];
-    Exchange<V> ex{slots, joined, R, rank};
+    Exchange ex{slots, joined, R, rank};
     ex.init();
     auto fetch = [&](int i) {
         if (kTma && threadIdx.x == 0 && i < steps) {
             const int t0 = tile_of(i) * kTile, s = i % kStages;
-            tc::mbar_arrive_expect_tx(full + s, 2 * kTileBytes<Tx>(V) + kTileBytes<Tg>(V));
+            tc::mbar_arrive_expect_tx(full + s, 2 * kTileBytes<Tx>(V, kRun) + kTileBytes<Tg>(V, kRun));
             tma_load_3d(bx + s * kTile * W, &maps.x, c0, t0, b, full + s);
             tma_load_3d(bg + s * kTile * W, &maps.gate, c0, t0, b, full + s);
             tma_load_3d(bd + s * kTile * W, &maps.dh, c0, t0, b, full + s);
@@ -481,11 +490,18 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __
         for (int i = 0; i < kStages - 1; ++i) fetch(i);
     }
 
+    auto saved = [&](int i) {                        // the state before the CTA's i-th tile
+        const int tile = tile_of(i);
+        return on && i < steps && tile < tiles
+                   ? load_pair<V>(p.ckpt_in + ((int64_t)b * all_tiles + tile) * p.D + c)
+                   : all2(0.f);
+    };
+    float2 next = saved(0);
     for (int i = 0; i < steps; ++i) {
-        const int tile = tile_of(i), t0 = tile * kTile + warp * kRun;
+        const int t0 = tile_of(i) * kTile + warp * kRun;
         const int live = kTma || on ? len - t0 : 0;
         const int at0 = ((i % kStages) * kTile + warp * kRun) * W + lane * V;
-        float start = joins && tile < tiles ? p.ckpt_in[((int64_t)b * all_tiles + tile) * p.D + c0 + ch] : 0.f;
+        float2 state = next;                         // before the tile, then before this run
         float2 a[kRun], bb[kRun], xr[kTma ? 1 : kRun] = {}, dr[kTma ? 1 : kRun] = {};
         auto x_at = [&](int j) {                     // x and dh of token j: again from the tile, or kept
             if constexpr (kTma) return load_pair<V>(bx + at0 + j * W);
@@ -496,77 +512,85 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __
             else return dr[j];
         };
         float2 A = all2(1.f), E = all2(0.f), M = all2(0.f);
-        if (kTma) pipe.wait(i);
+        if (kTma) {
+            pipe.wait(i);
+            if (live < kRun) {                       // whatever lies behind the length counts as zeros
+#pragma unroll
+                for (int j = 0; j < kRun; ++j)
+                    if (j >= live) {
+                        store_pair<V>(bx + at0 + j * W, all2(0.f));
+                        store_pair<V>(bd + at0 + j * W, all2(0.f));
+                        store_pair<V>(bg + at0 + j * W, all2(0.f));
+                    }
+            }
+        }
         with_kind(p.form, p.scale, [&](auto form, auto scale) {
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
                 float2 gv = all2(0.f);
                 if constexpr (kTma) {
                     gv = load_pair<V>(bg + at0 + j * W);
-                } else {
-                    xr[j] = dr[j] = all2(0.f);       // what lies behind the length is not read
-                    if (j < live) {
-                        xr[j] = load_pair<V>(x + lane * V + (t0 + j) * p.xt);
-                        gv = load_pair<V>(gate + lane * V + (t0 + j) * p.gt);
-                        dr[j] = load_pair<V>(dh + lane * V + (t0 + j) * p.ht);
-                    }
+                } else if (j < live) {
+                    xr[j] = load_pair<V>(x + lane * V + (t0 + j) * p.xt);
+                    gv = load_pair<V>(gate + lane * V + (t0 + j) * p.gt);
+                    dr[j] = load_pair<V>(dh + lane * V + (t0 + j) * p.ht);
                 }
                 decay_of<form>(gv, a[j], bb[j]);
-                if (live < kRun && j >= live) a[j] = all2(1.f), bb[j] = all2(0.f);
-                const float2 xv = j < live ? x_at(j) : all2(0.f);
+                if (!kTma && j >= live) a[j] = all2(1.f);
+            }
+            if (kTma && live < kRun) {
+#pragma unroll
+                for (int j = 0; j < kRun; ++j)
+                    if (j >= live) a[j] = all2(1.f);
+            }
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) {
+                const float2 xv = x_at(j);
                 E = fma2(a[j], E, scale == kNone ? xv : mul2(scale_of<scale>(a[j], bb[j]), xv));
                 A = mul2(A, a[j]);
             }
         });
 #pragma unroll
-        for (int j = kRun - 1; j >= 0; --j)
-            if (j < live) M = mul2(a[j], add2(dh_at(j), M));
-        store_pair<V>(&sA[warp][lane * V], A);
-        store_pair<V>(&sE[warp][lane * V], E);
-        store_pair<V>(&sM[warp][lane * V], M);
+        for (int j = kRun - 1; j >= 0; --j) M = mul2(a[j], add2(dh_at(j), M));
+        store_pair<V>(&sA[i & 1][warp][lane * V], A);
+        store_pair<V>(&sE[i & 1][warp][lane * V], E);
+        store_pair<V>(&sM[i & 1][warp][lane * V], M);
         if (kTma && lane == 0) tc::bulk_wait_read<0>();
         __syncthreads();
         fetch(i + kStages - 1);
-        if (ch < W) {                                // the states before each run
+        next = saved(i + 1);
+        float2 mu = join_runs<V, false>(sA[i & 1], sM[i & 1], ex, pipe, i, carry, entry);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                sH[w][ch] = start;
-                start = fmaf(sA[w][ch], start, sE[w][ch]);
-            }
-        }
-        join_runs<V, false>(&sA[0][0], &sM[0][0], &sIn[0][0], ex, pipe, i, carry, entry);
-        __syncthreads();
-        const bool whole = kTma && live >= kRun;    // a whole run goes out over its own tile
+        for (int w = 0; w < kWarps - 1; ++w)
+            if (w < warp) state = fma2(load_pair<V>(&sA[i & 1][w][lane * V]), state, load_pair<V>(&sE[i & 1][w][lane * V]));
         if (live > 0) {
-            float2 before[kRun], state = load_pair<V>(&sH[warp][lane * V]), mu = load_pair<V>(&sIn[warp][lane * V]);
+            float2 lam[kRun];
+#pragma unroll
+            for (int j = kRun - 1; j >= 0; --j) {
+                lam[j] = add2(dh_at(j), mu);
+                mu = mul2(a[j], lam[j]);
+            }
+            Tx* ox = dx + (int64_t)t0 * p.D;
+            Tg* og = dgate + (int64_t)t0 * p.D;
             with_kind(p.form, p.scale, [&](auto form, auto scale) {
-                float2 ds;
 #pragma unroll
-                for (int j = 0; j < kRun; ++j) {
-                    const float2 xv = j < live ? x_at(j) : all2(0.f);
-                    before[j] = state;               // h_{t-1}
-                    state = fma2(a[j], state, scale == kNone ? xv : mul2(scale_of<scale>(a[j], bb[j]), xv));
-                }
-                Tx* ox = dx + (int64_t)(t0 + kRun - 1) * p.D;
-                Tg* og = dgate + (int64_t)(t0 + kRun - 1) * p.D;
-#pragma unroll
-                for (int j = kRun - 1; j >= 0; --j, ox -= p.D, og -= p.D) {
-                    if (j >= live) continue;
-                    const float2 lam = add2(dh_at(j), mu);
-                    const float2 s = scale_of<scale>(a[j], bb[j], ds);
-                    float2 g = scale == kNone ? before[j] : fma2(x_at(j), ds, before[j]);
-                    g = mul2(form == kDecay ? lam : mul2(lam, slope_of<form>(a[j], bb[j])), g);
-                    mu = mul2(a[j], lam);
-                    if (whole) {
-                        store_pair<V>(bx + at0 + j * W, scale == kNone ? lam : mul2(s, lam));
+                for (int j = 0; j < kRun; ++j, ox += p.D, og += p.D) {
+                    float2 ds;
+                    const float2 xv = x_at(j), s = scale_of<scale>(a[j], bb[j], ds);
+                    float2 g = scale == kNone ? state : fma2(xv, ds, state);   // state: h_{t-1}
+                    g = mul2(form == kDecay ? lam[j] : mul2(lam[j], slope_of<form>(a[j], bb[j])), g);
+                    state = fma2(a[j], state, scale == kNone ? xv : mul2(s, xv));
+                    const float2 d = scale == kNone ? lam[j] : mul2(s, lam[j]);
+                    if (kTma) {                      // over their own tiles, and out from there
+                        store_pair<V>(bx + at0 + j * W, d);
                         store_pair<V>(bg + at0 + j * W, g);
-                    } else if (on) {
-                        store_pair<V>(ox, scale == kNone ? lam : mul2(s, lam));
+                    } else if (j < live) {
+                        store_pair<V>(ox, d);
                         store_pair<V>(og, g);
                     }
                 }
             });
-            if (whole) {
+            if (kTma && live >= kRun) {
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -574,10 +598,17 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __
                     tma_store_3d(&maps.o1, bg + at0, c0, t0, b);
                     tc::bulk_commit();
                 }
+            } else if (kTma && on) {
+                ox = dx + (int64_t)t0 * p.D;
+                og = dgate + (int64_t)t0 * p.D;
+                for (int j = 0; j < live; ++j, ox += p.D, og += p.D) {
+                    store_pair<V>(ox, load_pair<V>(bx + at0 + j * W));
+                    store_pair<V>(og, load_pair<V>(bg + at0 + j * W));
+                }
             }
         }
     }
-    if (joins && p.dh0 && rank == 0) p.dh0[(int64_t)b * p.D + c0 + ch] = carry;
+    if (warp == 0 && on && p.dh0 && rank == 0) store_pair<V>(p.dh0 + (int64_t)b * p.D + c, carry);
     if (kTma) {
         pipe.drain(0, steps);
         if (lane == 0) tc::bulk_wait_read<0>();
