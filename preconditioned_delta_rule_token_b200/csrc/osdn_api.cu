@@ -1481,43 +1481,39 @@ osdn::recur::Args recur_args(const osdn_recur_params* p) {
     return a;
 }
 
-// How a call runs: channels a thread takes (two where every row of every tensor starts on such a pair),
-// and whether tiles go by tensor maps (rows and widths in whole 16 bytes, no stride of 0). `each` lists the token tensors that are read or written at the strides, with their element size.
+// How the tokens of a call reach the tiles. `each` lists the token tensors that are read or written at
+// the strides, with their element size; dense outputs follow D.
 struct TokenPtr {
     const void* ptr;
     size_t elem;
 };
-struct RecurPlan {
-    int vec;
-    bool tma;
-};
-RecurPlan recur_plan(const osdn_recur_params* p, const osdn::recur::Args& a, std::initializer_list<TokenPtr> each) {
-    auto whole = [&](int bytes, int elems) {
-        const int64_t strides = a.xb | a.xt | a.gb | a.gt | a.hb | a.ht | p->D;
-        for (const TokenPtr& t : each) {
-            const int n = bytes ? bytes / (int)t.elem : elems;
-            if (strides % n || reinterpret_cast<uintptr_t>(t.ptr) % (n * t.elem)) return false;
-        }
-        return true;
-    };
-    RecurPlan pl;
-    pl.vec = whole(0, 2) ? 2 : 1;
-    pl.tma = whole(16, 0) && (p->B == 1 || (a.xb && a.gb && a.hb)) && (p->T == 1 || (a.xt && a.gt && a.ht));
-    for (int64_t st : {a.xb, a.xt, a.gb, a.gt, a.hb, a.ht}) pl.tma = pl.tma && st < ((int64_t)1 << 37);
-    return pl;
+int recur_mode(const osdn_recur_params* p, const osdn::recur::Args& a, std::initializer_list<TokenPtr> each) {
+    const int64_t strides = a.xb | a.xt | a.gb | a.gt | a.hb | a.ht | p->D;
+    bool pieces = true, words = true;
+    for (const TokenPtr& t : each) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(t.ptr);
+        pieces = pieces && at % 16 == 0 && strides % (16 / (int64_t)t.elem) == 0;
+        words = words && (t.elem == 4 || (at % 4 == 0 && strides % 2 == 0));
+    }
+    pieces = pieces && (p->B == 1 || (a.xb && a.gb && a.hb)) && (p->T == 1 || (a.xt && a.gt && a.ht));
+    for (int64_t st : {a.xb, a.xt, a.gb, a.gt, a.hb, a.ht}) pieces = pieces && st < ((int64_t)1 << 37);
+    return pieces ? osdn::recur::kTma : words ? osdn::recur::kCopies : osdn::recur::kLoads;
 }
 
-// f(V, tma, Tx, Tg) for the plan and the types as constants.
-template <typename F> int recur_dispatch(const osdn_recur_params* p, const RecurPlan& pl, F&& f) {
+// f(mode, Tx, Tg) for the mode and the types as constants.
+template <typename F> int recur_dispatch(const osdn_recur_params* p, int mode, F&& f) {
+    using namespace osdn::recur;
     using bf = __nv_bfloat16;
-    auto types = [&](auto v, auto as) {
-        if (p->dtype == OSDN_FP32) return f(v, as, float{}, float{});
-        if (p->gate_dtype == OSDN_FP32) return f(v, as, bf{}, float{});
-        return f(v, as, bf{}, bf{});
+    auto types = [&](auto m) {
+        if (p->gate_dtype == OSDN_FP32) return f(m, bf{}, float{});
+        return f(m, bf{}, bf{});
     };
-    if (pl.tma) return types(std::integral_constant<int, 2>{}, std::true_type{});
-    if (pl.vec == 2) return types(std::integral_constant<int, 2>{}, std::false_type{});
-    return types(std::integral_constant<int, 1>{}, std::false_type{});
+    if (p->dtype == OSDN_FP32)
+        return mode == kTma ? f(std::integral_constant<int, kTma>{}, float{}, float{})
+                            : f(std::integral_constant<int, kCopies>{}, float{}, float{});
+    if (mode == kTma) return types(std::integral_constant<int, kTma>{});
+    if (mode == kCopies) return types(std::integral_constant<int, kCopies>{});
+    return types(std::integral_constant<int, kLoads>{});
 }
 
 // Tensor map of [B, T, D] (a stride of 0: one sequence or token, never stepped over) with boxes of
@@ -1529,7 +1525,7 @@ int make_rows_map(CUtensorMap* m, const void* base, const osdn_recur_params* p, 
     const cuuint64_t es = elem_size(dtype);
     const cuuint64_t dims[3] = {(cuuint64_t)p->D, (cuuint64_t)p->T, (cuuint64_t)p->B};
     const cuuint64_t strides[2] = {(cuuint64_t)(st ? st : p->D) * es, (cuuint64_t)(sb ? sb : p->D) * es};
-    const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+    const cuuint32_t box[3] = {osdn::recur::W, (cuuint32_t)rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(m, dtype == OSDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
                      const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1544,7 +1540,7 @@ struct RecurRoom {
 };
 
 // Launch of `kern`, with `stages` + slots(R) bytes of dynamic shared memory, on `units` walks (a sequence and
-// 32 V channels), each by a cluster of R CTAs: the most at which all clusters run at once, since the tokens
+// 64 channels), each by a cluster of R CTAs: the most at which all clusters run at once, since the tokens
 // split over more CTAs and a second wave would wait for the first.
 int launch_recur(void (*kern)(osdn::recur::Args, osdn::recur::Maps), osdn::recur::Args& a,
                  const osdn::recur::Maps& maps, int64_t units, int tile, int stages, int slot, RecurRoom (&room)[64],
@@ -1603,20 +1599,20 @@ bool element_aligned(const void* p, size_t elem) { return reinterpret_cast<uintp
 
 int launch_recur_fwd(const osdn_recur_params* p, osdn::recur::Args a, cudaStream_t st) {
     const size_t ex = elem_size(p->dtype), eg = elem_size(p->gate_dtype);
-    const RecurPlan pl = recur_plan(p, a, {{a.x, ex}, {a.gate, eg}, {a.h, ex}});
-    return recur_dispatch(p, pl, [&](auto v, auto as, auto tx, auto tg) {
+    const int mode = recur_mode(p, a, {{a.x, ex}, {a.gate, eg}, {a.h, ex}});
+    return recur_dispatch(p, mode, [&](auto m, auto tx, auto tg) {
         using namespace osdn::recur;
         static RecurRoom room[64];
-        a.cblocks = (p->D + 32 * v - 1) / (32 * v);
-        constexpr int stages = fwd_slots<v, as, decltype(tx), decltype(tg)>();
+        a.cblocks = (p->D + W - 1) / W;
+        constexpr int stages = fwd_slots<decltype(tx), decltype(tg)>();
         Maps maps{};
         int rc = OSDN_OK;
-        if (as && p->T > 0)
-            (void)((rc = make_rows_map(&maps.x, a.x, p, p->dtype, a.xb, a.xt, (kWarps * fwd_run<as, decltype(tx), decltype(tg)>()))) ||
-                   (rc = make_rows_map(&maps.gate, a.gate, p, p->gate_dtype, a.gb, a.gt, (kWarps * fwd_run<as, decltype(tx), decltype(tg)>()))) ||
-                   (a.h && (rc = make_rows_map(&maps.o0, a.h, p, p->dtype, a.hb, a.ht, fwd_run<as, decltype(tx), decltype(tg)>()))));
+        if (m == kTma && p->T > 0)
+            (void)((rc = make_rows_map(&maps.x, a.x, p, p->dtype, a.xb, a.xt, (kWarps * fwd_run<decltype(tx), decltype(tg)>()))) ||
+                   (rc = make_rows_map(&maps.gate, a.gate, p, p->gate_dtype, a.gb, a.gt, (kWarps * fwd_run<decltype(tx), decltype(tg)>()))) ||
+                   (a.h && (rc = make_rows_map(&maps.o0, a.h, p, p->dtype, a.hb, a.ht, fwd_run<decltype(tx), decltype(tg)>()))));
         if (rc) return rc;
-        return launch_recur(fwd_kernel<v, as, decltype(tx), decltype(tg)>, a, maps, (int64_t)p->B * a.cblocks, (kWarps * fwd_run<as, decltype(tx), decltype(tg)>()),
+        return launch_recur(fwd_kernel<m, decltype(tx), decltype(tg)>, a, maps, (int64_t)p->B * a.cblocks, (kWarps * fwd_run<decltype(tx), decltype(tg)>()),
                             stages, kSlotBytes, room, st, "recurrence launch");
     });
 }
@@ -1693,23 +1689,23 @@ int osdn_recur_bwd(const osdn_recur_params* p, const void* x, const void* gate, 
         a.ckpt = nullptr;
     }
     a.dh = dh; a.dfinal = dfinal_h; a.ckpt_in = checkpoints; a.dx = dx; a.dgate = dgate; a.dh0 = dh0;
-    const RecurPlan pl = recur_plan(p, a, {{x, ex}, {gate, eg}, {dh, ex}});
-    return recur_dispatch(p, pl, [&](auto v, auto as, auto tx, auto tg) {
+    const int mode = recur_mode(p, a, {{x, ex}, {gate, eg}, {dh, ex}, {dx, ex}, {dgate, eg}});
+    return recur_dispatch(p, mode, [&](auto m, auto tx, auto tg) {
         using namespace osdn::recur;
         static RecurRoom room[64];
-        a.cblocks = (p->D + 32 * v - 1) / (32 * v);
-        constexpr int stages = bwd_slots<v, as, decltype(tx), decltype(tg)>();
+        a.cblocks = (p->D + W - 1) / W;
+        constexpr int stages = bwd_slots<decltype(tx), decltype(tg)>();
         Maps maps{};
         int rc = OSDN_OK;
         const int64_t db = p->B > 1 ? (int64_t)p->T * p->D : 0, dt = p->T > 1 ? p->D : 0;
-        if (as && p->T > 0)
+        if (m == kTma && p->T > 0)
             (void)((rc = make_rows_map(&maps.x, x, p, p->dtype, a.xb, a.xt, kWarps * kBwdRun)) ||
                    (rc = make_rows_map(&maps.gate, gate, p, p->gate_dtype, a.gb, a.gt, kWarps * kBwdRun)) ||
                    (rc = make_rows_map(&maps.dh, dh, p, p->dtype, a.hb, a.ht, kWarps * kBwdRun)) ||
                    (rc = make_rows_map(&maps.o0, dx, p, p->dtype, db, dt, kBwdRun)) ||
                    (rc = make_rows_map(&maps.o1, dgate, p, p->gate_dtype, db, dt, kBwdRun)));
         if (rc) return rc;
-        return launch_recur(bwd_kernel<v, as, decltype(tx), decltype(tg)>, a, maps, (int64_t)p->B * a.cblocks, kWarps * kBwdRun,
+        return launch_recur(bwd_kernel<m, decltype(tx), decltype(tg)>, a, maps, (int64_t)p->B * a.cblocks, kWarps * kBwdRun,
                             stages, kSlotBytes, room, st, "recurrence backward launch");
     });
 }

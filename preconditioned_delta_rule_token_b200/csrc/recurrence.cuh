@@ -23,10 +23,9 @@ enum InputScale : int { kNone = 0, kComplement = 1, kNorm = 2 };  // s = 1, 1 - 
 constexpr int kSaved = 64;              // tokens between the saved states
 constexpr int kWarps = 8;               // runs of one tile, a warp each
 constexpr int kThreads = 32 * kWarps;
+constexpr int W = 64;                   // channels of one tile, two a lane
 // Tokens of one run, held in registers (forward, backward). More of them join fewer runs.
-template <bool kTma, typename Tx, typename Tg> constexpr int fwd_run() {
-    return !kTma || sizeof(Tx) + sizeof(Tg) > 6 ? 8 : 16;
-}
+template <typename Tx, typename Tg> constexpr int fwd_run() { return sizeof(Tx) + sizeof(Tg) > 6 ? 8 : 16; }
 constexpr int kBwdRun = 8;
 
 // ---- two channels at a time: one instruction for both where sm_100a has it (fma, mul, add on f32x2)
@@ -156,23 +155,29 @@ struct Args {
     int64_t xb, xt, gb, gt, hb, ht;     // element strides of x, gate and h (or dh) over (b, t)
 };
 
-// V (1 or 2) channels as a pair; the second of one channel is 0 and not stored.
-template <int V, typename T> __device__ __forceinline__ float2 load_pair(const T* p) {
-    if constexpr (V == 1) {
-        return make_float2(to_f32(*p), 0.f);
-    } else if constexpr (sizeof(T) == 2) {          // bf16 is the upper half of fp32
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-    } else {
-        return *reinterpret_cast<const float2*>(p);
-    }
+// Two neighbouring channels, from and to addresses on whole pairs (bf16 is the upper half of fp32).
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16* p) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
-template <int V, typename T> __device__ __forceinline__ void store_pair(T* p, float2 v) {
-    if constexpr (V == 1) {
-        *p = from_f32<T>(v.x);
+__device__ __forceinline__ float2 load_pair(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+__device__ __forceinline__ void store_pair(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+
+// A lane's two channels in device memory, kStep apart: 1, from and to whole pairs, or 32, where rows may start
+// anywhere and a warp still reads and writes whole runs of them. n: how many of the two are inside the row.
+template <int kStep, typename T> __device__ __forceinline__ float2 get_pair(const T* p, int n) {
+    if constexpr (kStep == 1) return n ? load_pair(p) : all2(0.f);
+    else return make_float2(n > 0 ? to_f32(p[0]) : 0.f, n > 1 ? to_f32(p[kStep]) : 0.f);
+}
+template <int kStep, typename T> __device__ __forceinline__ void put_pair(T* p, float2 v, int n) {
+    if constexpr (kStep == 1) {
+        if (n) store_pair(p, v);
     } else {
-        const float o[2] = {v.x, v.y};
-        VecIO<2, T>::store(p, o);
+        if (n > 0) p[0] = from_f32<T>(v.x);
+        if (n > 1) p[kStep] = from_f32<T>(v.y);
     }
 }
 
@@ -182,11 +187,18 @@ __device__ __forceinline__ int length_of(const Args& p, int b) {
     return n < 0 ? 0 : n > p.T ? p.T : n;
 }
 
-// ---- tiles in shared memory, by the tensor memory accelerator
+// ---- tiles in shared memory
 
+// How tokens come into the tiles: kTma, by tensor maps, a thread a tile (rows and widths in whole 16 bytes);
+// kCopies, each thread its own pairs by asynchronous copies of 4 bytes (fp32, or bf16 on whole pairs);
+// kLoads, its own pairs by plain loads, without any ahead (bf16 rows that start inside a pair).
+enum Mode : int { kTma = 0, kCopies = 1, kLoads = 2 };
+template <int kMode, typename Tx> constexpr int channel_step() {
+    return kMode == kLoads || (kMode == kCopies && sizeof(Tx) == 4) ? 32 : 1;
+}
 constexpr int kMaxCluster = 16;
 
-template <typename T> constexpr int kTileBytes(int V, int run) { return kWarps * run * 32 * V * (int)sizeof(T); }
+template <typename T> constexpr int kTileBytes(int run) { return kWarps * run * W * (int)sizeof(T); }
 
 // Tensor maps over [B, T, D] (innermost first: channels, tokens, sequences): loads of a tile, stores of a run.
 struct Maps {
@@ -210,6 +222,35 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 
 // The stages' barriers: one phase a use, waited for by every thread. A wait that passes the limit
 // sets the library's status word; later waits of that thread are then skipped, so the kernel still ends.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool read) {   // 4 zero bytes if not read
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(read ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One thread's pair of kRun tokens into its place in the tile (rows W apart), the first `live` of them and n
+// channels; the rest are zeros and not read.
+template <int kMode, int kRun, int kStep, typename T>
+__device__ __forceinline__ void fetch_own(T* own, const T* row, int64_t stride, int live, int n) {
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        const int m = j < live ? n : 0;
+        const T* src = m ? row + j * stride : row;
+        if constexpr (kMode == kLoads) {
+            own[j * W] = m > 0 ? src[0] : from_f32<T>(0.f);
+            own[j * W + 1] = m > 1 ? src[kStep] : from_f32<T>(0.f);
+        } else if constexpr (sizeof(T) == 2) {
+            cp_async4(own + j * W, src, m > 0);
+        } else {
+            cp_async4(own + j * W, src, m > 0);
+            cp_async4(own + j * W + 1, m > 1 ? src + kStep : row, m > 1);
+        }
+    }
+}
+
 template <int kStages> struct Pipe {
     uint64_t* full;                     // [kStages]
     unsigned long long limit_ns;
@@ -272,8 +313,8 @@ struct Exchange {
 // channels; carry = the value before the cluster's tiles, the same in every warp and CTA. Runs and CTAs are
 // taken in the order of the walk (kUp: first to last). entry = the value before this CTA's tile; carry
 // becomes the value behind all of the cluster's tiles.
-template <int V, bool kUp, typename P>
-__device__ __forceinline__ float2 join_runs(const float (*A)[32 * V], const float (*E)[32 * V], Exchange& ex, P& pipe,
+template <bool kUp, typename P>
+__device__ __forceinline__ float2 join_runs(const float (*A)[W], const float (*E)[W], Exchange& ex, P& pipe,
                                             int i, float2& carry, float2& entry) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float2 in = carry;
@@ -283,7 +324,7 @@ __device__ __forceinline__ float2 join_runs(const float (*A)[32 * V], const floa
         for (int k = 0; k < kWarps; ++k) {
             const int w = kUp ? k : kWarps - 1 - k;
             if (w == warp) in = carry;
-            carry = fma2(load_pair<V>(&A[w][lane * V]), carry, load_pair<V>(&E[w][lane * V]));
+            carry = fma2(load_pair(&A[w][lane * 2]), carry, load_pair(&E[w][lane * 2]));
         }
         return in;
     }
@@ -297,8 +338,8 @@ __device__ __forceinline__ float2 join_runs(const float (*A)[32 * V], const floa
             pe = e;
             if (!sends) break;
         }
-        const float2 aw = load_pair<V>(&A[w][lane * V]);
-        e = fma2(aw, e, load_pair<V>(&E[w][lane * V]));
+        const float2 aw = load_pair(&A[w][lane * 2]);
+        e = fma2(aw, e, load_pair(&E[w][lane * 2]));
         a = mul2(a, aw);
     }
     if (sends) ex.send(i, lane, a, e);
@@ -313,80 +354,86 @@ __device__ __forceinline__ float2 join_runs(const float (*A)[32 * V], const floa
 }
 
 // Dynamic shared memory: the stages (128-byte aligned), then the cluster's slots [2][R][32] (none for one CTA).
+// Three tiles in flight or in use; two where three would leave one CTA to an SM.
 template <typename Tx, typename Tg> constexpr int fwd_stages() { return sizeof(Tx) + sizeof(Tg) == 6 ? 2 : 3; }
-constexpr int kBwdStages = 3;
-template <int V, bool kTma, typename Tx, typename Tg> constexpr int fwd_slots() {
-    constexpr int run = fwd_run<kTma, Tx, Tg>();
-    return kTma ? fwd_stages<Tx, Tg>() * (kTileBytes<Tx>(V, run) + kTileBytes<Tg>(V, run)) : 0;
+template <typename Tx, typename Tg> constexpr int bwd_stages() { return sizeof(Tx) + sizeof(Tg) == 8 ? 2 : 3; }
+template <typename Tx, typename Tg> constexpr int fwd_slots() {
+    constexpr int run = fwd_run<Tx, Tg>();
+    return fwd_stages<Tx, Tg>() * (kTileBytes<Tx>(run) + kTileBytes<Tg>(run));
 }
-template <int V, bool kTma, typename Tx, typename Tg> constexpr int bwd_slots() {
-    return kTma ? kBwdStages * (2 * kTileBytes<Tx>(V, kBwdRun) + kTileBytes<Tg>(V, kBwdRun)) : 0;
+template <typename Tx, typename Tg> constexpr int bwd_slots() {
+    return bwd_stages<Tx, Tg>() * (2 * kTileBytes<Tx>(kBwdRun) + kTileBytes<Tg>(kBwdRun));
 }
 constexpr int kSlotBytes = 2 * 32 * (int)sizeof(float4);   // each CTA's
 
-// A cluster of R CTAs walks one sequence and 32 V channels, R tiles at a time.
-template <int V, bool kTma, typename Tx, typename Tg>
+// A cluster of R CTAs walks one sequence and 64 channels, R tiles at a time.
+template <int kMode, typename Tx, typename Tg>
 __global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const Args p, const __grid_constant__ Maps maps) {
-    constexpr int W = 32 * V, kRun = fwd_run<kTma, Tx, Tg>(), kStages = fwd_stages<Tx, Tg>(), kTile = kWarps * kRun;
+    constexpr int kRun = fwd_run<Tx, Tg>(), kStages = fwd_stages<Tx, Tg>(), kTile = kWarps * kRun;
+    constexpr int kStep = channel_step<kMode, Tx>();
     extern __shared__ __align__(128) char dyn[];
     Tx* bx = reinterpret_cast<Tx*>(dyn);                                        // [kStages][kTile][W]
-    Tg* bg = reinterpret_cast<Tg*>(dyn + kStages * kTileBytes<Tx>(V, kRun));
-    auto slots = reinterpret_cast<float4(*)[32]>(dyn + fwd_slots<V, kTma, Tx, Tg>());   // [2][R]
+    Tg* bg = reinterpret_cast<Tg*>(dyn + kStages * kTileBytes<Tx>(kRun));
+    auto slots = reinterpret_cast<float4(*)[32]>(dyn + fwd_slots<Tx, Tg>());    // [2][R]
     __shared__ float sA[2][kWarps][W], sE[2][kWarps][W];   // by the step's parity
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
-    const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * V;
-    const bool on = c < p.D;
+    const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * (kStep == 1 ? 2 : 1);
+    const int n = (c < p.D) + (c + kStep < p.D);    // this lane's channels inside the row
     const int len = length_of(p, b);
-    const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c0;
-    const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c0;
+    const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c;
+    const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c;
     Tx* h = p.h ? static_cast<Tx*>(p.h) + b * p.hb + c : nullptr;
     const int tiles = (len + kTile - 1) / kTile, saved = (p.T + kSaved - 1) / kSaved;
     const int steps = (tiles + R - 1) / R;
 
     float2 carry = all2(0.f), entry;
-    if (on && p.h0) carry = load_pair<V>(p.h0 + (int64_t)b * p.D + c);
+    if (p.h0) carry = get_pair<kStep>(p.h0 + (int64_t)b * p.D + c, n);
 
     __shared__ uint64_t full[kStages];
     Pipe<kStages> pipe{full, p.wait_limit_ns, false};
     __shared__ uint64_t joined[2];
     Exchange ex{slots, joined, R, rank};
     ex.init();
-    auto fetch = [&](int i) {                       // starts the copies of this CTA's i-th tile (thread 0)
-        if (kTma && threadIdx.x == 0 && i < steps) {
-            const int t0 = (i * R + rank) * kTile, s = i % kStages;
-            tc::mbar_arrive_expect_tx(full + s, kTileBytes<Tx>(V, kRun) + kTileBytes<Tg>(V, kRun));
-            tma_load_3d(bx + s * kTile * W, &maps.x, c0, t0, b, full + s);
-            tma_load_3d(bg + s * kTile * W, &maps.gate, c0, t0, b, full + s);
+    auto fetch = [&](int i) {                       // starts the copies of this CTA's i-th tile
+        const int t0 = (i * R + rank) * kTile, s = i % kStages;
+        if constexpr (kMode == kTma) {
+            if (threadIdx.x == 0 && i < steps) {
+                tc::mbar_arrive_expect_tx(full + s, kTileBytes<Tx>(kRun) + kTileBytes<Tg>(kRun));
+                tma_load_3d(bx + s * kTile * W, &maps.x, c0, t0, b, full + s);
+                tma_load_3d(bg + s * kTile * W, &maps.gate, c0, t0, b, full + s);
+            }
+        } else {
+            if (i < steps) {
+                const int t = t0 + warp * kRun, at = (s * kTile + warp * kRun) * W + lane * 2;
+                fetch_own<kMode, kRun, kStep>(bx + at, x + t * p.xt, p.xt, len - t, n);
+                fetch_own<kMode, kRun, kStep>(bg + at, gate + t * p.gt, p.gt, len - t, n);
+            }
+            cp_async_commit();
         }
     };
-    if (kTma) {
+    if constexpr (kMode == kTma) {
         if (threadIdx.x == 0) {
             for (int s = 0; s < kStages; ++s) tc::mbar_init(full + s, 1);
             tc::fence_mbar_init();
         }
         __syncthreads();
-        for (int i = 0; i < kStages - 1; ++i) fetch(i);
     }
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
     for (int i = 0; i < steps; ++i) {
         const int t0 = (i * R + rank) * kTile + warp * kRun;
-        const int live = kTma || on ? len - t0 : 0;   // tokens of this run inside the sequence
+        const int live = len - t0;                  // tokens of this run inside the sequence
+        const int at0 = ((i % kStages) * kTile + warp * kRun) * W + lane * 2;
         float2 P[kRun], H[kRun];
-        if (kTma) pipe.wait(i);
-        const int at0 = ((i % kStages) * kTile + warp * kRun) * W + lane * V;
+        if constexpr (kMode == kTma) pipe.wait(i);
+        else cp_async_wait<kStages - 2>();
         with_kind(p.form, p.scale, [&](auto form, auto scale) {
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
-                float2 xv = all2(0.f), gv = all2(0.f), a, bb;
-                if constexpr (kTma) {
-                    xv = load_pair<V>(bx + at0 + j * W);
-                    gv = load_pair<V>(bg + at0 + j * W);
-                } else if (j < live) {
-                    xv = load_pair<V>(x + lane * V + (t0 + j) * p.xt);
-                    gv = load_pair<V>(gate + lane * V + (t0 + j) * p.gt);
-                }
-                decay_of<form>(gv, a, bb);
+                float2 a, bb;
+                const float2 xv = load_pair(bx + at0 + j * W);
+                decay_of<form>(load_pair(bg + at0 + j * W), a, bb);
                 H[j] = scale == kNone ? xv : mul2(scale_of<scale>(a, bb), xv);
                 P[j] = a;
             }
@@ -401,70 +448,69 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const Args p, const __
             H[j] = fma2(P[j], H[j - 1], H[j]);
             P[j] = mul2(P[j], P[j - 1]);
         }
-        store_pair<V>(&sA[i & 1][warp][lane * V], P[kRun - 1]);
-        store_pair<V>(&sE[i & 1][warp][lane * V], H[kRun - 1]);
-        if (kTma && lane == 0) tc::bulk_wait_read<0>();   // the last tile has left: its stage is free
+        store_pair(&sA[i & 1][warp][lane * 2], P[kRun - 1]);
+        store_pair(&sE[i & 1][warp][lane * 2], H[kRun - 1]);
+        if (kMode == kTma && lane == 0) tc::bulk_wait_read<0>();   // the last tile has left: its stage is free
         __syncthreads();
         fetch(i + kStages - 1);
-        const float2 hin = join_runs<V, true>(sA[i & 1], sE[i & 1], ex, pipe, i, carry, entry);
-        if (warp % (kSaved / kRun) == 0 && on && p.ckpt && t0 < len)
-            store_pair<V>(p.ckpt + ((int64_t)b * saved + t0 / kSaved) * p.D + c, hin);
-        if (kTma && h && live >= kRun) {            // a whole run: over its own x in the tile, and out from there
+        const float2 hin = join_runs<true>(sA[i & 1], sE[i & 1], ex, pipe, i, carry, entry);
+        if (warp % (kSaved / kRun) == 0 && p.ckpt && t0 < len)
+            put_pair<kStep>(p.ckpt + ((int64_t)b * saved + t0 / kSaved) * p.D + c, hin, n);
+        if (h && live > 0) {
+            if (kMode == kTma && live >= kRun) {    // a whole run: over its own x in the tile, and out from there
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) store_pair<V>(bx + at0 + j * W, fma2(P[j], hin, H[j]));
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                tma_store_3d(&maps.o0, bx + at0, c0, t0, b);
-                tc::bulk_commit();
-            }
-        } else if (h && on && live > 0) {
-            Tx* o = h + t0 * p.ht;
-            if (live >= kRun) {
-#pragma unroll
-                for (int j = 0; j < kRun; ++j, o += p.ht) store_pair<V>(o, fma2(P[j], hin, H[j]));
+                for (int j = 0; j < kRun; ++j) store_pair(bx + at0 + j * W, fma2(P[j], hin, H[j]));
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&maps.o0, bx + at0, c0, t0, b);
+                    tc::bulk_commit();
+                }
             } else {
+                Tx* o = h + t0 * p.ht;
 #pragma unroll
                 for (int j = 0; j < kRun; ++j, o += p.ht)
-                    if (j < live) store_pair<V>(o, fma2(P[j], hin, H[j]));
+                    if (j < live) put_pair<kStep>(o, fma2(P[j], hin, H[j]), n);
             }
         }
     }
-    if (warp == 0 && on && p.final_h && rank == 0) store_pair<V>(p.final_h + (int64_t)b * p.D + c, carry);
-    if (kTma) {
+    if (warp == 0 && rank == 0 && p.final_h) put_pair<kStep>(p.final_h + (int64_t)b * p.D + c, carry, n);
+    if constexpr (kMode == kTma) {
         pipe.drain(0, steps);
         if (lane == 0) tc::bulk_wait_read<0>();
     }
     if (R > 1) cluster_sync();   // no CTA leaves while another may still store to it
 }
 
-// A cluster of R CTAs walks the tiles of one sequence and 32 V channels from the last to the first; the
-// states h_{t-1} are run again from the state that the forward saved at the tile's start.
-template <int V, bool kTma, typename Tx, typename Tg>
+// A cluster of R CTAs walks the tiles of one sequence and 64 channels from the last to the first. A run first
+// walks back for its lam, then forward through its states h_{t-1}, which start from the state that the
+// forward saved at the tile's start, and gives dx and dgate on the way.
+template <int kMode, typename Tx, typename Tg>
 __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __grid_constant__ Maps maps) {
-    constexpr int W = 32 * V, kRun = kBwdRun, kStages = kBwdStages, kTile = kWarps * kRun;
+    constexpr int kRun = kBwdRun, kStages = bwd_stages<Tx, Tg>(), kTile = kWarps * kRun;
+    constexpr int kStep = channel_step<kMode, Tx>();
+    static_assert(kTile == kSaved, "a saved state before each tile");
     extern __shared__ __align__(128) char dyn[];
     Tx* bx = reinterpret_cast<Tx*>(dyn);                                        // [kStages][kTile][W]
-    Tx* bd = reinterpret_cast<Tx*>(dyn + kStages * kTileBytes<Tx>(V, kRun));
-    Tg* bg = reinterpret_cast<Tg*>(dyn + 2 * kStages * kTileBytes<Tx>(V, kRun));
-    auto slots = reinterpret_cast<float4(*)[32]>(dyn + bwd_slots<V, kTma, Tx, Tg>());   // [2][R]
+    Tx* bd = reinterpret_cast<Tx*>(dyn + kStages * kTileBytes<Tx>(kRun));
+    Tg* bg = reinterpret_cast<Tg*>(dyn + 2 * kStages * kTileBytes<Tx>(kRun));
+    auto slots = reinterpret_cast<float4(*)[32]>(dyn + bwd_slots<Tx, Tg>());    // [2][R]
     __shared__ float sA[2][kWarps][W], sE[2][kWarps][W], sM[2][kWarps][W];   // by the step's parity
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
-    const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * V;
-    const bool on = c < p.D;
+    const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * (kStep == 1 ? 2 : 1);
+    const int n = (c < p.D) + (c + kStep < p.D);
     const int len = length_of(p, b);
-    const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c0;
-    const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c0;
-    const Tx* dh = static_cast<const Tx*>(p.dh) + b * p.hb + c0;
+    const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c;
+    const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c;
+    const Tx* dh = static_cast<const Tx*>(p.dh) + b * p.hb + c;
     Tx* dx = static_cast<Tx*>(p.dx) + (int64_t)b * p.T * p.D + c;
     Tg* dgate = static_cast<Tg*>(p.dgate) + (int64_t)b * p.T * p.D + c;
     const int tiles = (len + kTile - 1) / kTile, all_tiles = (p.T + kTile - 1) / kTile;
-    static_assert(kTile == kSaved, "a saved state before each tile");
     const int steps = (tiles + R - 1) / R;
 
     float2 carry = all2(0.f), entry;
-    if (on && p.dfinal) carry = load_pair<V>(p.dfinal + (int64_t)b * p.D + c);
+    if (p.dfinal) carry = get_pair<kStep>(p.dfinal + (int64_t)b * p.D + c, n);
     auto tile_of = [&](int i) { return (steps - 1 - i) * R + rank; };
 
     __shared__ uint64_t full[kStages];
@@ -473,101 +519,92 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __
     Exchange ex{slots, joined, R, rank};
     ex.init();
     auto fetch = [&](int i) {
-        if (kTma && threadIdx.x == 0 && i < steps) {
-            const int t0 = tile_of(i) * kTile, s = i % kStages;
-            tc::mbar_arrive_expect_tx(full + s, 2 * kTileBytes<Tx>(V, kRun) + kTileBytes<Tg>(V, kRun));
-            tma_load_3d(bx + s * kTile * W, &maps.x, c0, t0, b, full + s);
-            tma_load_3d(bg + s * kTile * W, &maps.gate, c0, t0, b, full + s);
-            tma_load_3d(bd + s * kTile * W, &maps.dh, c0, t0, b, full + s);
+        const int t0 = tile_of(i) * kTile, s = i % kStages;
+        if constexpr (kMode == kTma) {
+            if (threadIdx.x == 0 && i < steps) {
+                tc::mbar_arrive_expect_tx(full + s, 2 * kTileBytes<Tx>(kRun) + kTileBytes<Tg>(kRun));
+                tma_load_3d(bx + s * kTile * W, &maps.x, c0, t0, b, full + s);
+                tma_load_3d(bg + s * kTile * W, &maps.gate, c0, t0, b, full + s);
+                tma_load_3d(bd + s * kTile * W, &maps.dh, c0, t0, b, full + s);
+            }
+        } else {
+            if (i < steps) {
+                const int t = t0 + warp * kRun, at = (s * kTile + warp * kRun) * W + lane * 2;
+                fetch_own<kMode, kRun, kStep>(bx + at, x + t * p.xt, p.xt, len - t, n);
+                fetch_own<kMode, kRun, kStep>(bg + at, gate + t * p.gt, p.gt, len - t, n);
+                fetch_own<kMode, kRun, kStep>(bd + at, dh + t * p.ht, p.ht, len - t, n);
+            }
+            cp_async_commit();
         }
     };
-    if (kTma) {
+    if constexpr (kMode == kTma) {
         if (threadIdx.x == 0) {
             for (int s = 0; s < kStages; ++s) tc::mbar_init(full + s, 1);
             tc::fence_mbar_init();
         }
         __syncthreads();
-        for (int i = 0; i < kStages - 1; ++i) fetch(i);
     }
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
     auto saved = [&](int i) {                        // the state before the CTA's i-th tile
         const int tile = tile_of(i);
-        return on && i < steps && tile < tiles
-                   ? load_pair<V>(p.ckpt_in + ((int64_t)b * all_tiles + tile) * p.D + c)
-                   : all2(0.f);
+        if (i >= steps || tile >= tiles) return all2(0.f);
+        return get_pair<kStep>(p.ckpt_in + ((int64_t)b * all_tiles + tile) * p.D + c, n);
     };
     float2 next = saved(0);
     for (int i = 0; i < steps; ++i) {
         const int t0 = tile_of(i) * kTile + warp * kRun;
-        const int live = kTma || on ? len - t0 : 0;
-        const int at0 = ((i % kStages) * kTile + warp * kRun) * W + lane * V;
+        const int live = len - t0;
+        const int at0 = ((i % kStages) * kTile + warp * kRun) * W + lane * 2;
         float2 state = next;                         // before the tile, then before this run
-        float2 a[kRun], bb[kRun], xr[kTma ? 1 : kRun] = {}, dr[kTma ? 1 : kRun] = {};
-        auto x_at = [&](int j) {                     // x and dh of token j: again from the tile, or kept
-            if constexpr (kTma) return load_pair<V>(bx + at0 + j * W);
-            else return xr[j];
-        };
-        auto dh_at = [&](int j) {
-            if constexpr (kTma) return load_pair<V>(bd + at0 + j * W);
-            else return dr[j];
-        };
-        float2 A = all2(1.f), E = all2(0.f), M = all2(0.f);
-        if (kTma) {
+        float2 a[kRun], bb[kRun], A = all2(1.f), E = all2(0.f), M = all2(0.f);
+        if constexpr (kMode == kTma) {
             pipe.wait(i);
             if (live < kRun) {                       // whatever lies behind the length counts as zeros
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)
                     if (j >= live) {
-                        store_pair<V>(bx + at0 + j * W, all2(0.f));
-                        store_pair<V>(bd + at0 + j * W, all2(0.f));
-                        store_pair<V>(bg + at0 + j * W, all2(0.f));
+                        store_pair(bx + at0 + j * W, all2(0.f));
+                        store_pair(bd + at0 + j * W, all2(0.f));
+                        store_pair(bg + at0 + j * W, all2(0.f));
                     }
             }
+        } else {
+            cp_async_wait<kStages - 2>();
         }
         with_kind(p.form, p.scale, [&](auto form, auto scale) {
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) {
-                float2 gv = all2(0.f);
-                if constexpr (kTma) {
-                    gv = load_pair<V>(bg + at0 + j * W);
-                } else if (j < live) {
-                    xr[j] = load_pair<V>(x + lane * V + (t0 + j) * p.xt);
-                    gv = load_pair<V>(gate + lane * V + (t0 + j) * p.gt);
-                    dr[j] = load_pair<V>(dh + lane * V + (t0 + j) * p.ht);
-                }
-                decay_of<form>(gv, a[j], bb[j]);
-                if (!kTma && j >= live) a[j] = all2(1.f);
-            }
-            if (kTma && live < kRun) {
+            for (int j = 0; j < kRun; ++j) decay_of<form>(load_pair(bg + at0 + j * W), a[j], bb[j]);
+            if (live < kRun) {
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)
                     if (j >= live) a[j] = all2(1.f);
             }
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
-                const float2 xv = x_at(j);
+                const float2 xv = load_pair(bx + at0 + j * W);
                 E = fma2(a[j], E, scale == kNone ? xv : mul2(scale_of<scale>(a[j], bb[j]), xv));
                 A = mul2(A, a[j]);
             }
         });
 #pragma unroll
-        for (int j = kRun - 1; j >= 0; --j) M = mul2(a[j], add2(dh_at(j), M));
-        store_pair<V>(&sA[i & 1][warp][lane * V], A);
-        store_pair<V>(&sE[i & 1][warp][lane * V], E);
-        store_pair<V>(&sM[i & 1][warp][lane * V], M);
-        if (kTma && lane == 0) tc::bulk_wait_read<0>();
+        for (int j = kRun - 1; j >= 0; --j) M = mul2(a[j], add2(load_pair(bd + at0 + j * W), M));
+        store_pair(&sA[i & 1][warp][lane * 2], A);
+        store_pair(&sE[i & 1][warp][lane * 2], E);
+        store_pair(&sM[i & 1][warp][lane * 2], M);
+        if (kMode == kTma && lane == 0) tc::bulk_wait_read<0>();
         __syncthreads();
         fetch(i + kStages - 1);
         next = saved(i + 1);
-        float2 mu = join_runs<V, false>(sA[i & 1], sM[i & 1], ex, pipe, i, carry, entry);
+        float2 mu = join_runs<false>(sA[i & 1], sM[i & 1], ex, pipe, i, carry, entry);
 #pragma unroll
         for (int w = 0; w < kWarps - 1; ++w)
-            if (w < warp) state = fma2(load_pair<V>(&sA[i & 1][w][lane * V]), state, load_pair<V>(&sE[i & 1][w][lane * V]));
+            if (w < warp) state = fma2(load_pair(&sA[i & 1][w][lane * 2]), state, load_pair(&sE[i & 1][w][lane * 2]));
         if (live > 0) {
             float2 lam[kRun];
 #pragma unroll
             for (int j = kRun - 1; j >= 0; --j) {
-                lam[j] = add2(dh_at(j), mu);
+                lam[j] = add2(load_pair(bd + at0 + j * W), mu);
                 mu = mul2(a[j], lam[j]);
             }
             Tx* ox = dx + (int64_t)t0 * p.D;
@@ -576,21 +613,21 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __
 #pragma unroll
                 for (int j = 0; j < kRun; ++j, ox += p.D, og += p.D) {
                     float2 ds;
-                    const float2 xv = x_at(j), s = scale_of<scale>(a[j], bb[j], ds);
+                    const float2 xv = load_pair(bx + at0 + j * W), s = scale_of<scale>(a[j], bb[j], ds);
                     float2 g = scale == kNone ? state : fma2(xv, ds, state);   // state: h_{t-1}
                     g = mul2(form == kDecay ? lam[j] : mul2(lam[j], slope_of<form>(a[j], bb[j])), g);
                     state = fma2(a[j], state, scale == kNone ? xv : mul2(s, xv));
                     const float2 d = scale == kNone ? lam[j] : mul2(s, lam[j]);
-                    if (kTma) {                      // over their own tiles, and out from there
-                        store_pair<V>(bx + at0 + j * W, d);
-                        store_pair<V>(bg + at0 + j * W, g);
+                    if (kMode == kTma) {             // over their own tiles, and out from there
+                        store_pair(bx + at0 + j * W, d);
+                        store_pair(bg + at0 + j * W, g);
                     } else if (j < live) {
-                        store_pair<V>(ox, d);
-                        store_pair<V>(og, g);
+                        put_pair<kStep>(ox, d, n);
+                        put_pair<kStep>(og, g, n);
                     }
                 }
             });
-            if (kTma && live >= kRun) {
+            if (kMode == kTma && live >= kRun) {
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -598,22 +635,22 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __
                     tma_store_3d(&maps.o1, bg + at0, c0, t0, b);
                     tc::bulk_commit();
                 }
-            } else if (kTma && on) {
+            } else if (kMode == kTma) {
                 ox = dx + (int64_t)t0 * p.D;
                 og = dgate + (int64_t)t0 * p.D;
                 for (int j = 0; j < live; ++j, ox += p.D, og += p.D) {
-                    store_pair<V>(ox, load_pair<V>(bx + at0 + j * W));
-                    store_pair<V>(og, load_pair<V>(bg + at0 + j * W));
+                    put_pair<kStep>(ox, load_pair(bx + at0 + j * W), n);
+                    put_pair<kStep>(og, load_pair(bg + at0 + j * W), n);
                 }
             }
         }
     }
-    if (warp == 0 && on && p.dh0 && rank == 0) store_pair<V>(p.dh0 + (int64_t)b * p.D + c, carry);
-    if (kTma) {
+    if (warp == 0 && rank == 0 && p.dh0) put_pair<kStep>(p.dh0 + (int64_t)b * p.D + c, carry, n);
+    if constexpr (kMode == kTma) {
         pipe.drain(0, steps);
         if (lane == 0) tc::bulk_wait_read<0>();
     }
-    if (R > 1) cluster_sync();   // no CTA leaves while another may still store to it
+    if (R > 1) cluster_sync();
 }
 
 // One token for every channel: state <- a state + s x in place, h = the new state.
