@@ -491,7 +491,7 @@ typedef struct {
     int32_t dtype;          /* osdn_dtype of q, k and their outputs and gradients */
     int32_t norm;           /* osdn_norm */
     int32_t layout;         /* osdn_rope_layout */
-    int32_t rot_dim;        /* rotated features: even, 0 (none) .. width; OSDN_ROPE_HALF: a multiple of 16 */
+    int32_t rot_dim;        /* rotated features: even, 0 (none) .. width; OSDN_ROPE_HALF: a multiple of 8 */
     float eps;              /* >= 0 */
     float amplitude;        /* factor on the rotated features (1: a pure rotation) */
     float scale_q, scale_k; /* factors on q and k */

@@ -216,7 +216,7 @@ def qk_norm(q, k, freqs=None, positions=None, norm="l2", eps=1e-6, wq=None, wk=N
     read in place). norm: "l2" (x / sqrt(sum x^2 + eps), as the delta rule wants its keys), "rms"
     (x / sqrt(mean x^2 + eps)) or "none"; wq, wk [width] fp32 multiply after it, scale_q and scale_k too.
     freqs [rot/2] fp64 (rope_frequencies; None: no rotation) turns the first rot features: pairs
-    (i, i + rot/2) for layout "half" (rot a multiple of 16), (2i, 2i+1) for "interleaved". positions
+    (i, i + rot/2) for layout "half" (rot a multiple of 8), (2i, 2i+1) for "interleaved". positions
     [B,T] int64 (None: pos0 + t). lengths [B] int32: tokens from a sequence's length on give zeros
     (rows of a given q_out, k_out stay as they were). q_out may be q, k_out may be k.
     Returns (q_out, k_out)."""

@@ -6,8 +6,8 @@
 // features and y on the rest, R turning the pairs (i, i + rot/2) or (2i, 2i+1) by
 // theta_i = position * freq_i. Backward, with g = scale (m R(-theta)) dout:
 //   dw = sum over rows of g inv x,   dx = inv (g w - x inv^2 / n <g w, x>).
-// A row lies in a group of lanes, 8 features a lane; its sums and the partner features of the
-// half layout go between the lanes by shuffles.
+// A row lies in a group of lanes, 8 features a lane, chosen so that both features of a pair are in one lane;
+// only a row's sums go between the lanes.
 #pragma once
 #include "common.cuh"
 
@@ -39,34 +39,80 @@ struct Args {
     const int* lengths;             // [B] or NULL
     long long pos0, tokens;         // tokens = B * T
     int T, width, rot, norm, layout, inverse;
+    int parts, part_rows;           // a token's rows (of q, then of k) in parts of part_rows, a warp each
     float eps, amplitude;
 };
 
-template <typename T> __device__ __forceinline__ void load8(const T* p, float* o) {
-    VecIO<4, T>::load(p, o);
-    VecIO<4, T>::load(p + 4, o + 4);
+// A lane's 8 features as four pairs (p_i, q_i) that turn together where the row is rotated: half layout,
+// two runs of 4 at offsets op and oq; interleaved, one run of 8 with its even and odd features apart.
+struct Eight {
+    float2 p[2], q[2];
+};
+__device__ __forceinline__ float low(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float high(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* o) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o[2 * i] = __uint_as_float(w[i] << 16);
-        o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+
+template <int kLayout, typename T> struct Raw;   // as loaded, not yet converted
+template <int kLayout> struct Raw<kLayout, __nv_bfloat16> {
+    uint2 a, b;
+    __device__ __forceinline__ void load(const __nv_bfloat16* row, int op, int oq) {
+        if (kLayout == kHalf) {
+            a = *reinterpret_cast<const uint2*>(row + op);
+            b = *reinterpret_cast<const uint2*>(row + oq);
+        } else {
+            const uint4 u = *reinterpret_cast<const uint4*>(row + op);
+            a = make_uint2(u.x, u.y);
+            b = make_uint2(u.z, u.w);
+        }
+    }
+    __device__ __forceinline__ void zero() { a = b = make_uint2(0, 0); }
+    __device__ __forceinline__ Eight get() const {
+        if (kLayout == kHalf)
+            return {{make_float2(low(a.x), high(a.x)), make_float2(low(a.y), high(a.y))},
+                    {make_float2(low(b.x), high(b.x)), make_float2(low(b.y), high(b.y))}};
+        return {{make_float2(low(a.x), low(a.y)), make_float2(low(b.x), low(b.y))},
+                {make_float2(high(a.x), high(a.y)), make_float2(high(b.x), high(b.y))}};
+    }
+};
+template <int kLayout> struct Raw<kLayout, float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* row, int op, int oq) {
+        a = *reinterpret_cast<const float4*>(row + op);
+        b = *reinterpret_cast<const float4*>(row + oq);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ Eight get() const {
+        if (kLayout == kHalf) return {{make_float2(a.x, a.y), make_float2(a.z, a.w)}, {make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+        return {{make_float2(a.x, a.z), make_float2(b.x, b.z)}, {make_float2(a.y, a.w), make_float2(b.y, b.w)}};
+    }
+};
+template <int kLayout> __device__ __forceinline__ void put(__nv_bfloat16* row, int op, int oq, const Eight& v) {
+    if (kLayout == kHalf) {
+        *reinterpret_cast<uint2*>(row + op) = make_uint2(pack(v.p[0].x, v.p[0].y), pack(v.p[1].x, v.p[1].y));
+        *reinterpret_cast<uint2*>(row + oq) = make_uint2(pack(v.q[0].x, v.q[0].y), pack(v.q[1].x, v.q[1].y));
+    } else {
+        *reinterpret_cast<uint4*>(row + op) = make_uint4(pack(v.p[0].x, v.q[0].x), pack(v.p[0].y, v.q[0].y),
+                                                         pack(v.p[1].x, v.q[1].x), pack(v.p[1].y, v.q[1].y));
     }
 }
-template <typename T> __device__ __forceinline__ void store8(T* p, const float* o) {
-    VecIO<4, T>::store(p, o);
-    VecIO<4, T>::store(p + 4, o + 4);
-}
-template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float* o) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        __nv_bfloat162 a = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
-        w[i] = *reinterpret_cast<uint32_t*>(&a);
+template <int kLayout> __device__ __forceinline__ void put(float* row, int op, int oq, const Eight& v) {
+    if (kLayout == kHalf) {
+        *reinterpret_cast<float4*>(row + op) = make_float4(v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y);
+        *reinterpret_cast<float4*>(row + oq) = make_float4(v.q[0].x, v.q[0].y, v.q[1].x, v.q[1].y);
+    } else {
+        *reinterpret_cast<float4*>(row + op) = make_float4(v.p[0].x, v.q[0].x, v.p[0].y, v.q[0].y);
+        *reinterpret_cast<float4*>(row + oq) = make_float4(v.p[1].x, v.q[1].x, v.p[1].y, v.q[1].y);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float dot(const Eight& a, const Eight& b) {
+    float2 t = mul2(a.p[0], b.p[0]);
+    t = fma2(a.p[1], b.p[1], t);
+    t = fma2(a.q[0], b.q[0], t);
+    t = fma2(a.q[1], b.q[1], t);
+    return t.x + t.y;
 }
 
 // Sum over the G lanes of a group (every lane of the warp takes part).
@@ -85,151 +131,194 @@ __device__ __forceinline__ float2 cos_sin(double position, double freq, float am
     return make_float2(amplitude * c, amplitude * s);
 }
 
-// Rotate the lane's 8 features y (feature e0 of the row on); cs: this token's table; sign -1 turns back.
-template <int G>
-__device__ __forceinline__ void rotate(float* y, const float2* cs, int gl, int rot, int layout, float sign) {
-    const int e0 = gl * kVec;
-    if (layout == kInterleaved) {
+// Where a lane's pairs turn: m cos and m sin of the first `turning` of its four pairs.
+struct Turn {
+    float2 c[2], s[2], ns[2];           // ns = -s
+    int turning;
+    __device__ __forceinline__ void apply(Eight& v) const {
+        if (turning == 4) {
 #pragma unroll
-        for (int i = 0; i < kVec; i += 2)
-            if (e0 + i < rot) {
-                const float2 t = cs[(e0 + i) >> 1];
-                const float a = y[i], b = y[i + 1], sn = sign * t.y;
-                y[i] = a * t.x - b * sn;
-                y[i + 1] = b * t.x + a * sn;
+            for (int i = 0; i < 2; ++i) {
+                const float2 p = fma2(v.q[i], ns[i], mul2(v.p[i], c[i])), q = fma2(v.p[i], s[i], mul2(v.q[i], c[i]));
+                v.p[i] = p;
+                v.q[i] = q;
             }
-    } else {
-        const int half = rot / (2 * kVec);          // lanes of one half
-        const bool in = gl < 2 * half, lower = gl < half;
-        const int lane = threadIdx.x & 31;
-        const int src = !in ? lane : lower ? lane + half : lane - half;
-        const float sg = lower ? -sign : sign;
-        const int f0 = lower ? e0 : e0 - rot / 2;
+        } else if (turning > 0) {       // the end of a rotated part inside the lane (interleaved)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const float other = __shfl_sync(0xffffffffu, y[i], src);
-            if (in) {
-                const float2 t = cs[f0 + i];
-                y[i] = y[i] * t.x + other * (sg * t.y);
+            for (int i = 0; i < 2; ++i) {
+                const float2 p = fma2(v.q[i], ns[i], mul2(v.p[i], c[i])), q = fma2(v.p[i], s[i], mul2(v.q[i], c[i]));
+                if (2 * i < turning) v.p[i].x = p.x, v.q[i].x = q.x;
+                if (2 * i + 1 < turning) v.p[i].y = p.y, v.q[i].y = q.y;
             }
         }
     }
-}
+};
 
-// A CTA takes kTok tokens at a time: their table of cosines, then their rows of q and of k.
-template <int G, int kTok, bool kBackward, typename Tx>
+// A warp takes one token, or one of p.parts parts of its rows: its lanes make the token's table of cosines
+// (each angle once), each lane keeps its own four for every row, and groups of G lanes take the rows, kRows
+// of them in flight.
+template <int G, int kLayout, bool kBackward, typename Tx>
 __global__ void __launch_bounds__(kThreads) heads_kernel(const Args p) {
-    extern __shared__ float2 table[];               // [kTok][rot / 2]
-    __shared__ longlong2 where[kTok];               // sequence and token of each; token -1: past a length
+    extern __shared__ float2 tables[];              // [warps][rot / 2]
     __shared__ float sums[kBackward ? kThreads * kVec : 1];
-    constexpr int kGroups = kThreads / G;
-    const int group = threadIdx.x / G, gl = threadIdx.x % G, e0 = gl * kVec;
-    const bool on = e0 < p.width;
+    constexpr int kGroups = 32 / G, kRows = kBackward ? 2 : 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / G, gl = lane % G;
+    const bool on = gl * kVec < p.width;
     const int pairs = p.rot / 2;
+    float2* table = tables + warp * pairs;
     const float n_inv = p.norm == kRms ? 1.f / (float)p.width : 1.f;
-    float dw[2][kVec];
+    // half layout: the lanes of the rotated part take 4 features of each half, the others 8 in a row
+    const bool halves = kLayout == kHalf && gl * kVec < p.rot;
+    const int op = halves ? gl * 4 : gl * kVec, oq = halves ? pairs + gl * 4 : gl * kVec + 4;
+    Turn turn;
+    turn.turning = kLayout == kHalf ? (halves ? 4 : 0) : max(0, min(4, (p.rot - gl * kVec) / 2));
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) dw[0][i] = dw[1][i] = 0.f;
+    for (int i = 0; i < 2; ++i) turn.c[i] = turn.s[i] = turn.ns[i] = all2(0.f);
+    Eight dw[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) dw[0].p[i] = dw[0].q[i] = dw[1].p[i] = dw[1].q[i] = all2(0.f);
 
-    for (long long tok0 = (long long)blockIdx.x * kTok; tok0 < p.tokens; tok0 += (long long)gridDim.x * kTok) {
-        __syncthreads();                            // the previous tokens' table has been read
-        if (threadIdx.x < kTok) {
-            const long long tok = tok0 + threadIdx.x, b = tok / p.T, t = tok - b * p.T;
-            const bool live = tok < p.tokens && (!p.lengths || t < p.lengths[b]);
-            where[threadIdx.x] = make_longlong2(b, live ? t : -1);
-        }
-        for (int i = threadIdx.x; i < kTok * pairs; i += kThreads) {
-            const long long tok = tok0 + i / pairs;
-            if (tok < p.tokens) {
-                const long long pos = p.positions ? p.positions[tok] : p.pos0 + tok % p.T;
-                table[i] = cos_sin((double)pos, p.freqs[i % pairs], p.amplitude);
+    const long long items = p.tokens * p.parts;
+    for (long long item = (long long)blockIdx.x * (kThreads / 32) + warp; item < items;
+         item += (long long)gridDim.x * (kThreads / 32)) {
+        const long long tok = item / p.parts, b = tok / p.T, t = tok - b * p.T;
+        const int part = (int)(item - tok * p.parts);
+        if (p.lengths && t >= p.lengths[b]) continue;
+        if (pairs) {
+            const double pos = (double)(p.positions ? p.positions[tok] : p.pos0 + t);
+            __syncwarp();                           // the last token's table has been read
+            for (int i = lane; i < pairs; i += 32) table[i] = cos_sin(pos, p.freqs[i], p.amplitude);
+            __syncwarp();
+            if (turn.turning) {
+                const float2* mine = table + gl * 4;
+                const int m = turn.turning - 1;
+                const float2 t0 = mine[0], t1 = mine[min(1, m)], t2 = mine[min(2, m)], t3 = mine[min(3, m)];
+                const float sg = kBackward || p.inverse ? -1.f : 1.f;
+                turn.c[0] = make_float2(t0.x, t1.x);
+                turn.c[1] = make_float2(t2.x, t3.x);
+                turn.s[0] = make_float2(sg * t0.y, sg * t1.y);
+                turn.s[1] = make_float2(sg * t2.y, sg * t3.y);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) turn.ns[i] = make_float2(-turn.s[i].x, -turn.s[i].y);
             }
         }
-        __syncthreads();
+        int first = part * p.part_rows, last = first + p.part_rows;   // of the rows of q, then of k
 #pragma unroll
         for (int sd = 0; sd < 2; ++sd) {
             const Side& s = p.side[sd];
-            const int rows = kTok * s.H;
-            float w[kVec];
+            const int h0 = max(first, 0), h1 = min(last, s.H);
+            first -= s.H;
+            last -= s.H;
+            if (h0 >= h1) continue;
+            const Tx* x = static_cast<const Tx*>(s.x) + b * s.sx.b + t * s.sx.t;
+            const Tx* dout = kBackward ? static_cast<const Tx*>(s.dout) + b * s.so.b + t * s.so.t : nullptr;
+            const Tok3& to = kBackward ? s.sd : s.so;
+            Tx* out = static_cast<Tx*>(s.out) + b * to.b + t * to.t;
+            Eight w;                                // weight times scale
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) w[i] = 1.f;
-            if (on && s.w) load8<float>(s.w + e0, w);
-            for (int r0 = 0; r0 < rows; r0 += kGroups) {   // every lane of a warp takes part in the shuffles
-                const int r = r0 + group, k = r / max(s.H, 1), head = r - k * s.H;
-                const longlong2 at = where[k < kTok ? k : 0];
-                const long long b = at.x, t = at.y;
-                const bool live = on && r < rows && t >= 0;
-                const float2* cs = table + (k < kTok ? k : 0) * pairs;
-                float x[kVec], y[kVec];
+            for (int i = 0; i < 2; ++i) w.p[i] = w.q[i] = all2(s.scale);
+            if (on && s.w) {
+                Raw<kLayout, float> r;
+                r.load(s.w, op, oq);
+                const Eight v = r.get();
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) x[i] = y[i] = 0.f;
-                if (live) load8<Tx>(static_cast<const Tx*>(s.x) + s.sx.at(b, t, head) + e0, x);
-                float inv = 1.f;
-                if (p.norm != kNoNorm) {
-                    float ss = 0.f;
+                for (int i = 0; i < 2; ++i) w.p[i] = mul2(w.p[i], v.p[i]), w.q[i] = mul2(w.q[i], v.q[i]);
+            }
+            for (int r0 = h0; r0 < h1; r0 += kGroups * kRows) {   // every lane takes part in the sums
+                Raw<kLayout, Tx> xr[kRows], dr[kBackward ? kRows : 1];
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) ss = fmaf(x[i], x[i], ss);
-                    const float m = fmaf(group_sum<G>(ss), n_inv, p.eps);
-                    inv = m > 0.f ? 1.f / sqrtf(m) : 0.f;   // a row of zeros without eps stays zero
-                }
-                if constexpr (!kBackward) {
-#pragma unroll
-                    for (int i = 0; i < kVec; ++i) y[i] = x[i] * (inv * s.scale) * w[i];
-                    if (pairs) rotate<G>(y, cs, gl, p.rot, p.layout, p.inverse ? -1.f : 1.f);
-                    if (live) store8<Tx>(static_cast<Tx*>(s.out) + s.so.at(b, t, head) + e0, y);
-                } else {
-                    if (live) load8<Tx>(static_cast<const Tx*>(s.dout) + s.so.at(b, t, head) + e0, y);
-                    if (pairs) rotate<G>(y, cs, gl, p.rot, p.layout, -1.f);
-                    float dot = 0.f;
-#pragma unroll
-                    for (int i = 0; i < kVec; ++i) {
-                        y[i] *= s.scale;
-                        dw[sd][i] = fmaf(y[i], x[i] * inv, dw[sd][i]);
-                        y[i] *= w[i];
-                        dot = fmaf(y[i], x[i], dot);
+                for (int k = 0; k < kRows; ++k) {
+                    const int head = r0 + k * kGroups + group;
+                    if (on && head < h1) {
+                        xr[k].load(x + head * s.sx.h, op, oq);
+                        if constexpr (kBackward) dr[k].load(dout + head * s.so.h, op, oq);
+                    } else {
+                        xr[k].zero();
+                        if constexpr (kBackward) dr[k].zero();
                     }
-                    dot = p.norm == kNoNorm ? 0.f : group_sum<G>(dot) * (inv * inv * n_inv);
+                }
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) y[i] = inv * fmaf(-x[i], dot, y[i]);
-                    if (live) store8<Tx>(static_cast<Tx*>(s.out) + s.sd.at(b, t, head) + e0, y);
+                for (int k = 0; k < kRows; ++k) {
+                    if (r0 + k * kGroups >= h1) break;
+                    const int head = r0 + k * kGroups + group;
+                    const Eight v = xr[k].get();
+                    float inv = 1.f;
+                    if (p.norm != kNoNorm) {
+                        const float m = fmaf(group_sum<G>(dot(v, v)), n_inv, p.eps);
+                        inv = m > 0.f ? 1.f / sqrtf(m) : 0.f;   // a row of zeros without eps stays zero
+                    }
+                    const float2 inv2 = all2(inv);
+                    Eight y;
+                    if constexpr (!kBackward) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            y.p[i] = mul2(mul2(v.p[i], inv2), w.p[i]);
+                            y.q[i] = mul2(mul2(v.q[i], inv2), w.q[i]);
+                        }
+                        turn.apply(y);
+                    } else {
+                        y = dr[k].get();
+                        turn.apply(y);
+                        if (s.dw) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                dw[sd].p[i] = fma2(y.p[i], mul2(v.p[i], inv2), dw[sd].p[i]);
+                                dw[sd].q[i] = fma2(y.q[i], mul2(v.q[i], inv2), dw[sd].q[i]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) y.p[i] = mul2(y.p[i], w.p[i]), y.q[i] = mul2(y.q[i], w.q[i]);
+                        if (p.norm != kNoNorm) {
+                            const float2 g = all2(-group_sum<G>(dot(y, v)) * (inv * inv * n_inv));
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                y.p[i] = mul2(inv2, fma2(v.p[i], g, y.p[i]));
+                                y.q[i] = mul2(inv2, fma2(v.q[i], g, y.q[i]));
+                            }
+                        }
+                    }
+                    if (on && head < h1) put<kLayout>(out + head * to.h, op, oq, y);
                 }
             }
         }
     }
-    if constexpr (kBackward) {
+    if constexpr (kBackward) {                      // this CTA's part of dw, groups and warps in order
 #pragma unroll
         for (int sd = 0; sd < 2; ++sd) {
             if (!p.side[sd].dw) continue;
             __syncthreads();
+            if (on) {
+                const float2 sc = all2(p.side[sd].scale);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) sums[group * G * kVec + e0 + i] = dw[sd][i];
+                for (int i = 0; i < 2; ++i) dw[sd].p[i] = mul2(dw[sd].p[i], sc), dw[sd].q[i] = mul2(dw[sd].q[i], sc);
+                put<kLayout>(sums + (threadIdx.x / G) * G * kVec, op, oq, dw[sd]);
+            }
             __syncthreads();
             if (threadIdx.x < p.width) {
                 float t = 0.f;
-                for (int g = 0; g < kGroups; ++g) t += sums[g * G * kVec + threadIdx.x];
+                for (int g = 0; g < kThreads / G; ++g) t += sums[g * G * kVec + threadIdx.x];
                 p.side[sd].dw[(size_t)blockIdx.x * p.width + threadIdx.x] = t;
             }
         }
     }
 }
 
-// dw of both sides from the CTAs' partial sums, in a fixed order.
-__global__ void __launch_bounds__(256) dw_kernel(const float* part_q, const float* part_k, float* dwq, float* dwk,
-                                                 int parts, int width) {
+// dw of both sides from the CTAs' partial sums, in a fixed order: a warp a share of them, then the warps.
+__global__ void __launch_bounds__(1024) dw_kernel(const float* part_q, const float* part_k, float* dwq, float* dwk,
+                                                  int parts, int width) {
     const float* part = blockIdx.y ? part_k : part_q;
     float* dw = blockIdx.y ? dwk : dwq;
     if (!dw) return;
-    __shared__ float s[8][32];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, w = threadIdx.x >> 5;
     float t = 0.f;
     if (c < width)
-        for (int i = w; i < parts; i += 8) t += part[(size_t)i * width + c];
-    s[w][threadIdx.x & 31] = t;
+#pragma unroll 4
+        for (int i = w; i < parts; i += 32) t += part[(size_t)i * width + c];
+    s[lane][w] = t;
     __syncthreads();
-    if (w == 0 && c < width) {
-        for (int i = 1; i < 8; ++i) t += s[i][threadIdx.x & 31];
-        dw[c] = t;
-    }
+    t = warp_sum(s[w][lane]);                       // channel w of the block, share by share
+    if (lane == 0 && blockIdx.x * 32 + w < width) dw[blockIdx.x * 32 + w] = t;
 }
 
 }  // namespace heads

@@ -1777,8 +1777,8 @@ int check_qk(const osdn_qk_params* p) {
         return fail(OSDN_ERR_INVALID_ARG, "unknown layout %d", p->layout);
     if (p->rot_dim < 0 || p->rot_dim > p->width || p->rot_dim % 2)
         return fail(OSDN_ERR_INVALID_ARG, "rot_dim must be even, 0 .. width (got %d)", p->rot_dim);
-    if (p->layout == OSDN_ROPE_HALF && p->rot_dim % 16)
-        return fail(OSDN_ERR_UNSUPPORTED, "the half layout takes rot_dim in multiples of 16 (got %d)", p->rot_dim);
+    if (p->layout == OSDN_ROPE_HALF && p->rot_dim % 8)
+        return fail(OSDN_ERR_UNSUPPORTED, "the half layout takes rot_dim in multiples of 8 (got %d)", p->rot_dim);
     if (!(p->eps >= 0.f)) return fail(OSDN_ERR_INVALID_ARG, "eps must be >= 0");
     if (!(std::isfinite(p->amplitude) && std::isfinite(p->scale_q) && std::isfinite(p->scale_k)))
         return fail(OSDN_ERR_INVALID_ARG, "amplitude, scale_q and scale_k must be finite");
@@ -1795,30 +1795,49 @@ int check_qk(const osdn_qk_params* p) {
     return OSDN_OK;
 }
 
-// Tokens a CTA takes at a time, and its grid: forward as many CTAs as there are such groups; the
-// backward at most four to an SM, since each leaves a row of partial weight gradients.
-int qk_tok(const osdn_qk_params* p) { return (int64_t)p->B * p->T >= 4096 ? 4 : 1; }
-unsigned qk_grid(const osdn_qk_params* p, bool backward) {
-    const int64_t tokens = (int64_t)p->B * p->T, tok = qk_tok(p), n = (tokens + tok - 1) / tok;
-    return (unsigned)(backward ? std::min<int64_t>(n, 4 * sm_count()) : n);
+// Parts of a token's rows, a warp each: enough that every SM gets 16 warps, each with at least the rows that
+// a warp has in flight at a time.
+struct QkShape {
+    int lanes, parts, part_rows;
+    unsigned grid;
+};
+QkShape qk_shape(const osdn_qk_params* p, bool backward) {
+    QkShape q;
+    q.lanes = p->width <= 64 ? 8 : p->width <= 128 ? 16 : 32;
+    const int rows = p->Hq + p->Hk, flight = 32 / q.lanes * (backward ? 2 : 4), sms = sm_count();
+    const int64_t tokens = (int64_t)p->B * p->T, warps = osdn::heads::kThreads / 32;
+    const int64_t most = (rows + flight - 1) / flight, want = tokens ? (16LL * sms + tokens - 1) / tokens : 1;
+    const int parts = (int)std::min(most, want);
+    q.part_rows = ((rows + parts - 1) / parts + flight - 1) / flight * flight;
+    q.parts = (rows + q.part_rows - 1) / q.part_rows;
+    const int64_t blocks = (tokens * q.parts + warps - 1) / warps;
+    // the backward's CTAs each leave a row of partial weight gradients: at most what runs at a time
+    q.grid = (unsigned)(backward ? std::min<int64_t>(blocks, 4 * sms) : std::min<int64_t>(blocks, 2147483647));
+    return q;
 }
 
-template <bool kBackward> int launch_heads(const osdn_qk_params* p, const osdn::heads::Args& a, cudaStream_t st) {
+template <bool kBackward> int launch_heads(const osdn_qk_params* p, osdn::heads::Args& a, cudaStream_t st) {
+    using namespace osdn::heads;
     using bf = __nv_bfloat16;
-    const int tok = qk_tok(p);
-    auto go = [&](auto g, auto k, auto tx) {
-        osdn::heads::heads_kernel<g, k, kBackward, decltype(tx)>
-            <<<qk_grid(p, kBackward), osdn::heads::kThreads, sizeof(float2) * k * (a.rot / 2), st>>>(a);
+    const QkShape q = qk_shape(p, kBackward);
+    a.parts = q.parts;
+    a.part_rows = q.part_rows;
+    auto go = [&](auto g, auto layout, auto tx) {
+        heads_kernel<g, layout, kBackward, decltype(tx)>
+            <<<q.grid, kThreads, kThreads / 32 * sizeof(float2) * (a.rot / 2), st>>>(a);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "head norm and rotation launch");
     };
-    auto types = [&](auto g, auto k) { return p->dtype == OSDN_FP32 ? go(g, k, float{}) : go(g, k, bf{}); };
-    auto toks = [&](auto g) {
-        return tok == 4 ? types(g, std::integral_constant<int, 4>{}) : types(g, std::integral_constant<int, 1>{});
+    auto types = [&](auto g, auto layout) {
+        return p->dtype == OSDN_FP32 ? go(g, layout, float{}) : go(g, layout, bf{});
     };
-    if (p->width <= 64) return toks(std::integral_constant<int, 8>{});
-    if (p->width <= 128) return toks(std::integral_constant<int, 16>{});
-    return toks(std::integral_constant<int, 32>{});
+    auto layouts = [&](auto g) {
+        return p->layout == OSDN_ROPE_HALF ? types(g, std::integral_constant<int, kHalf>{})
+                                           : types(g, std::integral_constant<int, kInterleaved>{});
+    };
+    if (q.lanes == 8) return layouts(std::integral_constant<int, 8>{});
+    if (q.lanes == 16) return layouts(std::integral_constant<int, 16>{});
+    return layouts(std::integral_constant<int, 32>{});
 }
 
 osdn::heads::Args heads_args(const osdn_qk_params* p, const int64_t* positions, const double* freqs,
@@ -1893,7 +1912,7 @@ int osdn_qk_bwd_workspace_size(const osdn_qk_params* p, size_t* bytes) {
     int rc = check_qk(p);
     if (rc) return rc;
     if (!bytes) return fail(OSDN_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = round_up((size_t)2 * qk_grid(p, true) * p->width * sizeof(float), 256);
+    *bytes = round_up((size_t)2 * qk_shape(p, true).grid * p->width * sizeof(float), 256);
     return OSDN_OK;
 }
 
@@ -1924,7 +1943,7 @@ int osdn_qk_bwd(const osdn_qk_params* p, const void* q, const void* k, const flo
                 return cuda_fail(e, "weight gradient");
         return OSDN_OK;
     }
-    const unsigned grid = qk_grid(p, true);
+    const unsigned grid = qk_shape(p, true).grid;
     const size_t part = (size_t)grid * p->width;
     float* ws = static_cast<float*>(workspace);
     if (dwq || dwk) {
@@ -1939,7 +1958,7 @@ int osdn_qk_bwd(const osdn_qk_params* p, const void* q, const void* k, const flo
     a.side[1].dw = dwk ? ws + part : nullptr;
     if ((rc = launch_heads<true>(p, a, st))) return rc;
     if (dwq || dwk) {
-        osdn::heads::dw_kernel<<<dim3((p->width + 31) / 32, 2), 256, 0, st>>>(ws, ws + part, dwq, dwk, (int)grid,
+        osdn::heads::dw_kernel<<<dim3((p->width + 31) / 32, 2), 1024, 0, st>>>(ws, ws + part, dwq, dwk, (int)grid,
                                                                               p->width);
         if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "weight gradient launch");
     }
