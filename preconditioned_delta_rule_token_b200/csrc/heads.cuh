@@ -44,7 +44,7 @@ struct Args {
 };
 
 // A lane's 8 features as four pairs (p_i, q_i) that turn together where the row is rotated: half layout,
-// two runs of 4 at offsets op and oq; interleaved, one run of 8 with its even and odd features apart.
+// two runs of 4, d apart; interleaved, one run of 8 with its even and odd features apart (d = 4).
 struct Eight {
     float2 p[2], q[2];
 };
@@ -58,12 +58,12 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 template <int kLayout, typename T> struct Raw;   // as loaded, not yet converted
 template <int kLayout> struct Raw<kLayout, __nv_bfloat16> {
     uint2 a, b;
-    __device__ __forceinline__ void load(const __nv_bfloat16* row, int op, int oq) {
+    __device__ __forceinline__ void load(const __nv_bfloat16* at, int d) {
         if (kLayout == kHalf) {
-            a = *reinterpret_cast<const uint2*>(row + op);
-            b = *reinterpret_cast<const uint2*>(row + oq);
+            a = *reinterpret_cast<const uint2*>(at);
+            b = *reinterpret_cast<const uint2*>(at + d);
         } else {
-            const uint4 u = *reinterpret_cast<const uint4*>(row + op);
+            const uint4 u = *reinterpret_cast<const uint4*>(at);
             a = make_uint2(u.x, u.y);
             b = make_uint2(u.z, u.w);
         }
@@ -79,9 +79,9 @@ template <int kLayout> struct Raw<kLayout, __nv_bfloat16> {
 };
 template <int kLayout> struct Raw<kLayout, float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float* row, int op, int oq) {
-        a = *reinterpret_cast<const float4*>(row + op);
-        b = *reinterpret_cast<const float4*>(row + oq);
+    __device__ __forceinline__ void load(const float* at, int d) {
+        a = *reinterpret_cast<const float4*>(at);
+        b = *reinterpret_cast<const float4*>(at + d);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ Eight get() const {
@@ -89,22 +89,22 @@ template <int kLayout> struct Raw<kLayout, float> {
         return {{make_float2(a.x, a.z), make_float2(b.x, b.z)}, {make_float2(a.y, a.w), make_float2(b.y, b.w)}};
     }
 };
-template <int kLayout> __device__ __forceinline__ void put(__nv_bfloat16* row, int op, int oq, const Eight& v) {
+template <int kLayout> __device__ __forceinline__ void put(__nv_bfloat16* at, int d, const Eight& v) {
     if (kLayout == kHalf) {
-        *reinterpret_cast<uint2*>(row + op) = make_uint2(pack(v.p[0].x, v.p[0].y), pack(v.p[1].x, v.p[1].y));
-        *reinterpret_cast<uint2*>(row + oq) = make_uint2(pack(v.q[0].x, v.q[0].y), pack(v.q[1].x, v.q[1].y));
+        *reinterpret_cast<uint2*>(at) = make_uint2(pack(v.p[0].x, v.p[0].y), pack(v.p[1].x, v.p[1].y));
+        *reinterpret_cast<uint2*>(at + d) = make_uint2(pack(v.q[0].x, v.q[0].y), pack(v.q[1].x, v.q[1].y));
     } else {
-        *reinterpret_cast<uint4*>(row + op) = make_uint4(pack(v.p[0].x, v.q[0].x), pack(v.p[0].y, v.q[0].y),
+        *reinterpret_cast<uint4*>(at) = make_uint4(pack(v.p[0].x, v.q[0].x), pack(v.p[0].y, v.q[0].y),
                                                          pack(v.p[1].x, v.q[1].x), pack(v.p[1].y, v.q[1].y));
     }
 }
-template <int kLayout> __device__ __forceinline__ void put(float* row, int op, int oq, const Eight& v) {
+template <int kLayout> __device__ __forceinline__ void put(float* at, int d, const Eight& v) {
     if (kLayout == kHalf) {
-        *reinterpret_cast<float4*>(row + op) = make_float4(v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y);
-        *reinterpret_cast<float4*>(row + oq) = make_float4(v.q[0].x, v.q[0].y, v.q[1].x, v.q[1].y);
+        *reinterpret_cast<float4*>(at) = make_float4(v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y);
+        *reinterpret_cast<float4*>(at + d) = make_float4(v.q[0].x, v.q[0].y, v.q[1].x, v.q[1].y);
     } else {
-        *reinterpret_cast<float4*>(row + op) = make_float4(v.p[0].x, v.q[0].x, v.p[0].y, v.q[0].y);
-        *reinterpret_cast<float4*>(row + oq) = make_float4(v.p[1].x, v.q[1].x, v.p[1].y, v.q[1].y);
+        *reinterpret_cast<float4*>(at) = make_float4(v.p[0].x, v.q[0].x, v.p[0].y, v.q[0].y);
+        *reinterpret_cast<float4*>(at + d) = make_float4(v.p[1].x, v.q[1].x, v.p[1].y, v.q[1].y);
     }
 }
 __device__ __forceinline__ float dot(const Eight& a, const Eight& b) {
@@ -158,7 +158,7 @@ struct Turn {
 // (each angle once), each lane keeps its own four for every row, and groups of G lanes take the rows, kRows
 // of them in flight.
 template <int G, int kLayout, bool kBackward, typename Tx>
-__global__ void __launch_bounds__(kThreads) heads_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) heads_kernel(const Args p) {
     extern __shared__ float2 tables[];              // [warps][rot / 2]
     __shared__ float sums[kBackward ? kThreads * kVec : 1];
     constexpr int kGroups = 32 / G, kRows = kBackward ? 2 : 4;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const Args p) {
     const float n_inv = p.norm == kRms ? 1.f / (float)p.width : 1.f;
     // half layout: the lanes of the rotated part take 4 features of each half, the others 8 in a row
     const bool halves = kLayout == kHalf && gl * kVec < p.rot;
-    const int op = halves ? gl * 4 : gl * kVec, oq = halves ? pairs + gl * 4 : gl * kVec + 4;
+    const int op = halves ? gl * 4 : gl * kVec, d = halves ? pairs : 4;
     Turn turn;
     turn.turning = kLayout == kHalf ? (halves ? 4 : 0) : max(0, min(4, (p.rot - gl * kVec) / 2));
 #pragma unroll
@@ -210,55 +210,53 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const Args p) {
             first -= s.H;
             last -= s.H;
             if (h0 >= h1) continue;
-            const Tx* x = static_cast<const Tx*>(s.x) + b * s.sx.b + t * s.sx.t;
-            const Tx* dout = kBackward ? static_cast<const Tx*>(s.dout) + b * s.so.b + t * s.so.t : nullptr;
             const Tok3& to = kBackward ? s.sd : s.so;
-            Tx* out = static_cast<Tx*>(s.out) + b * to.b + t * to.t;
-            Eight w;                                // weight times scale
+            const Tx* xp = static_cast<const Tx*>(s.x) + s.sx.at(b, t, h0 + group) + op;
+            const Tx* dp = kBackward ? static_cast<const Tx*>(s.dout) + s.so.at(b, t, h0 + group) + op : nullptr;
+            Tx* out = static_cast<Tx*>(s.out) + to.at(b, t, h0 + group) + op;
+            const int64_t xs = kGroups * s.sx.h, ds = kGroups * s.so.h, os = kGroups * to.h;
+            Eight w;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) w.p[i] = w.q[i] = all2(s.scale);
+            for (int i = 0; i < 2; ++i) w.p[i] = w.q[i] = all2(1.f);
             if (on && s.w) {
                 Raw<kLayout, float> r;
-                r.load(s.w, op, oq);
-                const Eight v = r.get();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) w.p[i] = mul2(w.p[i], v.p[i]), w.q[i] = mul2(w.q[i], v.q[i]);
+                r.load(s.w + op, d);
+                w = r.get();
             }
             for (int r0 = h0; r0 < h1; r0 += kGroups * kRows) {   // every lane takes part in the sums
+                const int left = on ? h1 - r0 - group : 0;
                 Raw<kLayout, Tx> xr[kRows], dr[kBackward ? kRows : 1];
 #pragma unroll
-                for (int k = 0; k < kRows; ++k) {
-                    const int head = r0 + k * kGroups + group;
-                    if (on && head < h1) {
-                        xr[k].load(x + head * s.sx.h, op, oq);
-                        if constexpr (kBackward) dr[k].load(dout + head * s.so.h, op, oq);
-                    } else {
-                        xr[k].zero();
-                        if constexpr (kBackward) dr[k].zero();
+                for (int k = 0; k < kRows; ++k, xp += xs) {
+                    xr[k].zero();
+                    if (k * kGroups < left) xr[k].load(xp, d);
+                    if constexpr (kBackward) {
+                        dr[k].zero();
+                        if (k * kGroups < left) dr[k].load(dp, d);
+                        dp += ds;
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < kRows; ++k) {
+                for (int k = 0; k < kRows; ++k, out += os) {
                     if (r0 + k * kGroups >= h1) break;
-                    const int head = r0 + k * kGroups + group;
                     const Eight v = xr[k].get();
                     float inv = 1.f;
                     if (p.norm != kNoNorm) {
                         const float m = fmaf(group_sum<G>(dot(v, v)), n_inv, p.eps);
-                        inv = m > 0.f ? 1.f / sqrtf(m) : 0.f;   // a row of zeros without eps stays zero
+                        inv = m > 0.f ? rroot(m) : 0.f;   // a row of zeros without eps stays zero
                     }
                     const float2 inv2 = all2(inv);
                     Eight y;
                     if constexpr (!kBackward) {
+                        const float2 f = all2(inv * s.scale);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            y.p[i] = mul2(mul2(v.p[i], inv2), w.p[i]);
-                            y.q[i] = mul2(mul2(v.q[i], inv2), w.q[i]);
-                        }
-                        turn.apply(y);
+                        for (int i = 0; i < 2; ++i) y.p[i] = mul2(v.p[i], f), y.q[i] = mul2(v.q[i], f);
                     } else {
                         y = dr[k].get();
                         turn.apply(y);
+                        const float2 f = all2(s.scale);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) y.p[i] = mul2(y.p[i], f), y.q[i] = mul2(y.q[i], f);
                         if (s.dw) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
@@ -266,18 +264,22 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const Args p) {
                                 dw[sd].q[i] = fma2(y.q[i], mul2(v.q[i], inv2), dw[sd].q[i]);
                             }
                         }
+                    }
+                    if (s.w) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) y.p[i] = mul2(y.p[i], w.p[i]), y.q[i] = mul2(y.q[i], w.q[i]);
-                        if (p.norm != kNoNorm) {
-                            const float2 g = all2(-group_sum<G>(dot(y, v)) * (inv * inv * n_inv));
+                    }
+                    if constexpr (!kBackward) {
+                        turn.apply(y);
+                    } else if (p.norm != kNoNorm) {
+                        const float2 g = all2(-group_sum<G>(dot(y, v)) * (inv * inv * n_inv));
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                y.p[i] = mul2(inv2, fma2(v.p[i], g, y.p[i]));
-                                y.q[i] = mul2(inv2, fma2(v.q[i], g, y.q[i]));
-                            }
+                        for (int i = 0; i < 2; ++i) {
+                            y.p[i] = mul2(inv2, fma2(v.p[i], g, y.p[i]));
+                            y.q[i] = mul2(inv2, fma2(v.q[i], g, y.q[i]));
                         }
                     }
-                    if (on && head < h1) put<kLayout>(out + head * to.h, op, oq, y);
+                    if (k * kGroups < left) put<kLayout>(out, d, y);
                 }
             }
         }
@@ -288,10 +290,7 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const Args p) {
             if (!p.side[sd].dw) continue;
             __syncthreads();
             if (on) {
-                const float2 sc = all2(p.side[sd].scale);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) dw[sd].p[i] = mul2(dw[sd].p[i], sc), dw[sd].q[i] = mul2(dw[sd].q[i], sc);
-                put<kLayout>(sums + (threadIdx.x / G) * G * kVec, op, oq, dw[sd]);
+                put<kLayout>(sums + (threadIdx.x / G) * G * kVec + op, d, dw[sd]);
             }
             __syncthreads();
             if (threadIdx.x < p.width) {

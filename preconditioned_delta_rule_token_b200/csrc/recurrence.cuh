@@ -45,12 +45,6 @@ __device__ __forceinline__ float root(float x) {
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ float rroot(float x) {
-    float r;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // a and b = 1 - a, each without the cancellation of taking it from the other where that one is near 1:
 // a product of thousands of decays near 1 shows any bias of a single one.
 //   log:   |g| < 0.2: b = -g q(g) with q the polynomial of degree 4 that meets (e^g - 1) / g at the
