@@ -29,6 +29,8 @@ struct Side {                       // one of q and k
     Tok3 sx, so;                    // strides of x, and of out (forward) or dout (backward)
     Tok3 sd;                        // strides of dx (backward)
     int H;
+    int parts, part_rows;           // a token's rows in parts of part_rows, a warp each
+    unsigned blocks;                // CTAs of this side: those of q come first
     float scale;
 };
 
@@ -37,9 +39,9 @@ struct Args {
     const long long* positions;     // [B, T] or NULL: pos0 + t
     const double* freqs;            // [rot / 2]
     const int* lengths;             // [B] or NULL
-    long long pos0, tokens;         // tokens = B * T
+    long long pos0;
+    unsigned tokens;                // B * T
     int T, width, rot, norm, layout, inverse;
-    int parts, part_rows;           // a token's rows (of q, then of k) in parts of part_rows, a warp each
     float eps, amplitude;
 };
 
@@ -124,10 +126,17 @@ template <int G> __device__ __forceinline__ float group_sum(float x) {
 
 // m cos and m sin of position * freq: the angle in turns and its whole turns taken off in 64 bits
 // (a far position times a frequency leaves no digits of the angle in 32), the rest in 32.
-__device__ __forceinline__ float2 cos_sin(double position, double freq, float amplitude) {
+// For bf16 the fast sine and cosine do: within 2^-20 for an angle of up to pi, far below its half step.
+template <typename Tx> __device__ __forceinline__ float2 cos_sin(double position, double freq, float amplitude) {
     const double turns = position * freq * 0.15915494309189533577;
+    const float part = (float)(turns - rint(turns));
     float s, c;
-    sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+    if constexpr (sizeof(Tx) == 2) {
+        s = __sinf(6.2831853f * part);
+        c = __cosf(6.2831853f * part);
+    } else {
+        sincospif(2.f * part, &s, &c);
+    }
     return make_float2(amplitude * c, amplitude * s);
 }
 
@@ -154,14 +163,17 @@ struct Turn {
     }
 };
 
-// A warp takes one token, or one of p.parts parts of its rows: its lanes make the token's table of cosines
-// (each angle once), each lane keeps its own four for every row, and groups of G lanes take the rows, kRows
-// of them in flight.
+// A warp takes the rows of q, or those of k, of one token, or one of the parts that they come in: its lanes
+// make the token's table of cosines (each angle once), each lane keeps its own four for every row, and
+// groups of G lanes take the rows, kRows of them in flight.
 template <int G, int kLayout, bool kBackward, typename Tx>
-__global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) heads_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, kBackward && sizeof(Tx) == 4 ? 2 : 3) heads_kernel(const Args p) {
     extern __shared__ float2 tables[];              // [warps][rot / 2]
     __shared__ float sums[kBackward ? kThreads * kVec : 1];
-    constexpr int kGroups = 32 / G, kRows = kBackward ? 2 : 4;
+    constexpr int kGroups = 32 / G, kRows = kBackward ? 2 : 4, kWarps = kThreads / 32;
+    const bool of_k = blockIdx.x >= p.side[0].blocks;
+    const Side s = of_k ? p.side[1] : p.side[0];
+    const unsigned block = of_k ? blockIdx.x - p.side[0].blocks : blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / G, gl = lane % G;
     const bool on = gl * kVec < p.width;
     const int pairs = p.rot / 2;
@@ -174,137 +186,119 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) heads_kernel(cons
     turn.turning = kLayout == kHalf ? (halves ? 4 : 0) : max(0, min(4, (p.rot - gl * kVec) / 2));
 #pragma unroll
     for (int i = 0; i < 2; ++i) turn.c[i] = turn.s[i] = turn.ns[i] = all2(0.f);
-    Eight dw[2];
+    Eight w, dw;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) dw[0].p[i] = dw[0].q[i] = dw[1].p[i] = dw[1].q[i] = all2(0.f);
+    for (int i = 0; i < 2; ++i) w.p[i] = w.q[i] = all2(1.f), dw.p[i] = dw.q[i] = all2(0.f);
+    if (on && s.w) {
+        Raw<kLayout, float> r;
+        r.load(s.w + op, d);
+        w = r.get();
+    }
 
-    const long long items = p.tokens * p.parts;
-    for (long long item = (long long)blockIdx.x * (kThreads / 32) + warp; item < items;
-         item += (long long)gridDim.x * (kThreads / 32)) {
-        const long long tok = item / p.parts, b = tok / p.T, t = tok - b * p.T;
-        const int part = (int)(item - tok * p.parts);
-        if (p.lengths && t >= p.lengths[b]) continue;
-        if (pairs) {
-            const double pos = (double)(p.positions ? p.positions[tok] : p.pos0 + t);
-            __syncwarp();                           // the last token's table has been read
-            for (int i = lane; i < pairs; i += 32) table[i] = cos_sin(pos, p.freqs[i], p.amplitude);
-            __syncwarp();
-            if (turn.turning) {
-                const float2* mine = table + gl * 4;
-                const int m = turn.turning - 1;
-                const float2 t0 = mine[0], t1 = mine[min(1, m)], t2 = mine[min(2, m)], t3 = mine[min(3, m)];
-                const float sg = kBackward || p.inverse ? -1.f : 1.f;
-                turn.c[0] = make_float2(t0.x, t1.x);
-                turn.c[1] = make_float2(t2.x, t3.x);
-                turn.s[0] = make_float2(sg * t0.y, sg * t1.y);
-                turn.s[1] = make_float2(sg * t2.y, sg * t3.y);
+    const unsigned items = p.tokens * s.parts;      // below 2^31
+    for (unsigned item = block * kWarps + warp; item < items; item += s.blocks * kWarps) {
+        const unsigned tok = item / s.parts, b = tok / p.T, t = tok - b * p.T;
+        if (p.lengths && (int)t >= p.lengths[b]) continue;
+        const int h0 = (item - tok * s.parts) * s.part_rows, h1 = min(h0 + s.part_rows, s.H);
+        const Tok3& to = kBackward ? s.sd : s.so;
+        const Tx* xp = static_cast<const Tx*>(s.x) + s.sx.at(b, t, h0 + group) + op;
+        const Tx* dp = kBackward ? static_cast<const Tx*>(s.dout) + s.so.at(b, t, h0 + group) + op : nullptr;
+        Tx* out = static_cast<Tx*>(s.out) + to.at(b, t, h0 + group) + op;
+        const int64_t xs = kGroups * s.sx.h, ds = kGroups * s.so.h, os = kGroups * to.h;
+        for (int r0 = h0; r0 < h1; r0 += kGroups * kRows) {   // every lane takes part in the sums
+            const int left = on ? h1 - r0 - group : 0;
+            Raw<kLayout, Tx> xr[kRows], dr[kBackward ? kRows : 1];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) turn.ns[i] = make_float2(-turn.s[i].x, -turn.s[i].y);
-            }
-        }
-        int first = part * p.part_rows, last = first + p.part_rows;   // of the rows of q, then of k
-#pragma unroll
-        for (int sd = 0; sd < 2; ++sd) {
-            const Side& s = p.side[sd];
-            const int h0 = max(first, 0), h1 = min(last, s.H);
-            first -= s.H;
-            last -= s.H;
-            if (h0 >= h1) continue;
-            const Tok3& to = kBackward ? s.sd : s.so;
-            const Tx* xp = static_cast<const Tx*>(s.x) + s.sx.at(b, t, h0 + group) + op;
-            const Tx* dp = kBackward ? static_cast<const Tx*>(s.dout) + s.so.at(b, t, h0 + group) + op : nullptr;
-            Tx* out = static_cast<Tx*>(s.out) + to.at(b, t, h0 + group) + op;
-            const int64_t xs = kGroups * s.sx.h, ds = kGroups * s.so.h, os = kGroups * to.h;
-            Eight w;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) w.p[i] = w.q[i] = all2(1.f);
-            if (on && s.w) {
-                Raw<kLayout, float> r;
-                r.load(s.w + op, d);
-                w = r.get();
-            }
-            for (int r0 = h0; r0 < h1; r0 += kGroups * kRows) {   // every lane takes part in the sums
-                const int left = on ? h1 - r0 - group : 0;
-                Raw<kLayout, Tx> xr[kRows], dr[kBackward ? kRows : 1];
-#pragma unroll
-                for (int k = 0; k < kRows; ++k, xp += xs) {
-                    xr[k].zero();
-                    if (k * kGroups < left) xr[k].load(xp, d);
-                    if constexpr (kBackward) {
-                        dr[k].zero();
-                        if (k * kGroups < left) dr[k].load(dp, d);
-                        dp += ds;
-                    }
+            for (int k = 0; k < kRows; ++k, xp += xs) {
+                xr[k].zero();
+                if (k * kGroups < left) xr[k].load(xp, d);
+                if constexpr (kBackward) {
+                    dr[k].zero();
+                    if (k * kGroups < left) dr[k].load(dp, d);
+                    dp += ds;
                 }
+            }
+            if (pairs && r0 == h0) {                    // behind the first rows' loads
+                const double pos = (double)(p.positions ? p.positions[tok] : p.pos0 + (long long)t);
+                __syncwarp();                           // the last token's table has been read
+                for (int i = lane; i < pairs; i += 32) table[i] = cos_sin<Tx>(pos, p.freqs[i], p.amplitude);
+                __syncwarp();
+                if (turn.turning) {
+                    const float2* mine = table + gl * 4;
+                    const int m = turn.turning - 1;
+                    const float2 t0 = mine[0], t1 = mine[min(1, m)], t2 = mine[min(2, m)], t3 = mine[min(3, m)];
+                    const float sg = kBackward || p.inverse ? -1.f : 1.f;
+                    turn.c[0] = make_float2(t0.x, t1.x);
+                    turn.c[1] = make_float2(t2.x, t3.x);
+                    turn.s[0] = make_float2(sg * t0.y, sg * t1.y);
+                    turn.s[1] = make_float2(sg * t2.y, sg * t3.y);
 #pragma unroll
-                for (int k = 0; k < kRows; ++k, out += os) {
-                    if (r0 + k * kGroups >= h1) break;
-                    const Eight v = xr[k].get();
-                    float inv = 1.f;
-                    if (p.norm != kNoNorm) {
-                        const float m = fmaf(group_sum<G>(dot(v, v)), n_inv, p.eps);
-                        inv = m > 0.f ? rroot(m) : 0.f;   // a row of zeros without eps stays zero
-                    }
-                    const float2 inv2 = all2(inv);
-                    Eight y;
-                    if constexpr (!kBackward) {
-                        const float2 f = all2(inv * s.scale);
+                    for (int i = 0; i < 2; ++i) turn.ns[i] = make_float2(-turn.s[i].x, -turn.s[i].y);
+                }
+            }
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) y.p[i] = mul2(v.p[i], f), y.q[i] = mul2(v.q[i], f);
-                    } else {
-                        y = dr[k].get();
-                        turn.apply(y);
-                        const float2 f = all2(s.scale);
+            for (int k = 0; k < kRows; ++k, out += os) {
+                if (r0 + k * kGroups >= h1) break;
+                const Eight v = xr[k].get();
+                float inv = 1.f;
+                if (p.norm != kNoNorm) {
+                    const float m = fmaf(group_sum<G>(dot(v, v)), n_inv, p.eps);
+                    inv = m > 0.f ? rroot(m) : 0.f;   // a row of zeros without eps stays zero
+                }
+                const float2 inv2 = all2(inv);
+                Eight y;
+                if constexpr (!kBackward) {
+                    const float2 f = all2(inv * s.scale);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) y.p[i] = mul2(y.p[i], f), y.q[i] = mul2(y.q[i], f);
-                        if (s.dw) {
+                    for (int i = 0; i < 2; ++i) y.p[i] = mul2(v.p[i], f), y.q[i] = mul2(v.q[i], f);
+                } else {
+                    y = dr[k].get();
+                    turn.apply(y);
+                    const float2 f = all2(s.scale);
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                dw[sd].p[i] = fma2(y.p[i], mul2(v.p[i], inv2), dw[sd].p[i]);
-                                dw[sd].q[i] = fma2(y.q[i], mul2(v.q[i], inv2), dw[sd].q[i]);
-                            }
-                        }
-                    }
-                    if (s.w) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) y.p[i] = mul2(y.p[i], w.p[i]), y.q[i] = mul2(y.q[i], w.q[i]);
-                    }
-                    if constexpr (!kBackward) {
-                        turn.apply(y);
-                    } else if (p.norm != kNoNorm) {
-                        const float2 g = all2(-group_sum<G>(dot(y, v)) * (inv * inv * n_inv));
+                    for (int i = 0; i < 2; ++i) y.p[i] = mul2(y.p[i], f), y.q[i] = mul2(y.q[i], f);
+                    if (s.dw) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            y.p[i] = mul2(inv2, fma2(v.p[i], g, y.p[i]));
-                            y.q[i] = mul2(inv2, fma2(v.q[i], g, y.q[i]));
+                            dw.p[i] = fma2(y.p[i], mul2(v.p[i], inv2), dw.p[i]);
+                            dw.q[i] = fma2(y.q[i], mul2(v.q[i], inv2), dw.q[i]);
                         }
                     }
-                    if (k * kGroups < left) put<kLayout>(out, d, y);
                 }
+                if (s.w) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) y.p[i] = mul2(y.p[i], w.p[i]), y.q[i] = mul2(y.q[i], w.q[i]);
+                }
+                if constexpr (!kBackward) {
+                    turn.apply(y);
+                } else if (p.norm != kNoNorm) {
+                    const float2 g = all2(-group_sum<G>(dot(y, v)) * (inv * inv * n_inv));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        y.p[i] = mul2(inv2, fma2(v.p[i], g, y.p[i]));
+                        y.q[i] = mul2(inv2, fma2(v.q[i], g, y.q[i]));
+                    }
+                }
+                if (k * kGroups < left) put<kLayout>(out, d, y);
             }
         }
     }
     if constexpr (kBackward) {                      // this CTA's part of dw, groups and warps in order
-#pragma unroll
-        for (int sd = 0; sd < 2; ++sd) {
-            if (!p.side[sd].dw) continue;
-            __syncthreads();
-            if (on) {
-                put<kLayout>(sums + (threadIdx.x / G) * G * kVec + op, d, dw[sd]);
-            }
-            __syncthreads();
-            if (threadIdx.x < p.width) {
-                float t = 0.f;
-                for (int g = 0; g < kThreads / G; ++g) t += sums[g * G * kVec + threadIdx.x];
-                p.side[sd].dw[(size_t)blockIdx.x * p.width + threadIdx.x] = t;
-            }
+        if (!s.dw) return;
+        if (on) put<kLayout>(sums + (threadIdx.x / G) * G * kVec + op, d, dw);
+        __syncthreads();
+        if (threadIdx.x < p.width) {
+            float t = 0.f;
+            for (int g = 0; g < kThreads / G; ++g) t += sums[g * G * kVec + threadIdx.x];
+            s.dw[(size_t)block * p.width + threadIdx.x] = t;
         }
     }
 }
 
 // dw of both sides from the CTAs' partial sums, in a fixed order: a warp a share of them, then the warps.
 __global__ void __launch_bounds__(1024) dw_kernel(const float* part_q, const float* part_k, float* dwq, float* dwk,
-                                                  int parts, int width) {
+                                                  int parts_q, int parts_k, int width) {
+    const int parts = blockIdx.y ? parts_k : parts_q;
     const float* part = blockIdx.y ? part_k : part_q;
     float* dw = blockIdx.y ? dwk : dwq;
     if (!dw) return;

@@ -1791,28 +1791,42 @@ int check_qk(const osdn_qk_params* p) {
     const double tokens = (double)p->B * p->T;
     if (tokens * std::max(p->Hq, p->Hk) * p->width > 9.0e18)
         return fail(OSDN_ERR_INVALID_ARG, "tensor sizes overflow 64-bit indexing");
-    if (tokens > 2147483647.0) return fail(OSDN_ERR_INVALID_ARG, "B * T exceeds the grid limit");
+    if (tokens > 1073741824.0) return fail(OSDN_ERR_INVALID_ARG, "B * T must be at most 2^30");
     return OSDN_OK;
 }
 
-// Parts of a token's rows, a warp each: enough that every SM gets 16 warps, each with at least the rows that
-// a warp has in flight at a time.
+// How the rows of q and of k go to CTAs of 8 warps. A token's rows come in parts, a warp each: enough that
+// every SM gets 16 warps, each with at least the rows that a warp has in flight at a time.
 struct QkShape {
-    int lanes, parts, part_rows;
-    unsigned grid;
+    int lanes;
+    struct {
+        int parts, part_rows;
+        unsigned blocks;
+    } side[2];
 };
 QkShape qk_shape(const osdn_qk_params* p, bool backward) {
     QkShape q;
     q.lanes = p->width <= 64 ? 8 : p->width <= 128 ? 16 : 32;
-    const int rows = p->Hq + p->Hk, flight = 32 / q.lanes * (backward ? 2 : 4), sms = sm_count();
+    const int flight = 32 / q.lanes * (backward ? 2 : 4), sms = sm_count(), H = p->Hq + p->Hk;
     const int64_t tokens = (int64_t)p->B * p->T, warps = osdn::heads::kThreads / 32;
-    const int64_t most = (rows + flight - 1) / flight, want = tokens ? (16LL * sms + tokens - 1) / tokens : 1;
-    const int parts = (int)std::min(most, want);
-    q.part_rows = ((rows + parts - 1) / parts + flight - 1) / flight * flight;
-    q.parts = (rows + q.part_rows - 1) / q.part_rows;
-    const int64_t blocks = (tokens * q.parts + warps - 1) / warps;
-    // the backward's CTAs each leave a row of partial weight gradients: at most what runs at a time
-    q.grid = (unsigned)(backward ? std::min<int64_t>(blocks, 4 * sms) : std::min<int64_t>(blocks, 2147483647));
+    const int64_t want = tokens ? (16LL * sms + 2 * tokens - 1) / (2 * tokens) : 1;
+    for (int i = 0; i < 2; ++i) {
+        const int rows = i ? p->Hk : p->Hq;
+        auto& s = q.side[i];
+        s.parts = 1;
+        s.part_rows = rows;
+        s.blocks = 0;
+        if (!rows) continue;
+        const int parts = (int)std::min<int64_t>((rows + flight - 1) / flight, want);
+        s.part_rows = ((rows + parts - 1) / parts + flight - 1) / flight * flight;
+        s.parts = (rows + s.part_rows - 1) / s.part_rows;
+        const int64_t blocks = (tokens * s.parts + warps - 1) / warps;
+        // shared by rows between q and k: about what runs at a time in the backward, where each CTA leaves a row
+        // of partial weight gradients; some waves of it in the forward
+        static const int64_t waves = getenv("QK_WAVES") ? atoi(getenv("QK_WAVES")) : 4;
+        const int64_t most = std::max<int64_t>(1, (backward ? 3LL : 3LL * waves) * sms * rows / H);
+        s.blocks = (unsigned)std::min(blocks, most);
+    }
     return q;
 }
 
@@ -1820,11 +1834,14 @@ template <bool kBackward> int launch_heads(const osdn_qk_params* p, osdn::heads:
     using namespace osdn::heads;
     using bf = __nv_bfloat16;
     const QkShape q = qk_shape(p, kBackward);
-    a.parts = q.parts;
-    a.part_rows = q.part_rows;
+    for (int i = 0; i < 2; ++i) {
+        a.side[i].parts = q.side[i].parts;
+        a.side[i].part_rows = q.side[i].part_rows;
+        a.side[i].blocks = q.side[i].blocks;
+    }
     auto go = [&](auto g, auto layout, auto tx) {
         heads_kernel<g, layout, kBackward, decltype(tx)>
-            <<<q.grid, kThreads, kThreads / 32 * sizeof(float2) * (a.rot / 2), st>>>(a);
+            <<<q.side[0].blocks + q.side[1].blocks, kThreads, kThreads / 32 * sizeof(float2) * (a.rot / 2), st>>>(a);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "head norm and rotation launch");
     };
@@ -1847,7 +1864,7 @@ osdn::heads::Args heads_args(const osdn_qk_params* p, const int64_t* positions, 
     a.freqs = freqs;
     a.lengths = lengths;
     a.pos0 = p->pos0;
-    a.tokens = (long long)p->B * p->T;
+    a.tokens = (unsigned)p->B * p->T;
     a.T = p->T; a.width = p->width; a.rot = p->rot_dim; a.norm = p->norm; a.layout = p->layout;
     a.eps = p->eps; a.amplitude = p->amplitude;
     a.side[0].H = p->Hq; a.side[0].scale = p->scale_q;
@@ -1912,7 +1929,8 @@ int osdn_qk_bwd_workspace_size(const osdn_qk_params* p, size_t* bytes) {
     int rc = check_qk(p);
     if (rc) return rc;
     if (!bytes) return fail(OSDN_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = round_up((size_t)2 * qk_shape(p, true).grid * p->width * sizeof(float), 256);
+    const QkShape sh = qk_shape(p, true);
+    *bytes = round_up((size_t)(sh.side[0].blocks + sh.side[1].blocks) * p->width * sizeof(float), 256);
     return OSDN_OK;
 }
 
@@ -1943,14 +1961,15 @@ int osdn_qk_bwd(const osdn_qk_params* p, const void* q, const void* k, const flo
                 return cuda_fail(e, "weight gradient");
         return OSDN_OK;
     }
-    const unsigned grid = qk_shape(p, true).grid;
-    const size_t part = (size_t)grid * p->width;
+    const QkShape sh = qk_shape(p, true);
+    const size_t part = (size_t)sh.side[0].blocks * p->width;   // where the partial sums of k start
+    const size_t need = part + (size_t)sh.side[1].blocks * p->width;
     float* ws = static_cast<float*>(workspace);
     if (dwq || dwk) {
         if (!ws) return fail(OSDN_ERR_INVALID_ARG, "workspace is NULL");
-        if (workspace_bytes < 2 * part * sizeof(float))
+        if (workspace_bytes < need * sizeof(float))
             return fail(OSDN_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes,
-                        2 * part * sizeof(float));
+                        need * sizeof(float));
     }
     osdn::heads::Args a = heads_args(p, positions, freqs, lengths);
     a.side[0].x = q; a.side[0].w = wq; a.side[0].dout = dq_out; a.side[0].out = dq; a.side[0].dw = dwq ? ws : nullptr;
@@ -1958,8 +1977,8 @@ int osdn_qk_bwd(const osdn_qk_params* p, const void* q, const void* k, const flo
     a.side[1].dw = dwk ? ws + part : nullptr;
     if ((rc = launch_heads<true>(p, a, st))) return rc;
     if (dwq || dwk) {
-        osdn::heads::dw_kernel<<<dim3((p->width + 31) / 32, 2), 1024, 0, st>>>(ws, ws + part, dwq, dwk, (int)grid,
-                                                                              p->width);
+        osdn::heads::dw_kernel<<<dim3((p->width + 31) / 32, 2), 1024, 0, st>>>(
+            ws, ws + part, dwq, dwk, (int)sh.side[0].blocks, (int)sh.side[1].blocks, p->width);
         if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "weight gradient launch");
     }
     return OSDN_OK;
