@@ -221,6 +221,12 @@ def _set_strides(params, q=None, k=None, v=None, out=None):
     return params
 
 
+def _current_stream(device_index):
+    """Handle of the current stream of a device (what torch.cuda.current_stream().cuda_stream gives, without
+    making a Stream object: 3 us less a call)."""
+    return torch._C._cuda_getCurrentRawStream(device_index)
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -372,10 +378,15 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
+def _handle(stream):
+    """Handle of `stream`, or of the current device's current stream."""
+    return _current_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+
+
 def osdn_recur_fwd(params, x, gate, h0, lengths, h, final_h, checkpoints, stream=None):
     """Raw C-ABI call of the gated linear recurrence (every tensor preallocated; strides in params)."""
     _check(lib().osdn_recur_fwd(params, _address(x), _address(gate), _address(h0), _address(lengths), _address(h),
-                                _address(final_h), _address(checkpoints), _stream(stream)))
+                                _address(final_h), _address(checkpoints), _handle(stream)))
 
 
 def osdn_recur_bwd_workspace_size(params: osdn_recur_params) -> int:
@@ -388,18 +399,18 @@ def osdn_recur_bwd(params, x, gate, h0, lengths, dh, dfinal_h, checkpoints, dx, 
     """Raw C-ABI call of the recurrence's backward."""
     _check(lib().osdn_recur_bwd(params, _address(x), _address(gate), _address(h0), _address(lengths), _address(dh),
                                 _address(dfinal_h), _address(checkpoints), _address(dx), _address(dgate),
-                                _address(dh0), _address(workspace), _ws_bytes(workspace), _stream(stream)))
+                                _address(dh0), _address(workspace), _ws_bytes(workspace), _handle(stream)))
 
 
 def osdn_recur_step(params, x, gate, state, h, stream=None):
     """Raw C-ABI call: one token of the recurrence, state updated in place."""
-    _check(lib().osdn_recur_step(params, _address(x), _address(gate), _address(state), _address(h), _stream(stream)))
+    _check(lib().osdn_recur_step(params, _address(x), _address(gate), _address(state), _address(h), _handle(stream)))
 
 
 def osdn_qk_fwd(params, q, k, wq, wk, positions, freqs, lengths, q_out, k_out, stream=None):
     """Raw C-ABI call of the query and key norms with the rotation (strides in params)."""
     _check(lib().osdn_qk_fwd(params, _address(q), _address(k), _address(wq), _address(wk), _address(positions),
-                             _address(freqs), _address(lengths), _address(q_out), _address(k_out), _stream(stream)))
+                             _address(freqs), _address(lengths), _address(q_out), _address(k_out), _handle(stream)))
 
 
 def osdn_qk_bwd_workspace_size(params: osdn_qk_params) -> int:
@@ -414,13 +425,13 @@ def osdn_qk_bwd(params, q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out,
     _check(lib().osdn_qk_bwd(params, _address(q), _address(k), _address(wq), _address(wk), _address(positions),
                              _address(freqs), _address(lengths), _address(dq_out), _address(dk_out), _address(dq),
                              _address(dk), _address(dwq), _address(dwk), _address(workspace), _ws_bytes(workspace),
-                             _stream(stream)))
+                             _handle(stream)))
 
 
 def osdn_rope(params, x, positions, freqs, lengths, out, inverse=False, stream=None):
     """Raw C-ABI call of the rotation alone."""
     _check(lib().osdn_rope(params, _address(x), _address(positions), _address(freqs), _address(lengths),
-                           _address(out), 1 if inverse else 0, _stream(stream)))
+                           _address(out), 1 if inverse else 0, _handle(stream)))
 
 
 def osdn_rope_freqs(rot_dim, base, scaling, factor, original_length, low_turns, high_turns):

@@ -5,12 +5,15 @@ Wrappers that check shapes, types and devices, allocate the outputs and call the
 `stream` is a torch.cuda.Stream of the tensors' device (default: that device's current
 stream); outputs and workspaces are allocated on it. All tensors must be on one CUDA
 device; there is no CPU path.
+
+A decode token's kernels take a few microseconds, so a call does little in Python: the
+checks and the parameter block depend on the tensors' layouts alone (shape, strides,
+type, device) and are kept by them.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
-from functools import lru_cache
 
 import torch
 
@@ -32,6 +35,21 @@ def _scope(dev, stream):
             _bad("the stream is of %s, the tensors are on %s" % (stream.device, dev))
         return torch.cuda.stream(stream)
     return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+class _Kept(dict):
+    """Parameter blocks by the layouts they were checked for; emptied when it grows past 1024."""
+
+    def keep(self, key, value):
+        if len(self) >= 1024:
+            self.clear()
+        self[key] = value
+        return value
+
+
+def _lay(t):
+    """Everything about a tensor that the checks and the parameter block depend on."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
 
 
 def _choice(name, value, table):
@@ -74,31 +92,46 @@ def _strides(name, t, n):
     return st[:n]
 
 
-@lru_cache(maxsize=256)
-def _recur_params(nB, T, D, dtype, gate_dtype, gate_form, input_scale, sx, sg, sh):
-    p = B.osdn_recur_params()
-    p.struct_size = ctypes.sizeof(p)
-    p.B, p.T, p.D, p.dtype, p.gate_dtype, p.gate_form, p.input_scale = nB, T, D, dtype, gate_dtype, gate_form, input_scale
-    p.stride_x[:], p.stride_gate[:], p.stride_h[:] = sx, sg, sh
-    return p
+def _new(t, lengths=None):
+    """An uninitialised dense tensor like t; zeros where lengths leave rows unwritten."""
+    if lengths is not None:
+        return torch.zeros(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
-def _recur_inputs(x, gate, gate_form, input_scale, h0, lengths, h, h_name):
-    if x.dim() != 3:
-        _bad("x is [B, T, D] (got %s)" % (tuple(x.shape),))
-    nB, T, D = x.shape
+def _saved(nB, T, D):
+    return nB, (T + B.OSDN_RECUR_CHECKPOINT - 1) // B.OSDN_RECUR_CHECKPOINT, D
+
+
+_RECUR = _Kept()
+
+
+def _recur_params(x, gate, gate_form, input_scale, named, token=True):
+    """Checks a recurrence call and makes its parameter block. named: (name, tensor, kind) with kind "token" (like
+    x, any strides), "state" ([B, D] fp32), "lengths" or "saved"."""
+    if x.dim() != (3 if token else 2):
+        _bad("x is %s (got %s)" % ("[B, T, D]" if token else "[B, D]", tuple(x.shape)))
     if not x.is_cuda:
         _bad("x is on %s (the library has no CPU path)" % x.device)
-    dev = x.device
-    code, gcode = _dtype("x", x), _dtype("gate", gate)
+    dev, code, gcode = x.device, _dtype("x", x), _dtype("gate", gate)
+    nB, T, D = x.shape if token else (x.shape[0], 1, x.shape[1])
     _held(dev, "gate", gate, x.shape, gate.dtype, dense=False)
-    _held(dev, "h0", h0, (nB, D), torch.float32)
-    _held(dev, "lengths", lengths, (nB,), torch.int32)
-    _held(dev, h_name, h, x.shape, x.dtype, dense=False)
-    p = _recur_params(nB, T, D, code, gcode, _choice("gate_form", gate_form, B.GATE_FORMS),
-                      _choice("input_scale", input_scale, B.INPUT_SCALES), _strides("x", x, 2),
-                      _strides("gate", gate, 2), _strides(h_name, h, 2))
-    return p, dev, nB, T, D
+    p = B.osdn_recur_params()
+    p.struct_size = ctypes.sizeof(p)
+    p.B, p.T, p.D, p.dtype, p.gate_dtype = nB, T, D, code, gcode
+    p.gate_form = _choice("gate_form", gate_form, B.GATE_FORMS)
+    p.input_scale = _choice("input_scale", input_scale, B.INPUT_SCALES)
+    n = 2 if token else 1
+    p.stride_x[:n], p.stride_gate[:n] = _strides("x", x, n), _strides("gate", gate, n)
+    for name, t, kind in named:
+        if kind == "token":
+            _held(dev, name, t, x.shape, x.dtype, dense=False)
+            p.stride_h[:n] = _strides(name, t, n)
+        elif kind == "lengths":
+            _held(dev, name, t, (nB,), torch.int32)
+        else:
+            _held(dev, name, t, (nB, D) if kind == "state" else _saved(nB, T, D), torch.float32)
+    return p
 
 
 def recurrence(x, gate, h0=None, lengths=None, gate_form="decay", input_scale="none", checkpoints=False, h=None,
@@ -109,18 +142,18 @@ def recurrence(x, gate, h0=None, lengths=None, gate_form="decay", input_scale="n
     slices of one projection). gate_form: a = gate ("decay"), exp(gate) ("log") or sigmoid(gate) ("logit");
     a = 0 starts a new document. input_scale: s = 1 ("none"), 1 - a ("complement") or sqrt(1 - a^2) ("norm").
     h0 [B,D] fp32 or None (zeros). lengths [B] int32 (None: T each): tokens from a sequence's length
-    on are not read; their rows of h are zeros (left as they were when `h` is given).
+    on do not count; their rows of h are zeros (left as they were when `h` is given).
     Returns (h [B,T,D] in x's type, final_h [B,D] fp32), and with checkpoints=True the states
     [B,ceil(T/64),D] fp32 that recurrence_backward takes."""
-    p, dev, nB, T, D = _recur_inputs(x, gate, gate_form, input_scale, h0, lengths, h, "h")
-    with _scope(dev, stream):
+    key = ("fwd", gate_form, input_scale, _lay(x), _lay(gate), _lay(h0), _lay(lengths), _lay(h))
+    p = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
+        x, gate, gate_form, input_scale, (("h0", h0, "state"), ("lengths", lengths, "lengths"), ("h", h, "token"))))
+    nB, T, D = x.shape
+    with _scope(x.device, stream):
         if h is None:
-            h = (torch.empty if lengths is None else torch.zeros)((nB, T, D), dtype=x.dtype, device=dev)
-        final_h = torch.empty((nB, D), dtype=torch.float32, device=dev)
-        marks = None
-        if checkpoints:
-            marks = torch.empty((nB, (T + B.OSDN_RECUR_CHECKPOINT - 1) // B.OSDN_RECUR_CHECKPOINT, D),
-                                dtype=torch.float32, device=dev)
+            h = _new(x, lengths)
+        final_h = torch.empty((nB, D), dtype=torch.float32, device=x.device)
+        marks = torch.empty(_saved(nB, T, D), dtype=torch.float32, device=x.device) if checkpoints else None
         B.osdn_recur_fwd(p, x, gate, h0, lengths, h, final_h, marks)
     return (h, final_h, marks) if checkpoints else (h, final_h)
 
@@ -133,16 +166,17 @@ def recurrence_backward(x, gate, dh, h0=None, dfinal_h=None, lengths=None, check
     recurrence(..., checkpoints=True) returned for the same inputs; None runs the forward again for them.
     Returns a dict with dx (x's type), dgate (the gate's type; with respect to the gate as given) and
     dh0 [B,D] fp32. Rows from a sequence's length on are zeros."""
-    p, dev, nB, T, D = _recur_inputs(x, gate, gate_form, input_scale, h0, lengths, dh, "dh")
-    _held(dev, "dfinal_h", dfinal_h, (nB, D), torch.float32)
-    _held(dev, "checkpoints", checkpoints,
-          (nB, (T + B.OSDN_RECUR_CHECKPOINT - 1) // B.OSDN_RECUR_CHECKPOINT, D), torch.float32)
-    with _scope(dev, stream):
-        new = torch.empty if lengths is None else torch.zeros
-        g = {"dx": new((nB, T, D), dtype=x.dtype, device=dev), "dgate": new((nB, T, D), dtype=gate.dtype, device=dev),
-             "dh0": torch.empty((nB, D), dtype=torch.float32, device=dev)}
+    key = ("bwd", gate_form, input_scale, _lay(x), _lay(gate), _lay(dh), _lay(h0), _lay(dfinal_h), _lay(lengths),
+           _lay(checkpoints))
+    p = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
+        x, gate, gate_form, input_scale,
+        (("h0", h0, "state"), ("lengths", lengths, "lengths"), ("dh", dh, "token"), ("dfinal_h", dfinal_h, "state"),
+         ("checkpoints", checkpoints, "saved"))))
+    with _scope(x.device, stream):
+        g = {"dx": _new(x, lengths), "dgate": _new(gate, lengths),
+             "dh0": torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device)}
         if checkpoints is None and workspace is None:
-            workspace = torch.empty(B.osdn_recur_bwd_workspace_size(p), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(B.osdn_recur_bwd_workspace_size(p), dtype=torch.uint8, device=x.device)
         B.osdn_recur_bwd(p, x, gate, h0, lengths, dh, dfinal_h, checkpoints, g["dx"], g["dgate"], g["dh0"], workspace)
     return g
 
@@ -150,62 +184,45 @@ def recurrence_backward(x, gate, dh, h0=None, dfinal_h=None, lengths=None, check
 def recurrence_step(x, gate, state, gate_form="decay", input_scale="none", out=None, stream=None):
     """One decode token of the recurrence: x, gate [B,D]; state [B,D] fp32, updated in place.
     Returns the new state in x's type [B,D] (`out` if given)."""
-    if x.dim() != 2:
-        _bad("x is [B, D] (got %s)" % (tuple(x.shape),))
-    if not x.is_cuda:
-        _bad("x is on %s (the library has no CPU path)" % x.device)
-    (nB, D), dev = x.shape, x.device
-    code, gcode = _dtype("x", x), _dtype("gate", gate)
-    _held(dev, "gate", gate, x.shape, gate.dtype, dense=False)
-    _held(dev, "state", state, x.shape, torch.float32)
-    _held(dev, "out", out, x.shape, x.dtype, dense=False)
-    with _scope(dev, stream):
+    key = ("step", gate_form, input_scale, _lay(x), _lay(gate), _lay(state), _lay(out))
+    p = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
+        x, gate, gate_form, input_scale, (("state", state, "state"), ("out", out, "token")), token=False))
+    with _scope(x.device, stream):
         if out is None:
-            out = torch.empty((nB, D), dtype=x.dtype, device=dev)
-        p = _recur_params(nB, 1, D, code, gcode, _choice("gate_form", gate_form, B.GATE_FORMS),
-                          _choice("input_scale", input_scale, B.INPUT_SCALES), _strides("x", x, 1) + (0,),
-                          _strides("gate", gate, 1) + (0,), _strides("out", out, 1) + (0,))
+            out = _new(x)
         B.osdn_recur_step(p, x, gate, state, out)
     return out
 
 
-@lru_cache(maxsize=256)
-def _qk_params(nB, T, Hq, Hk, width, dtype, norm, layout, rot, eps, amplitude, scale_q, scale_k, pos0, sq, sk, soq, sok):
-    p = B.osdn_qk_params()
-    p.struct_size = ctypes.sizeof(p)
-    p.B, p.T, p.Hq, p.Hk, p.width, p.dtype, p.norm, p.layout, p.rot_dim = nB, T, Hq, Hk, width, dtype, norm, layout, rot
-    p.eps, p.amplitude, p.scale_q, p.scale_k, p.pos0 = eps, amplitude, scale_q, scale_k, pos0
-    p.stride_q[:], p.stride_k[:], p.stride_out_q[:], p.stride_out_k[:] = sq, sk, soq, sok
-    return p
+_HEADS = _Kept()
 
 
-def _heads_inputs(q, k, freqs, positions, lengths, norm, layout, wq, wk, out_q, out_k, eps, amplitude, scale_q, scale_k,
-                  pos0, names):
+def _heads_params(q, k, freqs, positions, lengths, norm, layout, wq, wk, out_q, out_k, numbers, names):
     if q.dim() != 4 or (k is not None and k.dim() != 4):
-        _bad("%s are [B, T, H, width]" % " and ".join(names[:2]))
+        _bad("%s [B, T, H, width]" % ("%s and %s are" % names[:2] if names[1] else "%s is" % names[0]))
     if not q.is_cuda:
         _bad("%s is on %s (the library has no CPU path)" % (names[0], q.device))
     (nB, T, Hq, width), dev = q.shape, q.device
     Hk = 0 if k is None else k.shape[2]
-    code = _dtype(names[0], q)
+    p = B.osdn_qk_params()
+    p.struct_size = ctypes.sizeof(p)
+    p.B, p.T, p.Hq, p.Hk, p.width, p.dtype = nB, T, Hq, Hk, width, _dtype(names[0], q)
+    p.norm, p.layout = _choice("norm", norm, B.NORMS), _choice("layout", layout, B.ROPE_LAYOUTS)
+    p.eps, p.amplitude, p.scale_q, p.scale_k, p.pos0 = numbers
     if k is not None:
         _held(dev, names[1], k, (nB, T, Hk, width), q.dtype, dense=False)
+        _held(dev, names[3], out_k, k.shape, q.dtype, dense=False)
+        p.stride_k[:], p.stride_out_k[:] = _strides(names[1], k, 3), _strides(names[3], out_k, 3)
+    _held(dev, names[2], out_q, q.shape, q.dtype, dense=False)
+    p.stride_q[:], p.stride_out_q[:] = _strides(names[0], q, 3), _strides(names[2], out_q, 3)
     _held(dev, "positions", positions, (nB, T), torch.int64)
     _held(dev, "lengths", lengths, (nB,), torch.int32)
     _held(dev, "wq", wq, (width,), torch.float32)
     _held(dev, "wk", wk, (width,), torch.float32)
-    rot = 0
     if freqs is not None:
         _held(dev, "freqs", freqs, (freqs.numel(),), torch.float64)
-        rot = 2 * freqs.numel()
-    _held(dev, names[2], out_q, q.shape, q.dtype, dense=False)
-    if k is not None:
-        _held(dev, names[3], out_k, k.shape, q.dtype, dense=False)
-    p = _qk_params(nB, T, Hq, Hk, width, code, _choice("norm", norm, B.NORMS),
-                   _choice("layout", layout, B.ROPE_LAYOUTS), rot, eps, amplitude, scale_q, scale_k, pos0,
-                   _strides(names[0], q, 3), _strides(names[1], k, 3), _strides(names[2], out_q, 3),
-                   _strides(names[3], out_k, 3))
-    return p, dev
+        p.rot_dim = 2 * freqs.numel()
+    return p
 
 
 def qk_norm(q, k, freqs=None, positions=None, norm="l2", eps=1e-6, wq=None, wk=None, layout="half", amplitude=1.0,
@@ -220,14 +237,16 @@ def qk_norm(q, k, freqs=None, positions=None, norm="l2", eps=1e-6, wq=None, wk=N
     [B,T] int64 (None: pos0 + t). lengths [B] int32: tokens from a sequence's length on give zeros
     (rows of a given q_out, k_out stay as they were). q_out may be q, k_out may be k.
     Returns (q_out, k_out)."""
-    p, dev = _heads_inputs(q, k, freqs, positions, lengths, norm, layout, wq, wk, q_out, k_out, float(eps),
-                           float(amplitude), float(scale_q), float(scale_k), int(pos0), ("q", "k", "q_out", "k_out"))
-    with _scope(dev, stream):
-        new = torch.empty if lengths is None else torch.zeros
+    numbers = (eps, amplitude, scale_q, scale_k, pos0)
+    key = (norm, layout, numbers, _lay(q), _lay(k), _lay(freqs), _lay(positions), _lay(lengths), _lay(wq), _lay(wk),
+           _lay(q_out), _lay(k_out))
+    p = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
+        q, k, freqs, positions, lengths, norm, layout, wq, wk, q_out, k_out, numbers, ("q", "k", "q_out", "k_out")))
+    with _scope(q.device, stream):
         if q_out is None:
-            q_out = new(q.shape, dtype=q.dtype, device=dev)
+            q_out = _new(q, lengths)
         if k is not None and k_out is None:
-            k_out = new(k.shape, dtype=k.dtype, device=dev)
+            k_out = _new(k, lengths)
         B.osdn_qk_fwd(p, q, k, wq, wk, positions, freqs, lengths, q_out, k_out)
     return q_out, k_out
 
@@ -240,16 +259,17 @@ def qk_norm_backward(q, k, dq_out, dk_out, freqs=None, positions=None, norm="l2"
     [width] fp32 (None without the weight)."""
     if (k is None) != (dk_out is None):
         _bad("k and dk_out go together")
-    p, dev = _heads_inputs(q, k, freqs, positions, lengths, norm, layout, wq, wk, dq_out, dk_out, float(eps),
-                           float(amplitude), float(scale_q), float(scale_k), int(pos0), ("q", "k", "dq_out", "dk_out"))
-    with _scope(dev, stream):
-        new = torch.empty if lengths is None else torch.zeros
-        g = {"dq": new(q.shape, dtype=q.dtype, device=dev),
-             "dk": None if k is None else new(k.shape, dtype=k.dtype, device=dev),
+    numbers = (eps, amplitude, scale_q, scale_k, pos0)
+    key = ("bwd", norm, layout, numbers, _lay(q), _lay(k), _lay(freqs), _lay(positions), _lay(lengths), _lay(wq), _lay(wk),
+           _lay(dq_out), _lay(dk_out))
+    p = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
+        q, k, freqs, positions, lengths, norm, layout, wq, wk, dq_out, dk_out, numbers, ("q", "k", "dq_out", "dk_out")))
+    with _scope(q.device, stream):
+        g = {"dq": _new(q, lengths), "dk": None if k is None else _new(k, lengths),
              "dwq": None if wq is None else torch.empty_like(wq),
              "dwk": None if wk is None or k is None else torch.empty_like(wk)}
         if workspace is None and (g["dwq"] is not None or g["dwk"] is not None):
-            workspace = torch.empty(B.osdn_qk_bwd_workspace_size(p), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(B.osdn_qk_bwd_workspace_size(p), dtype=torch.uint8, device=q.device)
         B.osdn_qk_bwd(p, q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, g["dq"], g["dk"], g["dwq"],
                       g["dwk"], workspace)
     return g
@@ -260,13 +280,17 @@ def rope(x, freqs, positions=None, layout="half", amplitude=1.0, scale=1.0, pos0
     """The position rotation alone on x [B,T,H,width]: see qk_norm for freqs, positions, layout and lengths.
     inverse=True turns back with the same amplitude: it takes the gradient of the result to that of x.
     `out` may be x. Returns the rotated tensor."""
-    if freqs is None:
-        _bad("freqs is needed")
-    p, dev = _heads_inputs(x, None, freqs, positions, lengths, "none", layout, None, None, out, None, 0.0,
-                           float(amplitude), float(scale), 1.0, int(pos0), ("x", "k", "out", "k_out"))
-    with _scope(dev, stream):
+    numbers = (0.0, amplitude, scale, 1.0, pos0)
+    key = ("rope", layout, numbers, _lay(x), _lay(freqs), _lay(positions), _lay(lengths), _lay(out))
+    p = _HEADS.get(key)
+    if p is None:
+        if freqs is None:
+            _bad("freqs is needed")
+        p = _HEADS.keep(key, _heads_params(x, None, freqs, positions, lengths, "none", layout, None, None, out, None,
+                                           numbers, ("x", None, "out", None)))
+    with _scope(x.device, stream):
         if out is None:
-            out = (torch.empty if lengths is None else torch.zeros)(x.shape, dtype=x.dtype, device=dev)
+            out = _new(x, lengths)
         B.osdn_rope(p, x, positions, freqs, lengths, out, inverse)
     return out
 
