@@ -9,6 +9,8 @@
 // A row lies in a group of lanes, 8 features a lane, chosen so that both features of a pair are in one lane;
 // only a row's sums go between the lanes.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace osdn {
@@ -29,7 +31,7 @@ struct Side {                       // one of q and k
     Tok3 sx, so;                    // strides of x, and of out (forward) or dout (backward)
     Tok3 sd;                        // strides of dx (backward)
     int H;
-    int parts, part_rows;           // a token's rows in parts of part_rows, a warp each
+    int parts, part_rows;           // a token's rows in parts of part_rows, a group each
     unsigned blocks;                // CTAs of this side: those of q come first
     float scale;
 };
@@ -144,8 +146,8 @@ template <typename Tx> __device__ __forceinline__ float2 cos_sin(double position
 struct Turn {
     float2 c[2], s[2], ns[2];           // ns = -s
     int turning;
-    __device__ __forceinline__ void apply(Eight& v) const {
-        if (turning == 4) {
+    __device__ __forceinline__ void apply(Eight& v, bool all) const {
+        if (all || turning == 4) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float2 p = fma2(v.q[i], ns[i], mul2(v.p[i], c[i])), q = fma2(v.p[i], s[i], mul2(v.q[i], c[i]));
@@ -163,21 +165,21 @@ struct Turn {
     }
 };
 
-// A warp takes the rows of q, or those of k, of one token, or one of the parts that they come in: its lanes
-// make the token's table of cosines (each angle once), each lane keeps its own four for every row, and
-// groups of G lanes take the rows, kRows of them in flight.
+// A group of G lanes takes the rows of q, or those of k, of one token, or one of the parts that they come in;
+// the groups of a warp take neighbouring tokens. A group makes its token's table of cosines (each angle
+// once), each lane keeps its own four for every row, and kRows rows are in flight.
 template <int G, int kLayout, bool kBackward, typename Tx>
 __global__ void __launch_bounds__(kThreads, kBackward && sizeof(Tx) == 4 ? 2 : 3) heads_kernel(const Args p) {
-    extern __shared__ float2 tables[];              // [warps][rot / 2]
+    extern __shared__ float2 tables[];              // [groups][rot / 2]
     __shared__ float sums[kBackward ? kThreads * kVec : 1];
     constexpr int kGroups = 32 / G, kRows = kBackward ? 2 : 4, kWarps = kThreads / 32;
     const bool of_k = blockIdx.x >= p.side[0].blocks;
     const Side s = of_k ? p.side[1] : p.side[0];
     const unsigned block = of_k ? blockIdx.x - p.side[0].blocks : blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / G, gl = lane % G;
-    const bool on = gl * kVec < p.width;
+    const int warp = threadIdx.x >> 5, group = threadIdx.x % 32 / G, gl = threadIdx.x % G;
+    const bool on = gl * kVec < p.width, whole = p.width == G * kVec, all_turn = p.rot == p.width;
     const int pairs = p.rot / 2;
-    float2* table = tables + warp * pairs;
+    float2* table = tables + threadIdx.x / G * pairs;
     const float n_inv = p.norm == kRms ? 1.f / (float)p.width : 1.f;
     // half layout: the lanes of the rotated part take 4 features of each half, the others 8 in a row
     const bool halves = kLayout == kHalf && gl * kVec < p.rot;
@@ -195,33 +197,36 @@ __global__ void __launch_bounds__(kThreads, kBackward && sizeof(Tx) == 4 ? 2 : 3
         w = r.get();
     }
 
-    const unsigned items = p.tokens * s.parts;      // below 2^31
+    const unsigned items = (p.tokens + kGroups - 1) / kGroups * s.parts;   // below 2^31
     for (unsigned item = block * kWarps + warp; item < items; item += s.blocks * kWarps) {
-        const unsigned tok = item / s.parts, b = tok / p.T, t = tok - b * p.T;
-        if (p.lengths && (int)t >= p.lengths[b]) continue;
-        const int h0 = (item - tok * s.parts) * s.part_rows, h1 = min(h0 + s.part_rows, s.H);
+        const unsigned first = item / s.parts, tok = min(first * kGroups + group, p.tokens - 1);
+        const unsigned b = tok / p.T, t = tok - b * p.T;
+        const bool live = first * kGroups + group < p.tokens && (!p.lengths || (int)t < p.lengths[b]);
+        const bool full_warp = whole && __all_sync(0xffffffffu, live);
+        const int h0 = (item - first * s.parts) * s.part_rows, h1 = min(h0 + s.part_rows, s.H);
         const Tok3& to = kBackward ? s.sd : s.so;
-        const Tx* xp = static_cast<const Tx*>(s.x) + s.sx.at(b, t, h0 + group) + op;
-        const Tx* dp = kBackward ? static_cast<const Tx*>(s.dout) + s.so.at(b, t, h0 + group) + op : nullptr;
-        Tx* out = static_cast<Tx*>(s.out) + to.at(b, t, h0 + group) + op;
-        const int64_t xs = kGroups * s.sx.h, ds = kGroups * s.so.h, os = kGroups * to.h;
-        for (int r0 = h0; r0 < h1; r0 += kGroups * kRows) {   // every lane takes part in the sums
-            const int left = on ? h1 - r0 - group : 0;
-            Raw<kLayout, Tx> xr[kRows], dr[kBackward ? kRows : 1];
+        const Tx* xp = static_cast<const Tx*>(s.x) + s.sx.at(b, t, h0) + op;
+        const Tx* dp = kBackward ? static_cast<const Tx*>(s.dout) + s.so.at(b, t, h0) + op : nullptr;
+        Tx* out = static_cast<Tx*>(s.out) + to.at(b, t, h0) + op;
+        // the kRows rows from r0 on; `full`: they are all there, in every group, and every lane has its part of them
+        auto rows = [&](int r0, auto full) {
+            const int left = on && live ? h1 - r0 : 0;
+            Raw<kLayout, Tx> xr[kRows];
+            [[maybe_unused]] Raw<kLayout, Tx> dr[kBackward ? kRows : 1];
 #pragma unroll
-            for (int k = 0; k < kRows; ++k, xp += xs) {
-                xr[k].zero();
-                if (k * kGroups < left) xr[k].load(xp, d);
+            for (int k = 0; k < kRows; ++k, xp += s.sx.h) {
+                if (!full) xr[k].zero();
+                if (full || k < left) xr[k].load(xp, d);
                 if constexpr (kBackward) {
-                    dr[k].zero();
-                    if (k * kGroups < left) dr[k].load(dp, d);
-                    dp += ds;
+                    if (!full) dr[k].zero();
+                    if (full || k < left) dr[k].load(dp, d);
+                    dp += s.so.h;
                 }
             }
             if (pairs && r0 == h0) {                    // behind the first rows' loads
                 const double pos = (double)(p.positions ? p.positions[tok] : p.pos0 + (long long)t);
                 __syncwarp();                           // the last token's table has been read
-                for (int i = lane; i < pairs; i += 32) table[i] = cos_sin<Tx>(pos, p.freqs[i], p.amplitude);
+                for (int i = gl; i < pairs; i += G) table[i] = cos_sin<Tx>(pos, p.freqs[i], p.amplitude);
                 __syncwarp();
                 if (turn.turning) {
                     const float2* mine = table + gl * 4;
@@ -237,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, kBackward && sizeof(Tx) == 4 ? 2 : 3
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kRows; ++k, out += os) {
-                if (r0 + k * kGroups >= h1) break;
+            for (int k = 0; k < kRows; ++k, out += to.h) {
+                if (!full && r0 + k >= h1) break;   // every lane takes part in the sums
                 const Eight v = xr[k].get();
                 float inv = 1.f;
                 if (p.norm != kNoNorm) {
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, kBackward && sizeof(Tx) == 4 ? 2 : 3
                     for (int i = 0; i < 2; ++i) y.p[i] = mul2(v.p[i], f), y.q[i] = mul2(v.q[i], f);
                 } else {
                     y = dr[k].get();
-                    turn.apply(y);
+                    turn.apply(y, all_turn);
                     const float2 f = all2(s.scale);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) y.p[i] = mul2(y.p[i], f), y.q[i] = mul2(y.q[i], f);
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, kBackward && sizeof(Tx) == 4 ? 2 : 3
                     for (int i = 0; i < 2; ++i) y.p[i] = mul2(y.p[i], w.p[i]), y.q[i] = mul2(y.q[i], w.q[i]);
                 }
                 if constexpr (!kBackward) {
-                    turn.apply(y);
+                    turn.apply(y, all_turn);
                 } else if (p.norm != kNoNorm) {
                     const float2 g = all2(-group_sum<G>(dot(y, v)) * (inv * inv * n_inv));
 #pragma unroll
@@ -279,8 +284,12 @@ __global__ void __launch_bounds__(kThreads, kBackward && sizeof(Tx) == 4 ? 2 : 3
                         y.q[i] = mul2(inv2, fma2(v.q[i], g, y.q[i]));
                     }
                 }
-                if (k * kGroups < left) put<kLayout>(out, d, y);
+                if (full || k < left) put<kLayout>(out, d, y);
             }
+        };
+        for (int r0 = h0; r0 < h1; r0 += kRows) {
+            if (full_warp && r0 + kRows <= h1) rows(r0, std::true_type{});
+            else rows(r0, std::false_type{});
         }
     }
     if constexpr (kBackward) {                      // this CTA's part of dw, groups and warps in order

@@ -1795,8 +1795,8 @@ int check_qk(const osdn_qk_params* p) {
     return OSDN_OK;
 }
 
-// How the rows of q and of k go to CTAs of 8 warps. A token's rows come in parts, a warp each: enough that
-// every SM gets 16 warps, each with at least the rows that a warp has in flight at a time.
+// How the rows of q and of k go to CTAs of 8 warps. A token's rows come in parts, a group of lanes each:
+// enough that every SM gets 16 warps, each with at least the rows that it has in flight at a time.
 struct QkShape {
     int lanes;
     struct {
@@ -1807,9 +1807,12 @@ struct QkShape {
 QkShape qk_shape(const osdn_qk_params* p, bool backward) {
     QkShape q;
     q.lanes = p->width <= 64 ? 8 : p->width <= 128 ? 16 : 32;
-    const int flight = 32 / q.lanes * (backward ? 2 : 4), sms = sm_count(), H = p->Hq + p->Hk;
-    const int64_t tokens = (int64_t)p->B * p->T, warps = osdn::heads::kThreads / 32;
-    const int64_t want = tokens ? (16LL * sms + 2 * tokens - 1) / (2 * tokens) : 1;
+    constexpr int kWarps = osdn::heads::kThreads / 32;
+    constexpr int kStart = 4;     // what a token costs besides its rows, in rows
+    const int flight = backward ? 2 : 4, groups = 32 / q.lanes, sms = sm_count();
+    const int64_t turns = ((int64_t)p->B * p->T + groups - 1) / groups;   // a warp's tokens at a time
+    const int64_t want = turns ? (16LL * sms + 2 * turns - 1) / (2 * turns) : 1;
+    const int total = p->Hq + kStart + (p->Hk ? p->Hk + kStart : 0);
     for (int i = 0; i < 2; ++i) {
         const int rows = i ? p->Hk : p->Hq;
         auto& s = q.side[i];
@@ -1820,11 +1823,11 @@ QkShape qk_shape(const osdn_qk_params* p, bool backward) {
         const int parts = (int)std::min<int64_t>((rows + flight - 1) / flight, want);
         s.part_rows = ((rows + parts - 1) / parts + flight - 1) / flight * flight;
         s.parts = (rows + s.part_rows - 1) / s.part_rows;
-        const int64_t blocks = (tokens * s.parts + warps - 1) / warps;
-        // shared by rows between q and k: about what runs at a time in the backward, where each CTA leaves a row
+        const int64_t blocks = (turns * s.parts + kWarps - 1) / kWarps;
+        // shared by their cost between q and k: what runs at a time in the backward, where each CTA leaves a row
         // of partial weight gradients; some waves of it in the forward
-        static const int64_t waves = getenv("QK_WAVES") ? atoi(getenv("QK_WAVES")) : 4;
-        const int64_t most = std::max<int64_t>(1, (backward ? 3LL : 3LL * waves) * sms * rows / H);
+        static const int64_t waves = getenv("QK_WAVES") ? atoi(getenv("QK_WAVES")) : 2;
+        const int64_t most = std::max<int64_t>(1, 3LL * (backward ? 1 : waves) * sms * (rows + kStart) / total);
         s.blocks = (unsigned)std::min(blocks, most);
     }
     return q;
@@ -1841,7 +1844,7 @@ template <bool kBackward> int launch_heads(const osdn_qk_params* p, osdn::heads:
     }
     auto go = [&](auto g, auto layout, auto tx) {
         heads_kernel<g, layout, kBackward, decltype(tx)>
-            <<<q.side[0].blocks + q.side[1].blocks, kThreads, kThreads / 32 * sizeof(float2) * (a.rot / 2), st>>>(a);
+            <<<q.side[0].blocks + q.side[1].blocks, kThreads, kThreads / g * sizeof(float2) * (a.rot / 2), st>>>(a);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "head norm and rotation launch");
     };
