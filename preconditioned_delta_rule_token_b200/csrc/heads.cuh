@@ -169,10 +169,10 @@ struct Turn {
 // the groups of a warp take neighbouring tokens. A group makes its token's table of cosines (each angle
 // once), each lane keeps its own four for every row, and kRows rows are in flight.
 template <int G, int kLayout, bool kBackward, typename Tx>
-__global__ void __launch_bounds__(kThreads, kBackward && sizeof(Tx) == 4 ? 2 : 3) heads_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) heads_kernel(const Args p) {
     extern __shared__ float2 tables[];              // [groups][rot / 2]
     __shared__ float sums[kBackward ? kThreads * kVec : 1];
-    constexpr int kGroups = 32 / G, kRows = kBackward ? 2 : 4, kWarps = kThreads / 32;
+    constexpr int kGroups = 32 / G, kRows = 4, kWarps = kThreads / 32;
     const bool of_k = blockIdx.x >= p.side[0].blocks;
     const Side s = of_k ? p.side[1] : p.side[0];
     const unsigned block = of_k ? blockIdx.x - p.side[0].blocks : blockIdx.x;

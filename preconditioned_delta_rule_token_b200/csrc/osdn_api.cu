@@ -1809,7 +1809,7 @@ QkShape qk_shape(const osdn_qk_params* p, bool backward) {
     q.lanes = p->width <= 64 ? 8 : p->width <= 128 ? 16 : 32;
     constexpr int kWarps = osdn::heads::kThreads / 32;
     constexpr int kStart = 4;     // what a token costs besides its rows, in rows
-    const int flight = backward ? 2 : 4, groups = 32 / q.lanes, sms = sm_count();
+    const int flight = 4, groups = 32 / q.lanes, sms = sm_count();
     const int64_t turns = ((int64_t)p->B * p->T + groups - 1) / groups;   // a warp's tokens at a time
     const int64_t want = turns ? (16LL * sms + 2 * turns - 1) / (2 * turns) : 1;
     const int total = p->Hq + kStart + (p->Hk ? p->Hk + kStart : 0);
@@ -1827,7 +1827,7 @@ QkShape qk_shape(const osdn_qk_params* p, bool backward) {
         // shared by their cost between q and k: what runs at a time in the backward, where each CTA leaves a row
         // of partial weight gradients; some waves of it in the forward
         static const int64_t waves = getenv("QK_WAVES") ? atoi(getenv("QK_WAVES")) : 2;
-        const int64_t most = std::max<int64_t>(1, 3LL * (backward ? 1 : waves) * sms * (rows + kStart) / total);
+        const int64_t most = std::max<int64_t>(1, (backward ? 2LL : 3LL * waves) * sms * (rows + kStart) / total);
         s.blocks = (unsigned)std::min(blocks, most);
     }
     return q;
