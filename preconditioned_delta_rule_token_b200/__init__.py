@@ -29,7 +29,7 @@ from ._binding import (OSDN_BF16, OSDN_ERR_CUDA, OSDN_ERR_INVALID_ARG, OSDN_ERR_
                        osdn_recur_params, osdn_recur_fwd, osdn_recur_bwd, osdn_recur_bwd_workspace_size,
                        osdn_recur_step, osdn_qk_params, osdn_qk_fwd, osdn_qk_bwd, osdn_qk_bwd_workspace_size,
                        osdn_rope, osdn_rope_freqs)
-from ._layer import (qk_norm, qk_norm_backward, recurrence, recurrence_backward, recurrence_step, rope,
+from ._layer import (QkNorm, qk_norm, qk_norm_backward, recurrence, recurrence_backward, recurrence_step, rope,
                      rope_frequencies)
 
 __all__ = ["forward", "backward", "step", "osdn_bwd", "osdn_bwd_gated", "osdn_bwd_workspace_size", "residual_ratio", "osdn_fwd_scan_diag", "osdn_fwd", "osdn_fwd_scan", "osdn_fwd_chunk", "osdn_step", "osdn_fwd_workspace_size", "osdn_fwd_segments", "osdn_fwd_launches", "osdn_sync_status",
@@ -38,19 +38,22 @@ __all__ = ["forward", "backward", "step", "osdn_bwd", "osdn_bwd_gated", "osdn_bw
            "forward_host", "osdn_params", "make_params", "get_last_error", "OsdnError", "build", "LIB_PATH",
            "OSDN_OK", "OSDN_ERR_INVALID_ARG", "OSDN_ERR_UNSUPPORTED", "OSDN_ERR_CUDA", "OSDN_ERR_TIMEOUT",
            "OSDN_BF16", "OSDN_FP32",
-           "recurrence", "recurrence_backward", "recurrence_step", "qk_norm", "qk_norm_backward", "rope",
+           "recurrence", "recurrence_backward", "recurrence_step", "QkNorm", "qk_norm", "qk_norm_backward", "rope",
            "rope_frequencies", "osdn_recur_params", "osdn_recur_fwd", "osdn_recur_bwd",
            "osdn_recur_bwd_workspace_size", "osdn_recur_step", "osdn_qk_params", "osdn_qk_fwd", "osdn_qk_bwd",
            "osdn_qk_bwd_workspace_size", "osdn_rope", "osdn_rope_freqs"]
 
 
 def forward(q, k, v, beta, r=None, d0=None, S0=None, eta=1e-2, chunk=64, workspace=None, stream=None,
-            apf_anchor=False, alpha=None):
+            apf_anchor=False, alpha=None, qk=None, positions=None):
     """OSDN forward. q, k [B,T,H,dk]; v [B,T,H,dv]; beta, r [B,T,H] (bf16 or fp32,
     one dtype); d0 [B,H,dk] and S0 [B,H,dv,dk] fp32 or None. apf_anchor: anchored
     APF, the retention pulls d toward d0 instead of 0. alpha [B,T,H] (same dtype): gated OSDN,
-    S_t = alpha_t S_{t-1} (I - beta k kw^T) + beta v kw^T (bf16, dk = dv = 128).
+    S_t = alpha_t S_{t-1} (I - beta k kw^T) + beta v kw^T (bf16, dk = dv = 128). qk (a QkNorm): q and k
+    first go through qk_norm with these options, at `positions` [B,T] int64 (None: 0, 1, ...).
     Returns (out [B,T,H,dv], final_S [B,H,dv,dk] fp32, final_d [B,H,dk] fp32)."""
+    if qk is not None:
+        q, k = qk.apply(q, k, positions, stream)
     B, T, H, dk = k.shape
     dv = v.shape[-1]
     p = make_params(B, T, H, dk, dv, k.dtype, eta, chunk, apf_anchor)
@@ -87,12 +90,17 @@ def forward_host(q, k, v, beta, r=None, d0=None, S0=None, eta=1e-2, chunk=64, gr
 
 
 def backward(q, k, v, beta, dout, r=None, d0=None, S0=None, dS_final=None, dd_final=None, eta=1e-2, chunk=64,
-             workspace=None, stream=None, apf_anchor=False, alpha=None):
+             workspace=None, stream=None, apf_anchor=False, alpha=None, qk=None, positions=None):
     """Gradients of L = sum(dout * out) + sum(dS_final * final_S) + sum(dd_final * final_d) for the
     forward() with the same inputs (plain or anchored APF; gated OSDN when alpha [B,T,H] is given).
     dout [B,T,H,dv] in the input dtype; dS_final [B,H,dv,dk], dd_final [B,H,dk] fp32 or None (= 0).
     Returns a dict with dq, dk, dv, dbeta, dr (None without r), dalpha (None without alpha) in the
-    input dtype and dd0 [B,H,dk], dS0 [B,H,dv,dk] fp32."""
+    input dtype and dd0 [B,H,dk], dS0 [B,H,dv,dk] fp32. With qk and positions as in forward(), dq and dk
+    are of the q and k before qk_norm (which may be column slices of a projection), and dwq, dwk [dk]
+    fp32 of its weights (None without) come too."""
+    if qk is not None:
+        given = q, k
+        q, k = qk.apply(q, k, positions, stream)
     B, T, H, dk = k.shape
     dv = v.shape[-1]
     p = make_params(B, T, H, dk, dv, k.dtype, eta, chunk, apf_anchor)
@@ -111,6 +119,8 @@ def backward(q, k, v, beta, dout, r=None, d0=None, S0=None, dS_final=None, dd_fi
         g["dalpha"] = torch.empty_like(alpha)
         osdn_bwd_gated(p, q, k, v, beta, r, alpha, d0, S0, dout, dS_final, dd_final, g["dq"], g["dk"], g["dv"],
                        g["dbeta"], g["dr"], g["dalpha"], g["dd0"], g["dS0"], workspace, stream)
+    if qk is not None:
+        g.update(qk.gradients(*given, g["dq"], g["dk"], positions, stream))
     return g
 
 
@@ -129,11 +139,16 @@ def residual_ratio(k, beta, r=None, d0=None, eta=1e-2, stream=None, apf_anchor=F
     return rho, q_geo, d
 
 
-def step(q, k, v, beta, S, d, r=None, eta=1e-2, stream=None, d_anchor=None, apf_anchor=False, alpha=None):
+def step(q, k, v, beta, S, d, r=None, eta=1e-2, stream=None, d_anchor=None, apf_anchor=False, alpha=None, qk=None,
+         positions=None):
     """One decode token for every (b, h): q, k [B,H,dk]; v [B,H,dv]; beta, r [B,H];
     S [B,H,dv,dk] and d [B,H,dk] fp32, updated in place. Anchored APF (apf_anchor, or a
     d_anchor [B,H,dk] fp32 given) pulls d toward d_anchor (ones when None); alpha [B,H] decays S
-    first (gated OSDN). Returns out [B,H,dv]."""
+    first (gated OSDN). qk (a QkNorm): q and k first go through qk_norm at `positions` [B] int64 (None: 0).
+    Returns out [B,H,dv]."""
+    if qk is not None:
+        q, k = (t.squeeze(1) for t in qk.apply(q.unsqueeze(1), k.unsqueeze(1),
+                                               None if positions is None else positions.unsqueeze(1), stream))
     B, H, dk = k.shape
     dv = v.shape[-1]
     p = make_params(B, 1, H, dk, dv, k.dtype, eta, apf_anchor=apf_anchor or d_anchor is not None)

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -273,6 +274,30 @@ def qk_norm_backward(q, k, dq_out, dk_out, freqs=None, positions=None, norm="l2"
         B.osdn_qk_bwd(p, q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, g["dq"], g["dk"], g["dwq"],
                       g["dwk"], workspace)
     return g
+
+
+@dataclass(frozen=True)
+class QkNorm:
+    """Options of qk_norm for forward(), backward() and step(), which then take q and k before it: the delta
+    rule wants keys of unit length."""
+    norm: str = "l2"
+    eps: float = 1e-6
+    wq: torch.Tensor | None = None
+    wk: torch.Tensor | None = None
+    freqs: torch.Tensor | None = None
+    layout: str = "half"
+    amplitude: float = 1.0
+    scale_q: float = 1.0
+    scale_k: float = 1.0
+
+    def _options(self):
+        return {f.name: getattr(self, f.name) for f in fields(self)}
+
+    def apply(self, q, k, positions=None, stream=None):
+        return qk_norm(q, k, positions=positions, stream=stream, **self._options())
+
+    def gradients(self, q, k, dq_out, dk_out, positions=None, stream=None):
+        return qk_norm_backward(q, k, dq_out, dk_out, positions=positions, stream=stream, **self._options())
 
 
 def rope(x, freqs, positions=None, layout="half", amplitude=1.0, scale=1.0, pos0=0, inverse=False, lengths=None,

@@ -1584,10 +1584,7 @@ int launch_recur(void (*kern)(osdn::recur::Args, osdn::recur::Maps), osdn::recur
     }
     const int64_t tiles = std::max<int64_t>(1, ((int64_t)a.T + tile - 1) / tile);
     int R = (int)std::min<int64_t>(kMaxCluster, tiles);
-    static const int envR = getenv("RECUR_R") ? atoi(getenv("RECUR_R")) : 0;
-    if (envR) R = std::min(R, envR);
     while (R > 1 && room[dev].clusters[R].load(std::memory_order_relaxed) < units) --R;
-    if (getenv("RECUR_V")) fprintf(stderr, "%s units %ld R %d room1 %d room2 %d room16 %d\n", what, (long)units, R, room[dev].clusters[1].load(), room[dev].clusters[2].load(), room[dev].clusters[16].load());
     a.R = R;
     shape(R);
     cfg.gridDim = dim3((unsigned)(units * R));
@@ -1825,9 +1822,8 @@ QkShape qk_shape(const osdn_qk_params* p, bool backward) {
         s.parts = (rows + s.part_rows - 1) / s.part_rows;
         const int64_t blocks = (turns * s.parts + kWarps - 1) / kWarps;
         // shared by their cost between q and k: what runs at a time in the backward, where each CTA leaves a row
-        // of partial weight gradients; some waves of it in the forward
-        static const int64_t waves = getenv("QK_WAVES") ? atoi(getenv("QK_WAVES")) : 2;
-        const int64_t most = std::max<int64_t>(1, (backward ? 2LL : 3LL * waves) * sms * (rows + kStart) / total);
+        // of partial weight gradients; two waves of it in the forward
+        const int64_t most = std::max<int64_t>(1, (backward ? 2LL : 6LL) * sms * (rows + kStart) / total);
         s.blocks = (unsigned)std::min(blocks, most);
     }
     return q;
