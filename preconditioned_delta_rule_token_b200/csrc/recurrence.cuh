@@ -330,7 +330,7 @@ __device__ __forceinline__ float2 join_runs(const float (*A)[W], const float (*E
 // Dynamic shared memory: the stages (128-byte aligned), then the cluster's slots [2][R][32] (none for one CTA).
 // Three tiles in flight or in use; two where three would leave one CTA to an SM.
 template <typename Tx, typename Tg> constexpr int fwd_stages() { return sizeof(Tx) + sizeof(Tg) == 6 ? 2 : 3; }
-template <typename Tx, typename Tg> constexpr int bwd_stages() { return sizeof(Tx) + sizeof(Tg) == 8 ? 2 : 3; }
+template <typename Tx, typename Tg> constexpr int bwd_stages() { return sizeof(Tg) == 4 ? 2 : 3; }
 template <typename Tx, typename Tg> constexpr int fwd_slots() {
     constexpr int run = fwd_run<Tx, Tg>();
     return fwd_stages<Tx, Tg>() * (kTileBytes<Tx>(run) + kTileBytes<Tg>(run));
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const Args p, const __
 // walks back for its lam, then forward through its states h_{t-1}, which start from the state that the
 // forward saved at the tile's start, and gives dx and dgate on the way.
 template <int kMode, typename Tx, typename Tg>
-__global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args p, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kThreads, kMode == kTma && sizeof(Tg) > sizeof(Tx) ? 3 : 2) bwd_kernel(const Args p, const __grid_constant__ Maps maps) {
     constexpr int kRun = kBwdRun, kStages = bwd_stages<Tx, Tg>(), kTile = kWarps * kRun;
     constexpr int kStep = channel_step<kMode, Tx>();
     static_assert(kTile == kSaved, "a saved state before each tile");
