@@ -423,6 +423,8 @@ typedef struct {
     int32_t gate_dtype;     /* osdn_dtype of gate (and dgate): dtype, or OSDN_FP32 */
     int32_t gate_form;      /* osdn_gate_form */
     int32_t input_scale;    /* osdn_input_scale */
+    int32_t zero_rest;      /* rows from a sequence's length on: 0 left as they were, else written as zeros */
+    int32_t reserved;       /* 0 */
     /* Element strides of x, gate and h over (b, t); the channels are contiguous.
      * Both zero: dense [B, T, D]. Otherwise 0 .. 2^38; those of h keep its rows
      * apart. stride_h is also the stride of dh in the backward; dx and dgate are
@@ -434,7 +436,8 @@ typedef struct {
 
 /* Forward. x, gate [B, T, D]; h0 [B, D] fp32 (NULL: zeros); lengths [B] int32 in
  * device memory (NULL: T each; a value is taken as 0 .. T): tokens from a
- * sequence's length on are not read, and their rows of h are left as they were.
+ * sequence's length on do not count, whatever they hold; p->zero_rest says what
+ * becomes of their rows of h.
  * h [B, T, D] (NULL: not written); final_h [B, D] fp32, the state after each
  * sequence's last token (h0 for length 0; nullable); checkpoints
  * [B, ceil(T / 64), D] fp32, the state before every 64th token, for the backward
@@ -452,7 +455,7 @@ int osdn_recur_fwd(const osdn_recur_params *p, const void *x, const void *gate, 
  * h0 and lengths, or NULL: the call runs the forward again for them, in a workspace
  * of osdn_recur_bwd_workspace_size() bytes (unused, and nullable, with checkpoints).
  * Where s_t = 0 in OSDN_INPUT_NORM (a_t = 1) the root's unbounded slope counts as
- * 0. Rows of dx and dgate from a sequence's length on are left as they were. Bitwise
+ * 0. Rows of dx and dgate from a sequence's length on go by p->zero_rest. Bitwise
  * reproducible. dx and dgate must not overlap an input.
  * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */
 int osdn_recur_bwd_workspace_size(const osdn_recur_params *p, size_t *bytes);
@@ -495,6 +498,8 @@ typedef struct {
     float eps;              /* >= 0 */
     float amplitude;        /* factor on the rotated features (1: a pure rotation) */
     float scale_q, scale_k; /* factors on q and k */
+    int32_t zero_rest;      /* rows from a sequence's length on: 0 left as they were, else written as zeros */
+    int32_t reserved;       /* 0 */
     int64_t pos0;           /* position of token 0 where positions is NULL */
     /* Element strides over (b, t, h), as in osdn_params: all zero for dense
      * [B, T, H, width], else non-negative multiples of 8; those of outputs keep
@@ -510,7 +515,7 @@ typedef struct {
  * fp32 (NULL: ones; not with OSDN_NORM_NONE). positions [B, T] int64, any sign
  * (NULL: pos0 + t); freqs [rot_dim / 2] fp64 in device memory (osdn_rope_freqs).
  * lengths [B] int32 (NULL: T each): tokens from a sequence's length on are not read
- * and their output rows are left as they were. q_out may be q itself, and k_out k, with
+ * and their output rows go by p->zero_rest. q_out may be q itself, and k_out k, with
  * the same strides; else the outputs must not overlap the inputs. All pointers
  * 16-byte aligned. k, wk, k_out are ignored when Hk = 0.
  * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */
@@ -521,8 +526,8 @@ int osdn_qk_fwd(const osdn_qk_params *p, const void *q, const void *k, const flo
 /* Gradients of L = <dq_out, q_out> + <dk_out, k_out>: dq, dk (dense, input dtype) and
  * dwq, dwk [width] fp32 (nullable each; sums over every live token and head in a
  * fixed order, so results are bitwise reproducible on one device). Same inputs
- * as the forward; rows of dq and dk from a sequence's length on are left as they
- * were. workspace: osdn_qk_bwd_workspace_size() bytes, 16-byte aligned, no
+ * as the forward; rows of dq and dk from a sequence's length on go by
+ * p->zero_rest. workspace: osdn_qk_bwd_workspace_size() bytes, 16-byte aligned, no
  * initialisation (nullable when dwq and dwk both are).
  * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */
 int osdn_qk_bwd_workspace_size(const osdn_qk_params *p, size_t *bytes);

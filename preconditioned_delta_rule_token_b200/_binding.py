@@ -44,7 +44,8 @@ class osdn_params(ctypes.Structure):
 class osdn_recur_params(ctypes.Structure):
     _fields_ = [("struct_size", ctypes.c_uint32), ("B", ctypes.c_int32), ("T", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32),
-                ("gate_form", ctypes.c_int32), ("input_scale", ctypes.c_int32), ("stride_x", ctypes.c_int64 * 2),
+                ("gate_form", ctypes.c_int32), ("input_scale", ctypes.c_int32), ("zero_rest", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("stride_x", ctypes.c_int64 * 2),
                 ("stride_gate", ctypes.c_int64 * 2), ("stride_h", ctypes.c_int64 * 2)]
 
 
@@ -53,7 +54,7 @@ class osdn_qk_params(ctypes.Structure):
                 ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("norm", ctypes.c_int32), ("layout", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("amplitude", ctypes.c_float), ("scale_q", ctypes.c_float),
-                ("scale_k", ctypes.c_float), ("pos0", ctypes.c_int64), ("stride_q", ctypes.c_int64 * 3),
+                ("scale_k", ctypes.c_float), ("zero_rest", ctypes.c_int32), ("reserved", ctypes.c_int32), ("pos0", ctypes.c_int64), ("stride_q", ctypes.c_int64 * 3),
                 ("stride_k", ctypes.c_int64 * 3), ("stride_out_q", ctypes.c_int64 * 3),
                 ("stride_out_k", ctypes.c_int64 * 3)]
 

@@ -93,10 +93,8 @@ def _strides(name, t, n):
     return st[:n]
 
 
-def _new(t, lengths=None):
-    """An uninitialised dense tensor like t; zeros where lengths leave rows unwritten."""
-    if lengths is not None:
-        return torch.zeros(t.shape, dtype=t.dtype, device=t.device)
+def _new(t):
+    """An uninitialised dense tensor like t."""
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
@@ -122,6 +120,7 @@ def _recur_params(x, gate, gate_form, input_scale, named, token=True):
     p.B, p.T, p.D, p.dtype, p.gate_dtype = nB, T, D, code, gcode
     p.gate_form = _choice("gate_form", gate_form, B.GATE_FORMS)
     p.input_scale = _choice("input_scale", input_scale, B.INPUT_SCALES)
+    p.zero_rest = not any(t is not None for name, t, _ in named if name == "h")   # our own outputs
     n = 2 if token else 1
     p.stride_x[:n], p.stride_gate[:n] = _strides("x", x, n), _strides("gate", gate, n)
     for name, t, kind in named:
@@ -152,7 +151,7 @@ def recurrence(x, gate, h0=None, lengths=None, gate_form="decay", input_scale="n
     nB, T, D = x.shape
     with _scope(x.device, stream):
         if h is None:
-            h = _new(x, lengths)
+            h = _new(x)
         final_h = torch.empty((nB, D), dtype=torch.float32, device=x.device)
         marks = torch.empty(_saved(nB, T, D), dtype=torch.float32, device=x.device) if checkpoints else None
         B.osdn_recur_fwd(p, x, gate, h0, lengths, h, final_h, marks)
@@ -174,7 +173,7 @@ def recurrence_backward(x, gate, dh, h0=None, dfinal_h=None, lengths=None, check
         (("h0", h0, "state"), ("lengths", lengths, "lengths"), ("dh", dh, "token"), ("dfinal_h", dfinal_h, "state"),
          ("checkpoints", checkpoints, "saved"))))
     with _scope(x.device, stream):
-        g = {"dx": _new(x, lengths), "dgate": _new(gate, lengths),
+        g = {"dx": _new(x), "dgate": _new(gate),
              "dh0": torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device)}
         if checkpoints is None and workspace is None:
             workspace = torch.empty(B.osdn_recur_bwd_workspace_size(p), dtype=torch.uint8, device=x.device)
@@ -210,6 +209,7 @@ def _heads_params(q, k, freqs, positions, lengths, norm, layout, wq, wk, out_q, 
     p.B, p.T, p.Hq, p.Hk, p.width, p.dtype = nB, T, Hq, Hk, width, _dtype(names[0], q)
     p.norm, p.layout = _choice("norm", norm, B.NORMS), _choice("layout", layout, B.ROPE_LAYOUTS)
     p.eps, p.amplitude, p.scale_q, p.scale_k, p.pos0 = numbers
+    p.zero_rest = names[2].startswith("d") or (out_q is None and out_k is None)   # our own outputs
     if k is not None:
         _held(dev, names[1], k, (nB, T, Hk, width), q.dtype, dense=False)
         _held(dev, names[3], out_k, k.shape, q.dtype, dense=False)
@@ -244,10 +244,11 @@ def qk_norm(q, k, freqs=None, positions=None, norm="l2", eps=1e-6, wq=None, wk=N
     p = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
         q, k, freqs, positions, lengths, norm, layout, wq, wk, q_out, k_out, numbers, ("q", "k", "q_out", "k_out")))
     with _scope(q.device, stream):
+        both = lengths is None or (q_out is None and k_out is None)
         if q_out is None:
-            q_out = _new(q, lengths)
+            q_out = _new(q) if both else torch.zeros(q.shape, dtype=q.dtype, device=q.device)
         if k is not None and k_out is None:
-            k_out = _new(k, lengths)
+            k_out = _new(k) if both else torch.zeros(k.shape, dtype=k.dtype, device=k.device)
         B.osdn_qk_fwd(p, q, k, wq, wk, positions, freqs, lengths, q_out, k_out)
     return q_out, k_out
 
@@ -266,7 +267,7 @@ def qk_norm_backward(q, k, dq_out, dk_out, freqs=None, positions=None, norm="l2"
     p = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
         q, k, freqs, positions, lengths, norm, layout, wq, wk, dq_out, dk_out, numbers, ("q", "k", "dq_out", "dk_out")))
     with _scope(q.device, stream):
-        g = {"dq": _new(q, lengths), "dk": None if k is None else _new(k, lengths),
+        g = {"dq": _new(q), "dk": None if k is None else _new(k),
              "dwq": None if wq is None else torch.empty_like(wq),
              "dwk": None if wk is None or k is None else torch.empty_like(wk)}
         if workspace is None and (g["dwq"] is not None or g["dwk"] is not None):
@@ -315,7 +316,7 @@ def rope(x, freqs, positions=None, layout="half", amplitude=1.0, scale=1.0, pos0
                                            numbers, ("x", None, "out", None)))
     with _scope(x.device, stream):
         if out is None:
-            out = _new(x, lengths)
+            out = _new(x)
         B.osdn_rope(p, x, positions, freqs, lengths, out, inverse)
     return out
 

@@ -43,7 +43,7 @@ struct Args {
     const int* lengths;             // [B] or NULL
     long long pos0;
     unsigned tokens;                // B * T
-    int T, width, rot, norm, layout, inverse;
+    int T, width, rot, norm, layout, inverse, zero_rest;
     float eps, amplitude;
 };
 
@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) heads_kernel(cons
     for (unsigned item = block * kWarps + warp; item < items; item += s.blocks * kWarps) {
         const unsigned first = item / s.parts, tok = min(first * kGroups + group, p.tokens - 1);
         const unsigned b = tok / p.T, t = tok - b * p.T;
-        const bool live = first * kGroups + group < p.tokens && (!p.lengths || (int)t < p.lengths[b]);
+        const bool there = first * kGroups + group < p.tokens;
+        const bool live = there && (!p.lengths || (int)t < p.lengths[b]);
         const bool full_warp = whole && __all_sync(0xffffffffu, live);
         const int h0 = (item - first * s.parts) * s.part_rows, h1 = min(h0 + s.part_rows, s.H);
         const Tok3& to = kBackward ? s.sd : s.so;
@@ -210,7 +211,8 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) heads_kernel(cons
         Tx* out = static_cast<Tx*>(s.out) + to.at(b, t, h0) + op;
         // the kRows rows from r0 on; `full`: they are all there, in every group, and every lane has its part of them
         auto rows = [&](int r0, auto full) {
-            const int left = on && live ? h1 - r0 : 0;
+            // rows read, and rows written: those behind a length come out as zeros of zeros
+            const int left = on && live ? h1 - r0 : 0, wanted = on && there && (live || p.zero_rest) ? h1 - r0 : 0;
             Raw<kLayout, Tx> xr[kRows];
             [[maybe_unused]] Raw<kLayout, Tx> dr[kBackward ? kRows : 1];
 #pragma unroll
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) heads_kernel(cons
                         y.q[i] = mul2(inv2, fma2(v.q[i], g, y.q[i]));
                     }
                 }
-                if (full || k < left) put<kLayout>(out, d, y);
+                if (full || k < wanted) put<kLayout>(out, d, y);
             }
         };
         for (int r0 = h0; r0 < h1; r0 += kRows) {

@@ -1452,6 +1452,7 @@ int check_recur(const osdn_recur_params* p, bool step) {
         return fail(OSDN_ERR_INVALID_ARG, "unknown gate_form %d", p->gate_form);
     if (p->input_scale < OSDN_INPUT_NONE || p->input_scale > OSDN_INPUT_NORM)
         return fail(OSDN_ERR_INVALID_ARG, "unknown input_scale %d", p->input_scale);
+    if (p->reserved) return fail(OSDN_ERR_INVALID_ARG, "reserved must be 0");
     for (const int64_t* st : {p->stride_x, p->stride_gate, p->stride_h})
         for (int i = 0; i < 2; ++i)
             if (st[i] < 0 || st[i] > ((int64_t)1 << 38))
@@ -1473,6 +1474,7 @@ int check_h_rows(const osdn_recur_params* p, bool step) {
 osdn::recur::Args recur_args(const osdn_recur_params* p) {
     osdn::recur::Args a{};
     a.B = p->B; a.T = p->T; a.D = p->D; a.form = p->gate_form; a.scale = p->input_scale;
+    a.zero_rest = p->zero_rest;
     const Str2 x = recur_strides(p, p->stride_x), g = recur_strides(p, p->stride_gate),
                h = recur_strides(p, p->stride_h);
     if (p->B > 1) a.xb = x.b, a.gb = g.b, a.hb = h.b;   // a stride over one element is not used: 0
@@ -1776,6 +1778,7 @@ int check_qk(const osdn_qk_params* p) {
         return fail(OSDN_ERR_INVALID_ARG, "rot_dim must be even, 0 .. width (got %d)", p->rot_dim);
     if (p->layout == OSDN_ROPE_HALF && p->rot_dim % 8)
         return fail(OSDN_ERR_UNSUPPORTED, "the half layout takes rot_dim in multiples of 8 (got %d)", p->rot_dim);
+    if (p->reserved) return fail(OSDN_ERR_INVALID_ARG, "reserved must be 0");
     if (!(p->eps >= 0.f)) return fail(OSDN_ERR_INVALID_ARG, "eps must be >= 0");
     if (!(std::isfinite(p->amplitude) && std::isfinite(p->scale_q) && std::isfinite(p->scale_k)))
         return fail(OSDN_ERR_INVALID_ARG, "amplitude, scale_q and scale_k must be finite");
@@ -1865,7 +1868,7 @@ osdn::heads::Args heads_args(const osdn_qk_params* p, const int64_t* positions, 
     a.pos0 = p->pos0;
     a.tokens = (unsigned)p->B * p->T;
     a.T = p->T; a.width = p->width; a.rot = p->rot_dim; a.norm = p->norm; a.layout = p->layout;
-    a.eps = p->eps; a.amplitude = p->amplitude;
+    a.eps = p->eps; a.amplitude = p->amplitude; a.zero_rest = p->zero_rest;
     a.side[0].H = p->Hq; a.side[0].scale = p->scale_q;
     a.side[1].H = p->Hk; a.side[1].scale = p->scale_k;
     a.side[0].sx = qk_strides(p, p->stride_q, p->Hq);

@@ -124,7 +124,7 @@ struct Args {
     const int* lengths;
     void *h, *dx, *dgate;
     float *final_h, *ckpt, *dh0;
-    int B, T, D, form, scale, cblocks, R;
+    int B, T, D, form, scale, cblocks, R, zero_rest;
     unsigned long long wait_limit_ns;
     int64_t xb, xt, gb, gt, hb, ht;     // element strides of x, gate and h (or dh) over (b, t)
 };
@@ -448,6 +448,8 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const Args p, const __
             }
         }
     }
+    if (h && p.zero_rest)
+        for (int t = len + rank * kWarps + warp; t < p.T; t += R * kWarps) put_pair<kStep>(h + t * p.ht, all2(0.f), n);
     if (warp == 0 && rank == 0 && p.final_h) put_pair<kStep>(p.final_h + (int64_t)b * p.D + c, carry, n);
     if constexpr (kMode == kTma) {
         pipe.drain(0, steps);
@@ -619,6 +621,11 @@ __global__ void __launch_bounds__(kThreads, kMode == kTma && sizeof(Tg) > sizeof
             }
         }
     }
+    if (p.zero_rest)
+        for (int t = len + rank * kWarps + warp; t < p.T; t += R * kWarps) {
+            put_pair<kStep>(dx + (int64_t)t * p.D, all2(0.f), n);
+            put_pair<kStep>(dgate + (int64_t)t * p.D, all2(0.f), n);
+        }
     if (warp == 0 && rank == 0 && p.dh0) put_pair<kStep>(p.dh0 + (int64_t)b * p.D + c, carry, n);
     if constexpr (kMode == kTma) {
         pipe.drain(0, steps);

@@ -100,14 +100,14 @@ def test_arguments_are_checked_on_the_host(osdn_lib):
     B, L = osdn_lib, osdn_lib.lib()
     n = ctypes.c_size_t(0)
     inv, uns, nan = B.OSDN_ERR_INVALID_ARG, B.OSDN_ERR_UNSUPPORTED, float("nan")
-    assert ctypes.sizeof(B.osdn_qk_params) == 160
+    assert ctypes.sizeof(B.osdn_qk_params) == 168
     assert L.osdn_qk_bwd_workspace_size(_params(B), ctypes.byref(n)) == 0 and n.value >= 2 * 128 * 4
     for kw, code in ((dict(B=0), inv), (dict(T=-1), inv), (dict(Hq=0), inv), (dict(Hk=-1), inv), (dict(width=0), inv),
                      (dict(width=100), uns), (dict(width=264, rot_dim=0), uns), (dict(dtype=5), inv), (dict(norm=3), inv),
                      (dict(layout=2), inv), (dict(rot_dim=63), inv), (dict(rot_dim=130), inv), (dict(rot_dim=20), uns),
                      (dict(eps=-1.0), inv), (dict(eps=nan), inv), (dict(amplitude=nan), inv),
                      (dict(scale_q=float("inf")), inv), (dict(stride_q=(4, 0, 0)), inv),
-                     (dict(stride_out_k=(-8, 8, 8)), inv), (dict(B=1 << 20, T=1 << 20), inv)):
+                     (dict(stride_out_k=(-8, 8, 8)), inv), (dict(B=1 << 20, T=1 << 20), inv), (dict(reserved=1), inv)):
         assert L.osdn_qk_bwd_workspace_size(_params(B, **kw), ctypes.byref(n)) == code, kw
         assert B.get_last_error()
 
@@ -299,10 +299,17 @@ def test_lengths_and_rows_of_zeros():
     pk.qk_norm(nan_q, None, lengths=lengths.cuda(), q_out=out, **how)
     want = pk.qk_norm(q.cuda(), None, **how)[0]
     assert torch.equal(out, torch.where(inside.cuda(), want, 3.0))
+    for eps in (1e-6, 0.0):   # without q_out: zeros there
+        own = pk.qk_norm(nan_q, nan_q, lengths=lengths.cuda(), eps=eps, **how)
+        assert all(bool((t[~inside.expand_as(q).cuda()] == 0).all()) and bool(torch.isfinite(t).all()) for t in own)
+    own = pk.qk_norm(nan_q, nan_q, lengths=lengths.cuda(), q_out=out.fill_(3.0), **how)
+    assert bool((own[1][~inside.expand_as(q).cuda()] == 0).all())
+    assert torch.equal(out, torch.where(inside.cuda(), want, 3.0))
     got = pk.qk_norm_backward(nan_q, None, nan_d, None, lengths=lengths.cuda(), **how)
     a = ("rms", 1e-6, 1.0, ref.plain_freqs(32), ref.positions_of(B, T), "half", 1.0)
     dx, dw = ref.head_norm_grads(torch.where(inside, q, 1.0), w, torch.where(inside, dq, 0.0), *a)
     ref.close(got["dq"], *dx, 96, "dq")
+    assert bool((got["dq"][~inside.expand_as(q).cuda()] == 0).all())
     ref.close(got["dwq"], *dw, B * T * H + 96, "dwq")
     z = torch.zeros(1, 2, 2, 64, device="cuda")
     for eps in (0.0, 1e-6):

@@ -73,13 +73,13 @@ def _params(lib_, **kw):
 def test_arguments_are_checked_on_the_host(osdn_lib):
     B, L = osdn_lib, osdn_lib.lib()
     n = ctypes.c_size_t(0)
-    assert ctypes.sizeof(B.osdn_recur_params) == 80
+    assert ctypes.sizeof(B.osdn_recur_params) == 88
     assert L.osdn_recur_bwd_workspace_size(_params(B), ctypes.byref(n)) == 0 and n.value >= 2 * 2 * 48 * 4
     inv, uns = B.OSDN_ERR_INVALID_ARG, B.OSDN_ERR_UNSUPPORTED
     for kw, code in ((dict(B=0), inv), (dict(T=-1), inv), (dict(D=0), inv), (dict(D=1 << 25), inv), (dict(dtype=2), inv),
                      (dict(gate_dtype=7), inv), (dict(dtype=1, gate_dtype=0), uns), (dict(gate_form=3), inv),
                      (dict(input_scale=-1), inv), (dict(stride_x=(-8, 48)), inv), (dict(stride_h=(1 << 39, 48)), inv),
-                     (dict(T=(1 << 30) + 1), inv), (dict(B=1 << 30, D=1 << 20, T=1), inv)):
+                     (dict(T=(1 << 30) + 1), inv), (dict(reserved=1), inv), (dict(B=1 << 30, D=1 << 20, T=1), inv)):
         assert L.osdn_recur_bwd_workspace_size(_params(B, **kw), ctypes.byref(n)) == code, kw
         assert B.get_last_error()
     p = _params(B)
@@ -183,6 +183,9 @@ def test_lengths_leave_later_rows_alone(D):
     for b in range(7):
         assert bool((h[b, n[b]:] == 7.0).all()) and bool(torch.isfinite(h[b]).all())
         assert bool(torch.isfinite(g["dx"][b]).all()) and bool((g["dgate"][b, n[b]:] == 0).all())
+        assert bool((g["dx"][b, n[b]:] == 0).all())
+    own = pk.recurrence(xs, gs, h0=hs, lengths=ns)[0]   # without h: zeros there
+    assert all(bool((own[b, n[b]:] == 0).all()) and torch.equal(own[b, :n[b]], h[b, :n[b]]) for b in range(7))
 
 
 @pytest.mark.gpu
