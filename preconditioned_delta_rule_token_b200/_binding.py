@@ -386,7 +386,7 @@ def _handle(stream):
 
 def osdn_recur_fwd(params, x, gate, h0, lengths, h, final_h, checkpoints, stream=None):
     """Raw C-ABI call of the gated linear recurrence (every tensor preallocated; strides in params)."""
-    _check(lib().osdn_recur_fwd(params, _address(x), _address(gate), _address(h0), _address(lengths), _address(h),
+    _check(lib().osdn_recur_fwd(params, x.data_ptr(), gate.data_ptr(), _address(h0), _address(lengths), _address(h),
                                 _address(final_h), _address(checkpoints), _handle(stream)))
 
 
@@ -398,20 +398,20 @@ def osdn_recur_bwd_workspace_size(params: osdn_recur_params) -> int:
 
 def osdn_recur_bwd(params, x, gate, h0, lengths, dh, dfinal_h, checkpoints, dx, dgate, dh0, workspace, stream=None):
     """Raw C-ABI call of the recurrence's backward."""
-    _check(lib().osdn_recur_bwd(params, _address(x), _address(gate), _address(h0), _address(lengths), _address(dh),
-                                _address(dfinal_h), _address(checkpoints), _address(dx), _address(dgate),
+    _check(lib().osdn_recur_bwd(params, x.data_ptr(), gate.data_ptr(), _address(h0), _address(lengths), dh.data_ptr(),
+                                _address(dfinal_h), _address(checkpoints), dx.data_ptr(), dgate.data_ptr(),
                                 _address(dh0), _address(workspace), _ws_bytes(workspace), _handle(stream)))
 
 
 def osdn_recur_step(params, x, gate, state, h, stream=None):
     """Raw C-ABI call: one token of the recurrence, state updated in place."""
-    _check(lib().osdn_recur_step(params, _address(x), _address(gate), _address(state), _address(h), _handle(stream)))
+    _check(lib().osdn_recur_step(params, x.data_ptr(), gate.data_ptr(), state.data_ptr(), h.data_ptr(), _handle(stream)))
 
 
 def osdn_qk_fwd(params, q, k, wq, wk, positions, freqs, lengths, q_out, k_out, stream=None):
     """Raw C-ABI call of the query and key norms with the rotation (strides in params)."""
-    _check(lib().osdn_qk_fwd(params, _address(q), _address(k), _address(wq), _address(wk), _address(positions),
-                             _address(freqs), _address(lengths), _address(q_out), _address(k_out), _handle(stream)))
+    _check(lib().osdn_qk_fwd(params, q.data_ptr(), _address(k), _address(wq), _address(wk), _address(positions),
+                             _address(freqs), _address(lengths), q_out.data_ptr(), _address(k_out), _handle(stream)))
 
 
 def osdn_qk_bwd_workspace_size(params: osdn_qk_params) -> int:
@@ -423,16 +423,16 @@ def osdn_qk_bwd_workspace_size(params: osdn_qk_params) -> int:
 def osdn_qk_bwd(params, q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
                 stream=None):
     """Raw C-ABI call of the backward of osdn_qk_fwd."""
-    _check(lib().osdn_qk_bwd(params, _address(q), _address(k), _address(wq), _address(wk), _address(positions),
-                             _address(freqs), _address(lengths), _address(dq_out), _address(dk_out), _address(dq),
+    _check(lib().osdn_qk_bwd(params, q.data_ptr(), _address(k), _address(wq), _address(wk), _address(positions),
+                             _address(freqs), _address(lengths), dq_out.data_ptr(), _address(dk_out), dq.data_ptr(),
                              _address(dk), _address(dwq), _address(dwk), _address(workspace), _ws_bytes(workspace),
                              _handle(stream)))
 
 
 def osdn_rope(params, x, positions, freqs, lengths, out, inverse=False, stream=None):
     """Raw C-ABI call of the rotation alone."""
-    _check(lib().osdn_rope(params, _address(x), _address(positions), _address(freqs), _address(lengths),
-                           _address(out), 1 if inverse else 0, _handle(stream)))
+    _check(lib().osdn_rope(params, x.data_ptr(), _address(positions), _address(freqs), _address(lengths),
+                           out.data_ptr(), 1 if inverse else 0, _handle(stream)))
 
 
 def osdn_rope_freqs(rot_dim, base, scaling, factor, original_length, low_turns, high_turns):

@@ -12,7 +12,6 @@ type, device) and are kept by them.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass, fields
 
@@ -22,7 +21,6 @@ from . import _binding as B
 from ._binding import OSDN_BF16, OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_FP32, OsdnError
 
 _DTYPES = {torch.bfloat16: OSDN_BF16, torch.float32: OSDN_FP32}
-_HERE = contextlib.nullcontext()
 
 
 def _bad(msg, code=OSDN_ERR_INVALID_ARG):
@@ -30,12 +28,13 @@ def _bad(msg, code=OSDN_ERR_INVALID_ARG):
 
 
 def _scope(dev, stream):
-    """Makes `stream` (None: the current one) of device `dev` current for allocations and the launch."""
+    """What makes `stream` (None: the current one) of device `dev` current for allocations and the launch; None
+    where that is so already."""
     if stream is not None:
         if stream.device != dev:
             _bad("the stream is of %s, the tensors are on %s" % (stream.device, dev))
         return torch.cuda.stream(stream)
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 class _Kept(dict):
@@ -149,12 +148,15 @@ def recurrence(x, gate, h0=None, lengths=None, gate_form="decay", input_scale="n
     p = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
         x, gate, gate_form, input_scale, (("h0", h0, "state"), ("lengths", lengths, "lengths"), ("h", h, "token"))))
     nB, T, D = x.shape
-    with _scope(x.device, stream):
-        if h is None:
-            h = _new(x)
-        final_h = torch.empty((nB, D), dtype=torch.float32, device=x.device)
-        marks = torch.empty(_saved(nB, T, D), dtype=torch.float32, device=x.device) if checkpoints else None
-        B.osdn_recur_fwd(p, x, gate, h0, lengths, h, final_h, marks)
+    scope = _scope(x.device, stream)
+    if scope is not None:
+        with scope:
+            return recurrence(x, gate, h0, lengths, gate_form, input_scale, checkpoints, h)
+    if h is None:
+        h = _new(x)
+    final_h = torch.empty((nB, D), dtype=torch.float32, device=x.device)
+    marks = torch.empty(_saved(nB, T, D), dtype=torch.float32, device=x.device) if checkpoints else None
+    B.osdn_recur_fwd(p, x, gate, h0, lengths, h, final_h, marks)
     return (h, final_h, marks) if checkpoints else (h, final_h)
 
 
@@ -172,12 +174,16 @@ def recurrence_backward(x, gate, dh, h0=None, dfinal_h=None, lengths=None, check
         x, gate, gate_form, input_scale,
         (("h0", h0, "state"), ("lengths", lengths, "lengths"), ("dh", dh, "token"), ("dfinal_h", dfinal_h, "state"),
          ("checkpoints", checkpoints, "saved"))))
-    with _scope(x.device, stream):
-        g = {"dx": _new(x), "dgate": _new(gate),
-             "dh0": torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device)}
-        if checkpoints is None and workspace is None:
-            workspace = torch.empty(B.osdn_recur_bwd_workspace_size(p), dtype=torch.uint8, device=x.device)
-        B.osdn_recur_bwd(p, x, gate, h0, lengths, dh, dfinal_h, checkpoints, g["dx"], g["dgate"], g["dh0"], workspace)
+    scope = _scope(x.device, stream)
+    if scope is not None:
+        with scope:
+            return recurrence_backward(x, gate, dh, h0, dfinal_h, lengths, checkpoints, gate_form, input_scale,
+                                       workspace)
+    g = {"dx": _new(x), "dgate": _new(gate),
+         "dh0": torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device)}
+    if checkpoints is None and workspace is None:
+        workspace = torch.empty(B.osdn_recur_bwd_workspace_size(p), dtype=torch.uint8, device=x.device)
+    B.osdn_recur_bwd(p, x, gate, h0, lengths, dh, dfinal_h, checkpoints, g["dx"], g["dgate"], g["dh0"], workspace)
     return g
 
 
@@ -187,10 +193,13 @@ def recurrence_step(x, gate, state, gate_form="decay", input_scale="none", out=N
     key = ("step", gate_form, input_scale, _lay(x), _lay(gate), _lay(state), _lay(out))
     p = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
         x, gate, gate_form, input_scale, (("state", state, "state"), ("out", out, "token")), token=False))
-    with _scope(x.device, stream):
-        if out is None:
-            out = _new(x)
-        B.osdn_recur_step(p, x, gate, state, out)
+    scope = _scope(x.device, stream)
+    if scope is not None:
+        with scope:
+            return recurrence_step(x, gate, state, gate_form, input_scale, out)
+    if out is None:
+        out = _new(x)
+    B.osdn_recur_step(p, x, gate, state, out)
     return out
 
 
@@ -243,13 +252,17 @@ def qk_norm(q, k, freqs=None, positions=None, norm="l2", eps=1e-6, wq=None, wk=N
            _lay(q_out), _lay(k_out))
     p = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
         q, k, freqs, positions, lengths, norm, layout, wq, wk, q_out, k_out, numbers, ("q", "k", "q_out", "k_out")))
-    with _scope(q.device, stream):
-        both = lengths is None or (q_out is None and k_out is None)
-        if q_out is None:
-            q_out = _new(q) if both else torch.zeros(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = _new(k) if both else torch.zeros(k.shape, dtype=k.dtype, device=k.device)
-        B.osdn_qk_fwd(p, q, k, wq, wk, positions, freqs, lengths, q_out, k_out)
+    scope = _scope(q.device, stream)
+    if scope is not None:
+        with scope:
+            return qk_norm(q, k, freqs, positions, norm, eps, wq, wk, layout, amplitude, scale_q, scale_k, pos0, lengths,
+                           q_out, k_out)
+    both = lengths is None or (q_out is None and k_out is None)
+    if q_out is None:
+        q_out = _new(q) if both else torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = _new(k) if both else torch.zeros(k.shape, dtype=k.dtype, device=k.device)
+    B.osdn_qk_fwd(p, q, k, wq, wk, positions, freqs, lengths, q_out, k_out)
     return q_out, k_out
 
 
@@ -266,14 +279,18 @@ def qk_norm_backward(q, k, dq_out, dk_out, freqs=None, positions=None, norm="l2"
            _lay(dq_out), _lay(dk_out))
     p = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
         q, k, freqs, positions, lengths, norm, layout, wq, wk, dq_out, dk_out, numbers, ("q", "k", "dq_out", "dk_out")))
-    with _scope(q.device, stream):
-        g = {"dq": _new(q), "dk": None if k is None else _new(k),
-             "dwq": None if wq is None else torch.empty_like(wq),
-             "dwk": None if wk is None or k is None else torch.empty_like(wk)}
-        if workspace is None and (g["dwq"] is not None or g["dwk"] is not None):
-            workspace = torch.empty(B.osdn_qk_bwd_workspace_size(p), dtype=torch.uint8, device=q.device)
-        B.osdn_qk_bwd(p, q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, g["dq"], g["dk"], g["dwq"],
-                      g["dwk"], workspace)
+    scope = _scope(q.device, stream)
+    if scope is not None:
+        with scope:
+            return qk_norm_backward(q, k, dq_out, dk_out, freqs, positions, norm, eps, wq, wk, layout, amplitude, scale_q,
+                                    scale_k, pos0, lengths, workspace)
+    g = {"dq": _new(q), "dk": None if k is None else _new(k),
+         "dwq": None if wq is None else torch.empty_like(wq),
+         "dwk": None if wk is None or k is None else torch.empty_like(wk)}
+    if workspace is None and (g["dwq"] is not None or g["dwk"] is not None):
+        workspace = torch.empty(B.osdn_qk_bwd_workspace_size(p), dtype=torch.uint8, device=q.device)
+    B.osdn_qk_bwd(p, q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, g["dq"], g["dk"], g["dwq"],
+                  g["dwk"], workspace)
     return g
 
 
@@ -314,10 +331,13 @@ def rope(x, freqs, positions=None, layout="half", amplitude=1.0, scale=1.0, pos0
             _bad("freqs is needed")
         p = _HEADS.keep(key, _heads_params(x, None, freqs, positions, lengths, "none", layout, None, None, out, None,
                                            numbers, ("x", None, "out", None)))
-    with _scope(x.device, stream):
-        if out is None:
-            out = _new(x)
-        B.osdn_rope(p, x, positions, freqs, lengths, out, inverse)
+    scope = _scope(x.device, stream)
+    if scope is not None:
+        with scope:
+            return rope(x, freqs, positions, layout, amplitude, scale, pos0, inverse, lengths, out)
+    if out is None:
+        out = _new(x)
+    B.osdn_rope(p, x, positions, freqs, lengths, out, inverse)
     return out
 
 
