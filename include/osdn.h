@@ -481,7 +481,8 @@ int osdn_recur_step(const osdn_recur_params *p, const void *x, const void *gate,
  * (OSDN_ROPE_INTERLEAVED) turn:
  *     (y_i, y_j) <- amplitude (y_i cos - y_j sin, y_j cos + y_i sin),
  *     angle = position freqs[pair], formed in 64 bits.
- * Sums are fp32; a row whose sum and eps are both 0 gives zeros. */
+ * Sums are fp32; a row whose sum plus eps lies outside fp32's normal range (a row of
+ * zeros without eps, values near 1e19) gives zeros. */
 typedef enum { OSDN_NORM_NONE = 0, OSDN_NORM_L2 = 1, OSDN_NORM_RMS = 2 } osdn_norm;
 typedef enum { OSDN_ROPE_HALF = 0, OSDN_ROPE_INTERLEAVED = 1 } osdn_rope_layout;
 
@@ -512,8 +513,8 @@ typedef struct {
 } osdn_qk_params;
 
 /* Forward: q [B, T, Hq, width] to q_out, k [B, T, Hk, width] to k_out. wq, wk [width]
- * fp32 (NULL: ones; not with OSDN_NORM_NONE). positions [B, T] int64, any sign
- * (NULL: pos0 + t); freqs [rot_dim / 2] fp64 in device memory (osdn_rope_freqs).
+ * fp32 (NULL: ones; not with OSDN_NORM_NONE). positions [B, T] int64 within
+ * +-2^53 (NULL: pos0 + t); freqs [rot_dim / 2] fp64 in device memory (osdn_rope_freqs).
  * lengths [B] int32 (NULL: T each): tokens from a sequence's length on are not read
  * and their output rows go by p->zero_rest. q_out may be q itself, and k_out k, with
  * the same strides; else the outputs must not overlap the inputs. All pointers

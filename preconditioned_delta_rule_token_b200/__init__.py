@@ -54,6 +54,8 @@ def forward(q, k, v, beta, r=None, d0=None, S0=None, eta=1e-2, chunk=64, workspa
     Returns (out [B,T,H,dv], final_S [B,H,dv,dk] fp32, final_d [B,H,dk] fp32)."""
     if qk is not None:
         q, k = qk.apply(q, k, positions, stream)
+    elif positions is not None:
+        raise OsdnError(OSDN_ERR_INVALID_ARG, "positions need qk")
     B, T, H, dk = k.shape
     dv = v.shape[-1]
     p = make_params(B, T, H, dk, dv, k.dtype, eta, chunk, apf_anchor)
@@ -101,6 +103,8 @@ def backward(q, k, v, beta, dout, r=None, d0=None, S0=None, dS_final=None, dd_fi
     if qk is not None:
         given = q, k
         q, k = qk.apply(q, k, positions, stream)
+    elif positions is not None:
+        raise OsdnError(OSDN_ERR_INVALID_ARG, "positions need qk")
     B, T, H, dk = k.shape
     dv = v.shape[-1]
     p = make_params(B, T, H, dk, dv, k.dtype, eta, chunk, apf_anchor)
@@ -149,6 +153,8 @@ def step(q, k, v, beta, S, d, r=None, eta=1e-2, stream=None, d_anchor=None, apf_
     if qk is not None:
         q, k = (t.squeeze(1) for t in qk.apply(q.unsqueeze(1), k.unsqueeze(1),
                                                None if positions is None else positions.unsqueeze(1), stream))
+    elif positions is not None:
+        raise OsdnError(OSDN_ERR_INVALID_ARG, "positions need qk")
     B, H, dk = k.shape
     dv = v.shape[-1]
     p = make_params(B, 1, H, dk, dv, k.dtype, eta, apf_anchor=apf_anchor or d_anchor is not None)

@@ -194,8 +194,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
                  : "memory");
 }
 
-// The stages' barriers: one phase a use, waited for by every thread. A wait that passes the limit
-// sets the library's status word; later waits of that thread are then skipped, so the kernel still ends.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool read) {   // 4 zero bytes if not read
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(read ? 4 : 0)
                  : "memory");
@@ -206,13 +204,13 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
 }
 
 // One thread's pair of kRun tokens into its place in the tile (rows W apart), the first `live` of them and n
-// channels; the rest are zeros and not read.
+// channels; the rest are zeros and not read (their copies of no bytes name `any`, the tensor's start).
 template <int kMode, int kRun, int kStep, typename T>
-__device__ __forceinline__ void fetch_own(T* own, const T* row, int64_t stride, int live, int n) {
+__device__ __forceinline__ void fetch_own(T* own, const T* row, int64_t stride, int live, int n, const T* any) {
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
         const int m = j < live ? n : 0;
-        const T* src = m ? row + j * stride : row;
+        const T* src = m ? row + j * stride : any;
         if constexpr (kMode == kLoads) {
             own[j * W] = m > 0 ? src[0] : from_f32<T>(0.f);
             own[j * W + 1] = m > 1 ? src[kStep] : from_f32<T>(0.f);
@@ -220,26 +218,40 @@ __device__ __forceinline__ void fetch_own(T* own, const T* row, int64_t stride, 
             cp_async4(own + j * W, src, m > 0);
         } else {
             cp_async4(own + j * W, src, m > 0);
-            cp_async4(own + j * W + 1, m > 1 ? src + kStep : row, m > 1);
+            cp_async4(own + j * W + 1, m > 1 ? src + kStep : any, m > 1);
         }
     }
 }
 
+// The stages' barriers: one phase a use, waited for by every thread. A wait that passes the limit sets the
+// library's status word; that thread then waits and sends no more, so that the kernel still ends (its
+// results are undefined), and the thread that starts the copies lets those in flight land first.
 template <int kStages> struct Pipe {
     uint64_t* full;                     // [kStages]
     unsigned long long limit_ns;
     bool failed;
+    int started;                        // tiles whose copies this thread has started
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
-        if (!failed && !tc::mbar_wait(bar, parity, limit_ns)) {
-            failed = true;
-            atomicOr(&g_osdn_status, kStatusTimeout);
-        }
+        if (failed) return;
+        // a try suspends the thread for some microseconds; under a shorter limit the phase is only looked at
+        auto ready = [&] { return limit_ns < 20000ull ? tc::mbar_test(bar, parity) : tc::mbar_try_wait(bar, parity); };
+        if (ready()) return;
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (!ready())
+            if (tc::globaltimer_ns() - t0 > limit_ns) {
+                failed = true;
+                atomicOr(&g_osdn_status, kStatusTimeout);
+                return;
+            }
     }
     __device__ __forceinline__ void wait(int i) { wait(full + i % kStages, (i / kStages) & 1); }
-    // Copies that were started and not waited for, before the block leaves (only after a failed wait).
-    __device__ __forceinline__ void drain(int from, int to) {
+    // Before the block leaves, only after a failed wait: copies into its tiles, and a cluster's stores (100 us).
+    __device__ __forceinline__ void drain(int R) {
         if (!failed) return;
-        for (int i = from; i < to; ++i) tc::mbar_wait(full + i % kStages, (i / kStages) & 1, 1000000000ull);
+        for (int i = max(0, started - kStages); i < started; ++i)
+            tc::mbar_wait(full + i % kStages, (i / kStages) & 1, 1000000000ull);
+        if (R > 1)
+            for (const uint64_t t0 = tc::globaltimer_ns(); tc::globaltimer_ns() - t0 < 100000;) {}
     }
 };
 
@@ -316,7 +328,7 @@ __device__ __forceinline__ float2 join_runs(const float (*A)[W], const float (*E
         e = fma2(aw, e, load_pair(&E[w][lane * 2]));
         a = mul2(a, aw);
     }
-    if (sends) ex.send(i, lane, a, e);
+    if (sends && !pipe.failed) ex.send(i, lane, a, e);
     pipe.wait(ex.bar + (i & 1), (i >> 1) & 1);
     for (int k = 0; k < ex.R; ++k) {
         const int r = kUp ? k : ex.R - 1 - k;
@@ -365,14 +377,15 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const Args p, const __
     if (p.h0) carry = get_pair<kStep>(p.h0 + (int64_t)b * p.D + c, n);
 
     __shared__ uint64_t full[kStages];
-    Pipe<kStages> pipe{full, p.wait_limit_ns, false};
+    Pipe<kStages> pipe{full, p.wait_limit_ns, false, 0};
     __shared__ uint64_t joined[2];
     Exchange ex{slots, joined, R, rank};
     ex.init();
     auto fetch = [&](int i) {                       // starts the copies of this CTA's i-th tile
         const int t0 = (i * R + rank) * kTile, s = i % kStages;
         if constexpr (kMode == kTma) {
-            if (threadIdx.x == 0 && i < steps) {
+            if (threadIdx.x == 0 && i < steps && !pipe.failed) {
+                pipe.started = i + 1;
                 tc::mbar_arrive_expect_tx(full + s, kTileBytes<Tx>(kRun) + kTileBytes<Tg>(kRun));
                 tma_load_3d(bx + s * kTile * W, &maps.x, c0, t0, b, full + s);
                 tma_load_3d(bg + s * kTile * W, &maps.gate, c0, t0, b, full + s);
@@ -380,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const Args p, const __
         } else {
             if (i < steps) {
                 const int t = t0 + warp * kRun, at = (s * kTile + warp * kRun) * W + lane * 2;
-                fetch_own<kMode, kRun, kStep>(bx + at, x + t * p.xt, p.xt, len - t, n);
-                fetch_own<kMode, kRun, kStep>(bg + at, gate + t * p.gt, p.gt, len - t, n);
+                fetch_own<kMode, kRun, kStep>(bx + at, x + t * p.xt, p.xt, len - t, n, static_cast<const Tx*>(p.x));
+                fetch_own<kMode, kRun, kStep>(bg + at, gate + t * p.gt, p.gt, len - t, n, static_cast<const Tg*>(p.gate));
             }
             cp_async_commit();
         }
@@ -451,10 +464,9 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const Args p, const __
     if (h && p.zero_rest)
         for (int t = len + rank * kWarps + warp; t < p.T; t += R * kWarps) put_pair<kStep>(h + t * p.ht, all2(0.f), n);
     if (warp == 0 && rank == 0 && p.final_h) put_pair<kStep>(p.final_h + (int64_t)b * p.D + c, carry, n);
-    if constexpr (kMode == kTma) {
-        pipe.drain(0, steps);
-        if (lane == 0) tc::bulk_wait_read<0>();
-    }
+    if (kMode == kTma && lane == 0) tc::bulk_wait_read<0>();
+    pipe.drain(R);
+    __syncwarp();
     if (R > 1) cluster_sync();   // no CTA leaves while another may still store to it
 }
 
@@ -490,14 +502,15 @@ __global__ void __launch_bounds__(kThreads, kMode == kTma && sizeof(Tg) > sizeof
     auto tile_of = [&](int i) { return (steps - 1 - i) * R + rank; };
 
     __shared__ uint64_t full[kStages];
-    Pipe<kStages> pipe{full, p.wait_limit_ns, false};
+    Pipe<kStages> pipe{full, p.wait_limit_ns, false, 0};
     __shared__ uint64_t joined[2];
     Exchange ex{slots, joined, R, rank};
     ex.init();
     auto fetch = [&](int i) {
         const int t0 = tile_of(i) * kTile, s = i % kStages;
         if constexpr (kMode == kTma) {
-            if (threadIdx.x == 0 && i < steps) {
+            if (threadIdx.x == 0 && i < steps && !pipe.failed) {
+                pipe.started = i + 1;
                 tc::mbar_arrive_expect_tx(full + s, 2 * kTileBytes<Tx>(kRun) + kTileBytes<Tg>(kRun));
                 tma_load_3d(bx + s * kTile * W, &maps.x, c0, t0, b, full + s);
                 tma_load_3d(bg + s * kTile * W, &maps.gate, c0, t0, b, full + s);
@@ -506,9 +519,9 @@ __global__ void __launch_bounds__(kThreads, kMode == kTma && sizeof(Tg) > sizeof
         } else {
             if (i < steps) {
                 const int t = t0 + warp * kRun, at = (s * kTile + warp * kRun) * W + lane * 2;
-                fetch_own<kMode, kRun, kStep>(bx + at, x + t * p.xt, p.xt, len - t, n);
-                fetch_own<kMode, kRun, kStep>(bg + at, gate + t * p.gt, p.gt, len - t, n);
-                fetch_own<kMode, kRun, kStep>(bd + at, dh + t * p.ht, p.ht, len - t, n);
+                fetch_own<kMode, kRun, kStep>(bx + at, x + t * p.xt, p.xt, len - t, n, static_cast<const Tx*>(p.x));
+                fetch_own<kMode, kRun, kStep>(bg + at, gate + t * p.gt, p.gt, len - t, n, static_cast<const Tg*>(p.gate));
+                fetch_own<kMode, kRun, kStep>(bd + at, dh + t * p.ht, p.ht, len - t, n, static_cast<const Tx*>(p.dh));
             }
             cp_async_commit();
         }
@@ -544,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, kMode == kTma && sizeof(Tg) > sizeof
                         store_pair(bd + at0 + j * W, all2(0.f));
                         store_pair(bg + at0 + j * W, all2(0.f));
                     }
+                tc::fence_proxy_async_smem();
             }
         } else {
             cp_async_wait<kStages - 2>();
@@ -603,8 +617,8 @@ __global__ void __launch_bounds__(kThreads, kMode == kTma && sizeof(Tg) > sizeof
                     }
                 }
             });
+            if (kMode == kTma) tc::fence_proxy_async_smem();   // before the stores out, or the stage's next copies in
             if (kMode == kTma && live >= kRun) {
-                tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     tma_store_3d(&maps.o0, bx + at0, c0, t0, b);
@@ -627,10 +641,9 @@ __global__ void __launch_bounds__(kThreads, kMode == kTma && sizeof(Tg) > sizeof
             put_pair<kStep>(dgate + (int64_t)t * p.D, all2(0.f), n);
         }
     if (warp == 0 && rank == 0 && p.dh0) put_pair<kStep>(p.dh0 + (int64_t)b * p.D + c, carry, n);
-    if constexpr (kMode == kTma) {
-        pipe.drain(0, steps);
-        if (lane == 0) tc::bulk_wait_read<0>();
-    }
+    if (kMode == kTma && lane == 0) tc::bulk_wait_read<0>();
+    pipe.drain(R);
+    __syncwarp();
     if (R > 1) cluster_sync();
 }
 

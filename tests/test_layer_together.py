@@ -7,6 +7,10 @@ fp32) holds for the chain too: the norms' outputs enter the oracle as the kernel
 adds no error of its own before the delta rule; the norms' backward multiplies the delta rule's
 gradients by a map of norm at most 2 / |x|, and is compared on the same scale.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -14,6 +18,8 @@ import torch
 import oracle
 from tests import _layer_ref as ref
 from tests._util import BF16_TOL, FP32_TOL, slice_rel_err
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _inputs(seed, B, T, H, dk, dv, dt, gated):
@@ -129,3 +135,43 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_positions_need_the_norm():
+    import preconditioned_delta_rule_token_b200 as pk
+    x, b = torch.zeros(1, 4, 1, 64), torch.zeros(1, 4, 1)
+    for call in (lambda: pk.forward(x, x, x, b, positions=b), lambda: pk.backward(x, x, x, b, x, positions=b),
+                 lambda: pk.step(x[:, 0], x[:, 0], x[:, 0], b[:, 0], x, x, positions=b)):
+        with pytest.raises(pk.OsdnError, match="positions"):
+            call()
+
+
+_FIRST_IN_A_CAPTURE = """
+import torch
+import preconditioned_delta_rule_token_b200 as pk
+x = torch.randn(2, 300, 64, device="cuda").bfloat16()
+q = torch.randn(2, 300, 2, 64, device="cuda").bfloat16()
+w, f = torch.ones(64, device="cuda"), torch.ones(32, dtype=torch.float64, device="cuda")
+def run():
+    h, s, m = pk.recurrence(x, x, gate_form="logit", checkpoints=True)
+    g = pk.recurrence_backward(x, x, x, checkpoints=m, gate_form="logit")
+    o = pk.recurrence_step(x[:, 0], x[:, 0], s.clone(), gate_form="logit")
+    n = pk.qk_norm(q, q, freqs=f, wq=w)
+    d = pk.qk_norm_backward(q, q, q, q, freqs=f, wq=w)
+    return [h, s, g["dx"], g["dgate"], o, *n, d["dq"], d["dwq"], pk.rope(q, f)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+print("same")
+"""
+
+
+@pytest.mark.gpu
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing has to run before a capture: the kernels' limits and the room on the device are asked for on the host."""
+    r = subprocess.run([sys.executable, "-c", _FIRST_IN_A_CAPTURE], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

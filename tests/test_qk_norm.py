@@ -316,6 +316,8 @@ def test_lengths_and_rows_of_zeros():
         for norm in ("l2", "rms"):
             assert bool((pk.qk_norm(z, None, norm=norm, eps=eps)[0] == 0).all())
             assert bool(torch.isfinite(pk.qk_norm_backward(z, None, z + 1, None, norm=norm, eps=eps)["dq"]).all())
+    tiny = torch.full((1, 1, 1, 64), 1e-21, device="cuda")   # squares below fp32's range: as zeros
+    assert bool((pk.qk_norm(tiny, None, eps=0.0)[0] == 0).all())
     e = torch.zeros(2, 0, 3, 64, device="cuda")
     assert pk.qk_norm(e, None)[0].shape == e.shape
     assert bool((pk.qk_norm_backward(e, None, e, None, wq=w.cuda())["dwq"] == 0).all())

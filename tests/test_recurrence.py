@@ -359,3 +359,29 @@ def test_offsets_past_32_bits():
     a = pk.recurrence_backward(xs, gs, ds, h0=h0.cuda())
     b = pk.recurrence_backward(x.cuda(), gate.cuda(), dh.cuda(), h0=h0.cuda())
     assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,T,D", ((1, 32768, 1024), (32, 512, 2048)))
+def test_a_wait_that_gives_up_is_reported(B, T, D):
+    """With waits bounded to 1 ns some of thousands of waits for memory give up (alone and in a cluster; the
+    timer that bounds them ticks every microsecond or less): the call ends, the status says so, and the
+    next call is right again."""
+    import preconditioned_delta_rule_token_b200 as pk
+    x, gate, dh = (torch.randn(B, T, D, device="cuda").bfloat16() for _ in range(3))
+    want = pk.recurrence(x, gate, gate_form="logit", checkpoints=True)
+    grads = pk.recurrence_backward(x, gate, dh, checkpoints=want[2], gate_form="logit")
+    assert pk.osdn_sync_status() == pk.OSDN_OK
+    for call in (lambda: pk.recurrence(x, gate, gate_form="logit"),
+                 lambda: pk.recurrence_backward(x, gate, dh, checkpoints=want[2], gate_form="logit")):
+        pk.osdn_set_wait_limit_ns(1)
+        try:
+            call()
+            status = pk.osdn_sync_status()
+        finally:
+            pk.osdn_set_wait_limit_ns(0)
+        assert status == pk.OSDN_ERR_TIMEOUT and pk.osdn_sync_status() == pk.OSDN_OK
+    got = pk.recurrence(x, gate, gate_form="logit", checkpoints=True)
+    again = pk.recurrence_backward(x, gate, dh, checkpoints=got[2], gate_form="logit")
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and all(torch.equal(grads[k], again[k]) for k in grads)
+    assert pk.osdn_sync_status() == pk.OSDN_OK
