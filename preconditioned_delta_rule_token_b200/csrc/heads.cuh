@@ -8,6 +8,14 @@
 //   dw = sum over rows of g inv x,   dx = inv (g w - x inv^2 / n <g w, x>).
 // A row lies in a group of lanes, 8 features a lane, chosen so that both features of a pair are in one lane;
 // only a row's sums go between the lanes.
+//
+// Memory bounds it: 4 bytes an element (bf16) forward for 7 operations. What it takes to get there is few
+// instructions a row, 4 rows in flight a lane, and the angles made once a token and shared by its heads.
+// Measured, bf16, forward B8 T4096 16 + 16 heads of 128 (L2, rotation) / rotation alone B1 T32768 16 heads:
+// a table a CTA and partners by shuffles 188 / 98 us; a warp a token, pairs in one lane 148 / 69; rows by
+// stepped pointers and an approximate root 104 / 54; rows loaded ahead of the angles, CTAs that stay
+// 100 / 47; a group of lanes a token 95 / 46 us, 88% and 90% of the measured copy rate, bound by
+// instruction issue (2.6 of 4 a cycle) before memory. Backward at the first size 151 us (82%).
 #pragma once
 #include <type_traits>
 

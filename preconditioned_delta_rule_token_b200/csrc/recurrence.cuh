@@ -5,9 +5,24 @@
 //   lam_t = dh_t + mu_{t+1},  mu_t = a_t lam_t,  mu_{N+1} = dh_N (backward; dh_0 = mu_1)
 //   dx_t = s_t lam_t,  dgate_t = lam_t a'_t (h_{t-1} + x_t ds/da)
 // A run of tokens maps its incoming state affinely, h_out = A h_in + H with A the product of its
-// a_t and H its end state from 0, and mu_out = A mu_in + M the other way. So a CTA takes a tile of
-// kTile tokens x 32 V channels, each warp runs its kRun tokens from 0, and the runs are joined
-// through shared memory in the order of the tokens.
+// a_t and H its end state from 0, and mu_out = A mu_in + M the other way. So a CTA takes a tile of 8
+// runs x 64 channels, each warp goes through its run from 0 with two channels a lane, the runs are joined
+// through shared memory in the order of the tokens, and the run's results follow from what comes in.
+//
+// Why so. The operator reads and writes 6 bytes an element forward and 10 backward (bf16) for 10 to 40
+// operations, so memory bounds it; but a walk over the tokens is serial, and 148 SMs need more of them at a
+// time than there are channels / 64. A cluster of R CTAs therefore takes R tiles at a time and exchanges one
+// pair a channel through distributed shared memory: no second pass over the data, no flag in device
+// memory, and the same result on every run. R is the most (up to 16) at which all clusters are resident.
+// Measured on the way (bf16 forward, B8 T4096 D2048, log gate, norm scale / B1 T32768, fp32 log gate):
+// one CTA a walk with plain loads 648 / 3720 us; clusters with a hardware barrier each step 255 / 242;
+// packed arithmetic 114 / 165; tensor-map tiles and counted remote stores 107 / 108; 16 tokens a run instead
+// of 8 in the forward (half the joins) 83 / 95; unpacking bf16 by shifts 80 / 92 us, 78% and 90% of
+// the measured copy rate. The first is then bound by instruction issue (21 an element; 2.2 of 4 a
+// cycle with two CTAs on most SMs and one on the rest), the second by memory. The backward, B8 T4096 D2048:
+// 141 us (logit, complement), 156 us (log, norm), 74% and 67%: 43 instructions an element in two walks over a
+// run, and two CTAs an SM by registers. What did not pay in the forward: 16 warps a CTA (111 us where 8 took
+// 102), two warps that join for all behind a second barrier (107), scalar arithmetic (34 instructions, 105).
 #pragma once
 #include <type_traits>
 
@@ -24,7 +39,8 @@ constexpr int kSaved = 64;              // tokens between the saved states
 constexpr int kWarps = 8;               // runs of one tile, a warp each
 constexpr int kThreads = 32 * kWarps;
 constexpr int W = 64;                   // channels of one tile, two a lane
-// Tokens of one run, held in registers (forward, backward). More of them join fewer runs.
+// Tokens of one run, held in registers (forward, backward): 16 halve the joins against 8 (107 -> 83 us at B8
+// T4096 D2048 bf16); fp32 tiles of 16 would leave one CTA to an SM, and the backward's arrays do not fit.
 template <typename Tx, typename Tg> constexpr int fwd_run() { return sizeof(Tx) + sizeof(Tg) > 6 ? 8 : 16; }
 constexpr int kBwdRun = 8;
 
@@ -340,8 +356,11 @@ __device__ __forceinline__ float2 join_runs(const float (*A)[W], const float (*E
 }
 
 // Dynamic shared memory: the stages (128-byte aligned), then the cluster's slots [2][R][32] (none for one CTA).
-// Three tiles in flight or in use; two where three would leave one CTA to an SM.
+// Three tiles in flight or in use (two: 97 us instead of 83 at B8 T4096 D2048 bf16); two where three would leave
+// one CTA to an SM (fp32 gates at B1 T32768: three 120 us, two 95 us).
 template <typename Tx, typename Tg> constexpr int fwd_stages() { return sizeof(Tx) + sizeof(Tg) == 6 ? 2 : 3; }
+// Backward: three, two with fp32 gates, where three CTAs to an SM then pay for the registers that they spill
+// (B1 T16384 D2048: 98 us against 128; with bf16 gates they cost, B8 T4096 D2048 156 us against 141).
 template <typename Tx, typename Tg> constexpr int bwd_stages() { return sizeof(Tg) == 4 ? 2 : 3; }
 template <typename Tx, typename Tg> constexpr int fwd_slots() {
     constexpr int run = fwd_run<Tx, Tg>();
