@@ -8,8 +8,11 @@ are not on a CUDA device: there is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import subprocess
+import sysconfig
 
 import torch
 
@@ -86,6 +89,51 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def build_if_missing() -> str:
     return build(force=False)
+
+
+CALL_PATH = os.path.join(_PKG, "_call" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def build_call(force: bool = False) -> str:
+    """Compile the extension module that the layer's wrappers call through (csrc/call.cpp), in-tree with g++."""
+    src = os.path.join(_CSRC, "call.cpp")
+    if not force and os.path.exists(CALL_PATH) and os.path.getmtime(CALL_PATH) >= os.path.getmtime(src):
+        return CALL_PATH
+    home = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_path("include"), os.path.join(cuda, "include")]
+    libs, tmp = os.path.join(home, "lib"), CALL_PATH + ".tmp%d" % os.getpid()
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+                           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] +
+                          ["-I" + d for d in include] + ["-o", tmp, src, "-L" + libs, "-ltorch_python", "-ltorch",
+                                                         "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + libs])
+    os.replace(tmp, CALL_PATH)
+    return CALL_PATH
+
+
+_call = None
+
+
+def call():
+    """The extension module, and in it the addresses of the library's functions as `fn` (built if missing)."""
+    global _call
+    if _call is None:
+        L = lib()
+        try:
+            build_call(force=False)
+        except (OSError, subprocess.CalledProcessError) as exc:
+            if not os.path.exists(CALL_PATH):
+                raise OsdnError(OSDN_ERR_UNSUPPORTED, "_call is not built and g++ failed: %s" % exc)
+        name = __package__ + "._call"
+        spec = importlib.util.spec_from_file_location(
+            name, CALL_PATH, loader=importlib.machinery.ExtensionFileLoader(name, CALL_PATH))
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.fn = {n: ctypes.cast(getattr(L, "osdn_" + n), ctypes.c_void_p).value
+                for n in ("recur_fwd", "recur_bwd", "recur_step", "qk_fwd", "qk_bwd", "rope")}
+        _call = m
+    return _call
 
 
 _lib = None

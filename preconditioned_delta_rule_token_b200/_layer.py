@@ -8,11 +8,13 @@ device; there is no CPU path.
 
 A decode token's kernels take a few microseconds, so a call does little in Python: the
 checks and the parameter block depend on the tensors' layouts alone (shape, strides,
-type, device) and are kept by them.
+type, device) and are kept by them, and addresses and stream go through an extension
+module (csrc/call.cpp).
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass, fields
 
 import torch
@@ -28,28 +30,43 @@ def _bad(msg, code=OSDN_ERR_INVALID_ARG):
 
 
 def _scope(dev, stream):
-    """What makes `stream` (None: the current one) of device `dev` current for allocations and the launch; None
-    where that is so already."""
-    if stream is not None:
-        if stream.device != dev:
-            _bad("the stream is of %s, the tensors are on %s" % (stream.device, dev))
-        return torch.cuda.stream(stream)
-    return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    """Makes `stream` (None: the current one) of device `dev` current for allocations and the launch."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        _bad("the stream is of %s, the tensors are on %s" % (stream.device, dev))
+    return torch.cuda.stream(stream)
 
 
 class _Kept(dict):
-    """Parameter blocks by the layouts they were checked for; emptied when it grows past 1024."""
+    """Parameter blocks (and their addresses) by the layouts they were checked for; emptied when it grows past
+    1024."""
 
-    def keep(self, key, value):
+    def keep(self, key, params):
         if len(self) >= 1024:
             self.clear()
-        self[key] = value
-        return value
+        self[key] = kept = (params, ctypes.addressof(params))
+        return kept
 
 
-def _lay(t):
-    """Everything about a tensor that the checks and the parameter block depend on."""
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+class _Calls:
+    """The extension module's functions, loaded with the library at the first use."""
+
+    def __getattr__(self, name):
+        m = B.call()
+        for n in ("layouts", "here", "like", "floats"):
+            setattr(self, n, getattr(m, n))
+        for n, address in m.fn.items():
+            setattr(self, n, functools.partial(getattr(m, n), address))
+        return self.__dict__[name]
+
+
+_C = _Calls()
+
+
+def _done(rc):
+    if rc:
+        B._check(rc)
 
 
 def _choice(name, value, table):
@@ -90,11 +107,6 @@ def _strides(name, t, n):
     if not any(st[:n]):
         _bad("%s has strides of 0 in every dimension: expand it into memory" % name)
     return st[:n]
-
-
-def _new(t):
-    """An uninitialised dense tensor like t."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _saved(nB, T, D):
@@ -144,19 +156,18 @@ def recurrence(x, gate, h0=None, lengths=None, gate_form="decay", input_scale="n
     on do not count; their rows of h are zeros (left as they were when `h` is given).
     Returns (h [B,T,D] in x's type, final_h [B,D] fp32), and with checkpoints=True the states
     [B,ceil(T/64),D] fp32 that recurrence_backward takes."""
-    key = ("fwd", gate_form, input_scale, _lay(x), _lay(gate), _lay(h0), _lay(lengths), _lay(h))
-    p = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
+    key = ("fwd", gate_form, input_scale, _C.layouts(x, gate, h0, lengths, h))
+    kept = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
         x, gate, gate_form, input_scale, (("h0", h0, "state"), ("lengths", lengths, "lengths"), ("h", h, "token"))))
     nB, T, D = x.shape
-    scope = _scope(x.device, stream)
-    if scope is not None:
-        with scope:
+    if stream is not None or not _C.here(x):
+        with _scope(x.device, stream):
             return recurrence(x, gate, h0, lengths, gate_form, input_scale, checkpoints, h)
     if h is None:
-        h = _new(x)
-    final_h = torch.empty((nB, D), dtype=torch.float32, device=x.device)
-    marks = torch.empty(_saved(nB, T, D), dtype=torch.float32, device=x.device) if checkpoints else None
-    B.osdn_recur_fwd(p, x, gate, h0, lengths, h, final_h, marks)
+        h = _C.like(x)
+    final_h = _C.floats(x, nB, D)
+    marks = _C.floats(x, *_saved(nB, T, D)) if checkpoints else None
+    _done(_C.recur_fwd(kept[1], x, gate, h0, lengths, h, final_h, marks))
     return (h, final_h, marks) if checkpoints else (h, final_h)
 
 
@@ -168,38 +179,36 @@ def recurrence_backward(x, gate, dh, h0=None, dfinal_h=None, lengths=None, check
     recurrence(..., checkpoints=True) returned for the same inputs; None runs the forward again for them.
     Returns a dict with dx (x's type), dgate (the gate's type; with respect to the gate as given) and
     dh0 [B,D] fp32. Rows from a sequence's length on are zeros."""
-    key = ("bwd", gate_form, input_scale, _lay(x), _lay(gate), _lay(dh), _lay(h0), _lay(dfinal_h), _lay(lengths),
-           _lay(checkpoints))
-    p = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
+    key = ("bwd", gate_form, input_scale, _C.layouts(x, gate, dh, h0, dfinal_h, lengths, checkpoints))
+    kept = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
         x, gate, gate_form, input_scale,
         (("h0", h0, "state"), ("lengths", lengths, "lengths"), ("dh", dh, "token"), ("dfinal_h", dfinal_h, "state"),
          ("checkpoints", checkpoints, "saved"))))
-    scope = _scope(x.device, stream)
-    if scope is not None:
-        with scope:
+    if stream is not None or not _C.here(x):
+        with _scope(x.device, stream):
             return recurrence_backward(x, gate, dh, h0, dfinal_h, lengths, checkpoints, gate_form, input_scale,
                                        workspace)
-    g = {"dx": _new(x), "dgate": _new(gate),
-         "dh0": torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device)}
+    g = {"dx": _C.like(x), "dgate": _C.like(gate),
+         "dh0": _C.floats(x, x.shape[0], x.shape[2])}
     if checkpoints is None and workspace is None:
-        workspace = torch.empty(B.osdn_recur_bwd_workspace_size(p), dtype=torch.uint8, device=x.device)
-    B.osdn_recur_bwd(p, x, gate, h0, lengths, dh, dfinal_h, checkpoints, g["dx"], g["dgate"], g["dh0"], workspace)
+        workspace = torch.empty(B.osdn_recur_bwd_workspace_size(kept[0]), dtype=torch.uint8, device=x.device)
+    _done(_C.recur_bwd(kept[1], x, gate, h0, lengths, dh, dfinal_h, checkpoints, g["dx"], g["dgate"], g["dh0"],
+                       workspace))
     return g
 
 
 def recurrence_step(x, gate, state, gate_form="decay", input_scale="none", out=None, stream=None):
     """One decode token of the recurrence: x, gate [B,D]; state [B,D] fp32, updated in place.
     Returns the new state in x's type [B,D] (`out` if given)."""
-    key = ("step", gate_form, input_scale, _lay(x), _lay(gate), _lay(state), _lay(out))
-    p = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
+    key = ("step", gate_form, input_scale, _C.layouts(x, gate, state, out))
+    kept = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
         x, gate, gate_form, input_scale, (("state", state, "state"), ("out", out, "token")), token=False))
-    scope = _scope(x.device, stream)
-    if scope is not None:
-        with scope:
+    if stream is not None or not _C.here(x):
+        with _scope(x.device, stream):
             return recurrence_step(x, gate, state, gate_form, input_scale, out)
     if out is None:
-        out = _new(x)
-    B.osdn_recur_step(p, x, gate, state, out)
+        out = _C.like(x)
+    _done(_C.recur_step(kept[1], x, gate, state, out))
     return out
 
 
@@ -248,21 +257,19 @@ def qk_norm(q, k, freqs=None, positions=None, norm="l2", eps=1e-6, wq=None, wk=N
     (rows of a given q_out, k_out stay as they were). q_out may be q, k_out may be k.
     Returns (q_out, k_out)."""
     numbers = (eps, amplitude, scale_q, scale_k, pos0)
-    key = (norm, layout, numbers, _lay(q), _lay(k), _lay(freqs), _lay(positions), _lay(lengths), _lay(wq), _lay(wk),
-           _lay(q_out), _lay(k_out))
-    p = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
+    key = (norm, layout, numbers, _C.layouts(q, k, freqs, positions, lengths, wq, wk, q_out, k_out))
+    kept = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
         q, k, freqs, positions, lengths, norm, layout, wq, wk, q_out, k_out, numbers, ("q", "k", "q_out", "k_out")))
-    scope = _scope(q.device, stream)
-    if scope is not None:
-        with scope:
+    if stream is not None or not _C.here(q):
+        with _scope(q.device, stream):
             return qk_norm(q, k, freqs, positions, norm, eps, wq, wk, layout, amplitude, scale_q, scale_k, pos0, lengths,
                            q_out, k_out)
     both = lengths is None or (q_out is None and k_out is None)
     if q_out is None:
-        q_out = _new(q) if both else torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _C.like(q) if both else torch.zeros(q.shape, dtype=q.dtype, device=q.device)
     if k is not None and k_out is None:
-        k_out = _new(k) if both else torch.zeros(k.shape, dtype=k.dtype, device=k.device)
-    B.osdn_qk_fwd(p, q, k, wq, wk, positions, freqs, lengths, q_out, k_out)
+        k_out = _C.like(k) if both else torch.zeros(k.shape, dtype=k.dtype, device=k.device)
+    _done(_C.qk_fwd(kept[1], q, k, wq, wk, positions, freqs, lengths, q_out, k_out))
     return q_out, k_out
 
 
@@ -275,22 +282,20 @@ def qk_norm_backward(q, k, dq_out, dk_out, freqs=None, positions=None, norm="l2"
     if (k is None) != (dk_out is None):
         _bad("k and dk_out go together")
     numbers = (eps, amplitude, scale_q, scale_k, pos0)
-    key = ("bwd", norm, layout, numbers, _lay(q), _lay(k), _lay(freqs), _lay(positions), _lay(lengths), _lay(wq), _lay(wk),
-           _lay(dq_out), _lay(dk_out))
-    p = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
+    key = ("bwd", norm, layout, numbers, _C.layouts(q, k, freqs, positions, lengths, wq, wk, dq_out, dk_out))
+    kept = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
         q, k, freqs, positions, lengths, norm, layout, wq, wk, dq_out, dk_out, numbers, ("q", "k", "dq_out", "dk_out")))
-    scope = _scope(q.device, stream)
-    if scope is not None:
-        with scope:
+    if stream is not None or not _C.here(q):
+        with _scope(q.device, stream):
             return qk_norm_backward(q, k, dq_out, dk_out, freqs, positions, norm, eps, wq, wk, layout, amplitude, scale_q,
                                     scale_k, pos0, lengths, workspace)
-    g = {"dq": _new(q), "dk": None if k is None else _new(k),
-         "dwq": None if wq is None else torch.empty_like(wq),
-         "dwk": None if wk is None or k is None else torch.empty_like(wk)}
+    g = {"dq": _C.like(q), "dk": None if k is None else _C.like(k),
+         "dwq": None if wq is None else _C.like(wq),
+         "dwk": None if wk is None or k is None else _C.like(wk)}
     if workspace is None and (g["dwq"] is not None or g["dwk"] is not None):
-        workspace = torch.empty(B.osdn_qk_bwd_workspace_size(p), dtype=torch.uint8, device=q.device)
-    B.osdn_qk_bwd(p, q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, g["dq"], g["dk"], g["dwq"],
-                  g["dwk"], workspace)
+        workspace = torch.empty(B.osdn_qk_bwd_workspace_size(kept[0]), dtype=torch.uint8, device=q.device)
+    _done(_C.qk_bwd(kept[1], q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, g["dq"], g["dk"], g["dwq"],
+                    g["dwk"], workspace))
     return g
 
 
@@ -324,20 +329,19 @@ def rope(x, freqs, positions=None, layout="half", amplitude=1.0, scale=1.0, pos0
     inverse=True turns back with the same amplitude: it takes the gradient of the result to that of x.
     `out` may be x. Returns the rotated tensor."""
     numbers = (0.0, amplitude, scale, 1.0, pos0)
-    key = ("rope", layout, numbers, _lay(x), _lay(freqs), _lay(positions), _lay(lengths), _lay(out))
-    p = _HEADS.get(key)
-    if p is None:
+    key = ("rope", layout, numbers, _C.layouts(x, freqs, positions, lengths, out))
+    kept = _HEADS.get(key)
+    if kept is None:
         if freqs is None:
             _bad("freqs is needed")
-        p = _HEADS.keep(key, _heads_params(x, None, freqs, positions, lengths, "none", layout, None, None, out, None,
-                                           numbers, ("x", None, "out", None)))
-    scope = _scope(x.device, stream)
-    if scope is not None:
-        with scope:
+        kept = _HEADS.keep(key, _heads_params(x, None, freqs, positions, lengths, "none", layout, None, None, out, None,
+                                              numbers, ("x", None, "out", None)))
+    if stream is not None or not _C.here(x):
+        with _scope(x.device, stream):
             return rope(x, freqs, positions, layout, amplitude, scale, pos0, inverse, lengths, out)
     if out is None:
-        out = _new(x)
-    B.osdn_rope(p, x, positions, freqs, lengths, out, inverse)
+        out = _C.like(x)
+    _done(_C.rope(kept[1], x, positions, freqs, lengths, out, 1 if inverse else 0))
     return out
 
 
