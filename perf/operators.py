@@ -294,7 +294,12 @@ def _own_recurrence(s):
     if c["mode"] == "forward":
         return list(pk.recurrence(s["x"], s["gate"], h0=s["h0"], lengths=s["lengths"], **how))
     h, final, marks = pk.recurrence(s["x"], s["gate"], h0=s["h0"], lengths=s["lengths"], checkpoints=True, **how)
-    g = pk.recurrence_backward(s["x"], s["gate"], s["dh"], h0=s["h0"], dfinal_h=s["dfinal"], lengths=s["lengths"],
+    dfinal = s["dfinal"]
+    if s["lengths"] is None and s["dh"].dtype == torch.float32:
+        # the plain form adds the final state's gradient into dh in place there: the state goes the same way here
+        s["dh"][:, -1] += dfinal
+        dfinal = None
+    g = pk.recurrence_backward(s["x"], s["gate"], s["dh"], h0=s["h0"], dfinal_h=dfinal, lengths=s["lengths"],
                                checkpoints=marks, **how)
     return [h, final, g["dx"], g["dgate"], g["dh0"]]
 
