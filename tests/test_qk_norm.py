@@ -324,6 +324,29 @@ def test_lengths_and_rows_of_zeros():
 
 
 @pytest.mark.gpu
+def test_one_weight_and_given_positions():
+    """A weight on q alone, positions from a negative pos0, and the rotation alone with lengths."""
+    import preconditioned_delta_rule_token_b200 as pk
+    (q, dq), (k, dk) = rows(14, 2, 21, 2, 64, FP), rows(15, 2, 21, 3, 64, FP)
+    w = 1 + 0.1 * torch.randn(64, generator=torch.Generator().manual_seed(4))
+    fr, pos = ref.plain_freqs(64), ref.positions_of(2, 21, -7)
+    how = dict(freqs=fr.cuda(), wq=w.cuda(), pos0=-7, layout="interleaved")
+    qo, ko = pk.qk_norm(q.cuda(), k.cuda(), **how)
+    g = pk.qk_norm_backward(q.cuda(), k.cuda(), dq.cuda(), dk.cuda(), **how)
+    for x, wt, do, out, n in ((q, w, dq, qo, "q"), (k, None, dk, ko, "k")):
+        a = ("l2", 1e-6, 1.0, fr, pos, "interleaved", 1.0)
+        ref.close(out, *ref.head_norm(x, wt, *a), 32, n)
+        dx, dw = ref.head_norm_grads(x, wt, do, *a)
+        ref.close(g["d" + n], *dx, 96, "d" + n)
+        if wt is not None:
+            ref.close(g["dwq"], *dw, 2 * 21 * 2 + 96, "dwq")
+    assert g["dwk"] is None
+    n = torch.tensor([21, 5], dtype=torch.int32).cuda()
+    full, cut = pk.rope(q.cuda(), fr.cuda(), pos0=-7), pk.rope(q.cuda(), fr.cuda(), pos0=-7, lengths=n)
+    assert torch.equal(cut[0], full[0]) and torch.equal(cut[1, :5], full[1, :5]) and bool((cut[1, 5:] == 0).all())
+
+
+@pytest.mark.gpu
 def test_against_differences_on_the_device():
     """Directional derivatives of the fp32 forward: over 2 eps = 2^-5 the quotient is off by eps^2 of third
     derivatives and the rounding of the loss over 2 eps: within 1e-2 of the magnitude sum."""

@@ -237,6 +237,17 @@ def test_one_gate_for_the_batch():
                        pk.recurrence(x.cuda(), one.expand(4, -1, -1).contiguous())[0])
     with pytest.raises(pk.OsdnError):
         pk.recurrence(x.cuda(), one[:, :1].expand(4, 90, -1))
+    dh = torch.randn(4, 90, 64, generator=torch.Generator().manual_seed(1)).cuda()
+    a = pk.recurrence_backward(x.cuda(), one.expand(4, -1, -1), dh[:1].expand(4, -1, -1))
+    b = pk.recurrence_backward(x.cuda(), one.expand(4, -1, -1).contiguous(), dh[:1].expand(4, -1, -1).contiguous())
+    assert all(torch.equal(a[k], b[k]) for k in a) and a["dgate"].shape == (4, 90, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,T,D,dt", ((1, 1, 5000, torch.bfloat16), (300, 3, 8, torch.float32), (1, 2049, 72, torch.float32)))
+def test_corners_of_the_grid(B, T, D, dt):
+    """One token, more sequences than SMs with a handful of channels, one token past 16 tiles of 128."""
+    _check_all(B, T, D, dt, torch.float32, "decay", "complement", seed=21)
 
 
 @pytest.mark.gpu
