@@ -19,7 +19,7 @@
 #pragma once
 #include <type_traits>
 
-#include "common.cuh"
+#include "pairs.cuh"
 
 namespace osdn {
 namespace heads {

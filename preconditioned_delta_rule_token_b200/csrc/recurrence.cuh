@@ -26,7 +26,7 @@
 #pragma once
 #include <type_traits>
 
-#include "common.cuh"
+#include "pairs.cuh"
 #include "tc_ptx.cuh"
 
 namespace osdn {
