@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) heads_kernel(cons
     turn.turning = kLayout == kHalf ? (halves ? 4 : 0) : max(0, min(4, (p.rot - gl * kVec) / 2));
 #pragma unroll
     for (int i = 0; i < 2; ++i) turn.c[i] = turn.s[i] = turn.ns[i] = all2(0.f);
+    let_next_start();
+    wait_for_previous();
     Eight w, dw;
 #pragma unroll
     for (int i = 0; i < 2; ++i) w.p[i] = w.q[i] = all2(1.f), dw.p[i] = dw.q[i] = all2(0.f);
@@ -320,8 +322,10 @@ __global__ void __launch_bounds__(1024) dw_kernel(const float* part_q, const flo
     const int parts = blockIdx.y ? parts_k : parts_q;
     const float* part = blockIdx.y ? part_k : part_q;
     float* dw = blockIdx.y ? dwk : dwq;
-    if (!dw) return;
     __shared__ float s[32][33];
+    let_next_start();
+    wait_for_previous();
+    if (!dw) return;
     const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, w = threadIdx.x >> 5;
     float t = 0.f;
     if (c < width)

@@ -1536,6 +1536,22 @@ int make_rows_map(CUtensorMap* m, const void* base, const osdn_recur_params* p, 
     return OSDN_OK;
 }
 
+// Launch of a kernel that may start before the one ahead of it in the stream ends (pairs.cuh: it waits itself).
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kern)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // What a recurrence kernel needs to know of a device: clusters of R CTAs that run at a time, 0 until asked.
 struct RecurRoom {
     std::atomic<int> clusters[osdn::recur::kMaxCluster + 1];
@@ -1553,16 +1569,18 @@ int launch_recur(void (*kern)(osdn::recur::Args, osdn::recur::Maps), osdn::recur
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "current device");
     if (dev < 0 || dev >= 64) return fail(OSDN_ERR_UNSUPPORTED, "device index %d above 63", dev);
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr{};
+    cudaLaunchAttribute attr[2] = {};
     cfg.blockDim = dim3(osdn::recur::kThreads);
     cfg.stream = st;
-    cfg.attrs = &attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     auto shape = [&](int R) {
         cfg.dynamicSmemBytes = stages + (R > 1 ? R * slot : 0);
-        attr.val.clusterDim.x = R;
-        cfg.numAttrs = R > 1 ? 1 : 0;
+        attr[1].val.clusterDim.x = R;
+        cfg.numAttrs = R > 1 ? 2 : 1;
     };
     if (!room[dev].clusters[1].load(std::memory_order_acquire)) {   // once a device: limits, then the room
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1733,10 +1751,10 @@ int osdn_recur_step(const osdn_recur_params* p, const void* x, const void* gate,
     for (int i = 0; i < 3; ++i) four = four && element_aligned(ptrs[i], 4 * each[i]);
     auto go = [&](auto v, auto tx, auto tg) {
         const int64_t n = (int64_t)q.B * (q.D / v), blocks = (n + 255) / 256;
-        osdn::recur::step_kernel<v, decltype(tx), decltype(tg)>
-            <<<(unsigned)std::min<int64_t>(blocks, 148 * 8), 256, 0,
-               reinterpret_cast<cudaStream_t>(cuda_stream)>>>(a);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e =
+            launch_chained(osdn::recur::step_kernel<v, decltype(tx), decltype(tg)>,
+                           dim3((unsigned)std::min<int64_t>(blocks, 148 * 8)), 256, 0,
+                           reinterpret_cast<cudaStream_t>(cuda_stream), a);
         return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "recurrence step launch");
     };
     auto types = [&](auto v) {
@@ -1842,9 +1860,9 @@ template <bool kBackward> int launch_heads(const osdn_qk_params* p, osdn::heads:
         a.side[i].blocks = q.side[i].blocks;
     }
     auto go = [&](auto g, auto layout, auto tx) {
-        heads_kernel<g, layout, kBackward, decltype(tx)>
-            <<<q.side[0].blocks + q.side[1].blocks, kThreads, kThreads / g * sizeof(float2) * (a.rot / 2), st>>>(a);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_chained(heads_kernel<g, layout, kBackward, decltype(tx)>,
+                                             dim3(q.side[0].blocks + q.side[1].blocks), kThreads,
+                                             kThreads / g * sizeof(float2) * (a.rot / 2), st, a);
         return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "head norm and rotation launch");
     };
     auto types = [&](auto g, auto layout) {
@@ -1979,9 +1997,9 @@ int osdn_qk_bwd(const osdn_qk_params* p, const void* q, const void* k, const flo
     a.side[1].dw = dwk ? ws + part : nullptr;
     if ((rc = launch_heads<true>(p, a, st))) return rc;
     if (dwq || dwk) {
-        osdn::heads::dw_kernel<<<dim3((p->width + 31) / 32, 2), 1024, 0, st>>>(
-            ws, ws + part, dwq, dwk, (int)sh.side[0].blocks, (int)sh.side[1].blocks, p->width);
-        if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "weight gradient launch");
+        e = launch_chained(osdn::heads::dw_kernel, dim3((p->width + 31) / 32, 2), 1024, 0, st, ws, ws + part, dwq, dwk,
+                           sh.side[0].blocks, sh.side[1].blocks, p->width);
+        if (e != cudaSuccess) return cuda_fail(e, "weight gradient launch");
     }
     return OSDN_OK;
 }

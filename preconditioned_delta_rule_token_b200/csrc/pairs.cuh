@@ -1,8 +1,16 @@
-// Arithmetic on pairs of fp32 values, shared by the recurrence and the heads' kernels.
+// Shared by the recurrence's and the heads' kernels: arithmetic on pairs of fp32 values, and the order of a
+// kernel after the one before it.
 #pragma once
 #include "common.cuh"
 
 namespace osdn {
+
+// These kernels are launched so that they may start while the kernel before them in the stream still runs, once
+// all its blocks have called let_next_start(): what they do before wait_for_previous() touches no device memory, and
+// that returns when the earlier kernel is done and its writes are seen. A chain of them (a training step, a
+// decode loop) then pays for a launch once.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Two fp32 values at a time: one instruction for both (fma, mul, add on f32x2).
 

@@ -385,6 +385,13 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const Args p, const __
     const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
     const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * (kStep == 1 ? 2 : 1);
     const int n = (c < p.D) + (c + kStep < p.D);    // this lane's channels inside the row
+    __shared__ uint64_t full[kStages];
+    Pipe<kStages> pipe{full, p.wait_limit_ns, false, 0};
+    __shared__ uint64_t joined[2];
+    Exchange ex{slots, joined, R, rank};
+    let_next_start();
+    ex.init();
+    wait_for_previous();
     const int len = length_of(p, b);
     const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c;
     const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c;
@@ -395,11 +402,6 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const Args p, const __
     float2 carry = all2(0.f), entry;
     if (p.h0) carry = get_pair<kStep>(p.h0 + (int64_t)b * p.D + c, n);
 
-    __shared__ uint64_t full[kStages];
-    Pipe<kStages> pipe{full, p.wait_limit_ns, false, 0};
-    __shared__ uint64_t joined[2];
-    Exchange ex{slots, joined, R, rank};
-    ex.init();
     auto fetch = [&](int i) {                       // starts the copies of this CTA's i-th tile
         const int t0 = (i * R + rank) * kTile, s = i % kStages;
         if constexpr (kMode == kTma) {
@@ -507,6 +509,13 @@ __global__ void __launch_bounds__(kThreads, kMode == kTma && sizeof(Tg) > sizeof
     const int R = p.R, rank = blockIdx.x % R, unit = blockIdx.x / R;
     const int b = unit / p.cblocks, c0 = (unit % p.cblocks) * W, c = c0 + lane * (kStep == 1 ? 2 : 1);
     const int n = (c < p.D) + (c + kStep < p.D);
+    __shared__ uint64_t full[kStages];
+    Pipe<kStages> pipe{full, p.wait_limit_ns, false, 0};
+    __shared__ uint64_t joined[2];
+    Exchange ex{slots, joined, R, rank};
+    let_next_start();
+    ex.init();
+    wait_for_previous();
     const int len = length_of(p, b);
     const Tx* x = static_cast<const Tx*>(p.x) + b * p.xb + c;
     const Tg* gate = static_cast<const Tg*>(p.gate) + b * p.gb + c;
@@ -520,11 +529,6 @@ __global__ void __launch_bounds__(kThreads, kMode == kTma && sizeof(Tg) > sizeof
     if (p.dfinal) carry = get_pair<kStep>(p.dfinal + (int64_t)b * p.D + c, n);
     auto tile_of = [&](int i) { return (steps - 1 - i) * R + rank; };
 
-    __shared__ uint64_t full[kStages];
-    Pipe<kStages> pipe{full, p.wait_limit_ns, false, 0};
-    __shared__ uint64_t joined[2];
-    Exchange ex{slots, joined, R, rank};
-    ex.init();
     auto fetch = [&](int i) {
         const int t0 = tile_of(i) * kTile, s = i % kStages;
         if constexpr (kMode == kTma) {
@@ -671,6 +675,8 @@ template <int V, typename Tx, typename Tg>
 __global__ void __launch_bounds__(256) step_kernel(const Args p) {
     constexpr int kPairs = V == 4 ? 2 : 1;
     const int per = p.D / V;
+    let_next_start();
+    wait_for_previous();
     const int64_t n = (int64_t)p.B * per;
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t b = i / per, c = (i - b * per) * V;
