@@ -175,3 +175,47 @@ def test_first_calls_of_a_process_inside_a_capture():
     """Nothing has to run before a capture: the kernels' limits and the room on the device are asked for on the host."""
     r = subprocess.run([sys.executable, "-c", _FIRST_IN_A_CAPTURE], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.gpu
+def test_raw_calls_equal_the_wrappers():
+    """The C entry points through the ctypes binding, with everything preallocated."""
+    import ctypes
+
+    import preconditioned_delta_rule_token_b200 as pk
+    g = torch.Generator(device="cuda").manual_seed(1)
+    new = lambda *s, dt=torch.bfloat16: torch.randn(s, generator=g, device="cuda").to(dt)  # noqa: E731
+    x, gate, dh, h0 = new(2, 200, 64), new(2, 200, 64), new(2, 200, 64), new(2, 64, dt=torch.float32)
+    p = pk.osdn_recur_params()
+    p.struct_size, p.B, p.T, p.D, p.gate_form = ctypes.sizeof(p), 2, 200, 64, 2
+    h, f, m = torch.empty_like(x), torch.empty_like(h0), torch.empty(2, 4, 64, device="cuda")
+    pk.osdn_recur_fwd(p, x, gate, h0, None, h, f, m)
+    want = pk.recurrence(x, gate, h0=h0, gate_form="logit", checkpoints=True)
+    assert all(torch.equal(a, b) for a, b in zip((h, f, m), want))
+    dx, dg, d0 = torch.empty_like(x), torch.empty_like(x), torch.empty_like(h0)
+    ws = torch.empty(pk.osdn_recur_bwd_workspace_size(p), dtype=torch.uint8, device="cuda")
+    pk.osdn_recur_bwd(p, x, gate, h0, None, dh, None, None, dx, dg, d0, ws)
+    grads = pk.recurrence_backward(x, gate, dh, h0=h0, checkpoints=m, gate_form="logit")
+    assert all(torch.equal(a, grads[k]) for a, k in ((dx, "dx"), (dg, "dgate"), (d0, "dh0")))
+    s1, s2, o = f.clone(), f.clone(), torch.empty_like(x[:, 0].contiguous())
+    p.stride_x[0] = p.stride_gate[0] = 200 * 64
+    pk.osdn_recur_step(p, x, gate, s1, o)
+    assert torch.equal(o, pk.recurrence_step(x[:, 0], gate[:, 0], s2, gate_form="logit")) and torch.equal(s1, s2)
+
+    q, k, w = new(2, 30, 4, 64), new(2, 30, 2, 64), new(64, dt=torch.float32)
+    fr = torch.tensor(pk.osdn_rope_freqs(32, 10000.0, 0, 1.0, 0, 1.0, 4.0)[0], dtype=torch.float64, device="cuda")
+    p = pk.osdn_qk_params()
+    p.struct_size, p.B, p.T, p.Hq, p.Hk, p.width, p.norm, p.rot_dim = ctypes.sizeof(p), 2, 30, 4, 2, 64, 2, 32
+    p.eps, p.amplitude, p.scale_q, p.scale_k, p.pos0 = 1e-6, 1.0, 1.0, 1.0, 5
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    pk.osdn_qk_fwd(p, q, k, w, w, None, fr, None, qo, ko)
+    how = dict(freqs=fr, norm="rms", wq=w, wk=w, pos0=5)
+    assert all(torch.equal(a, b) for a, b in zip((qo, ko), pk.qk_norm(q, k, **how)))
+    dq, dk, dwq, dwk = torch.empty_like(q), torch.empty_like(k), torch.empty_like(w), torch.empty_like(w)
+    ws = torch.empty(pk.osdn_qk_bwd_workspace_size(p), dtype=torch.uint8, device="cuda")
+    pk.osdn_qk_bwd(p, q, k, w, w, None, fr, None, qo, ko, dq, dk, dwq, dwk, ws)
+    grads = pk.qk_norm_backward(q, k, qo, ko, **how)
+    assert all(torch.equal(a, grads[n]) for a, n in ((dq, "dq"), (dk, "dk"), (dwq, "dwq"), (dwk, "dwk")))
+    p.norm = 0
+    pk.osdn_rope(p, q, None, fr, None, qo, inverse=True)
+    assert torch.equal(qo, pk.rope(q, fr, pos0=5, inverse=True))
