@@ -373,11 +373,10 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B,T,D", ((1, 32768, 1024), (32, 512, 2048)))
+@pytest.mark.parametrize("B,T,D", ((1, 1500, 64), (40, 300, 512), (1, 32768, 1024), (32, 512, 2048)))
 def test_a_wait_that_gives_up_is_reported(B, T, D):
-    """With waits bounded to 1 ns some of thousands of waits for memory give up (alone and in a cluster; the
-    timer that bounds them ticks every microsecond or less): the call ends, the status says so, and the
-    next call is right again."""
+    """With waits bounded to 1 ns those for memory give up (alone and in a cluster): the call ends, the status
+    says so, and the next call is right again."""
     import preconditioned_delta_rule_token_b200 as pk
     x, gate, dh = (torch.randn(B, T, D, device="cuda").bfloat16() for _ in range(3))
     want = pk.recurrence(x, gate, gate_form="logit", checkpoints=True)
