@@ -455,7 +455,8 @@ int osdn_recur_fwd(const osdn_recur_params *p, const void *x, const void *gate, 
  * h0 and lengths, or NULL: the call runs the forward again for them, in a workspace
  * of osdn_recur_bwd_workspace_size() bytes (unused, and nullable, with checkpoints).
  * Where s_t = 0 in OSDN_INPUT_NORM (a_t = 1) the root's unbounded slope counts as
- * 0. Rows of dx and dgate from a sequence's length on go by p->zero_rest. Bitwise
+ * 0; a 1 - a_t^2 below fp32's normal range (a log gate in (-5.9e-39, 0)) counts as
+ * 0 too, in the forward and in the step as well. Rows of dx and dgate from a sequence's length on go by p->zero_rest. Bitwise
  * reproducible. dx and dgate must not overlap an input.
  * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */
 int osdn_recur_bwd_workspace_size(const osdn_recur_params *p, size_t *bytes);

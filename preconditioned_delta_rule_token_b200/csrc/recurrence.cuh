@@ -46,6 +46,8 @@ constexpr int kBwdRun = 8;
 
 // ---- the gate
 
+constexpr float kLeast = 1.17549435e-38f;   // the least normal number
+
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -100,7 +102,8 @@ template <int kScale> __device__ __forceinline__ float2 scale_of(float2 a, float
     return make_float2(root(y.x), root(y.y));
 }
 
-// s, and ds/da (0 where s = 0: the slope of the root is unbounded there).
+// s, and ds/da (0 where s = 0: the slope of the root is unbounded there). The root and its reciprocal take a
+// 1 - a^2 below the normal range as 0, which the reciprocal would make infinite: s = 0 there, as forward.
 template <int kScale> __device__ __forceinline__ float2 scale_of(float2 a, float2 b, float2& ds) {
     if constexpr (kScale == kNone) {
         ds = all2(0.f);
@@ -111,7 +114,7 @@ template <int kScale> __device__ __forceinline__ float2 scale_of(float2 a, float
         return b;
     }
     const float2 y = fma2(a, b, b);
-    const float2 r = make_float2(y.x > 0.f ? rroot(y.x) : 0.f, y.y > 0.f ? rroot(y.y) : 0.f);
+    const float2 r = make_float2(y.x >= kLeast ? rroot(y.x) : 0.f, y.y >= kLeast ? rroot(y.y) : 0.f);
     ds = mul2(a, mul2(r, all2(-1.f)));
     return mul2(y, r);
 }
