@@ -483,7 +483,9 @@ int osdn_recur_step(const osdn_recur_params *p, const void *x, const void *gate,
  *     (y_i, y_j) <- amplitude (y_i cos - y_j sin, y_j cos + y_i sin),
  *     angle = position freqs[pair], formed in 64 bits.
  * Sums are fp32; a row whose sum plus eps lies outside fp32's normal range (a row of
- * zeros without eps, values near 1e19) gives zeros. */
+ * zeros without eps, values near 1e19) gives zeros. With a norm, a NaN makes its whole
+ * row NaN, forward and backward; an infinity gives, in the forward, NaN in its place (and
+ * in its pair's) and zeros beside it. */
 typedef enum { OSDN_NORM_NONE = 0, OSDN_NORM_L2 = 1, OSDN_NORM_RMS = 2 } osdn_norm;
 typedef enum { OSDN_ROPE_HALF = 0, OSDN_ROPE_INTERLEAVED = 1 } osdn_rope_layout;
 

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) heads_kernel(cons
                 float inv = 1.f;
                 if (p.norm != kNoNorm) {
                     const float m = fmaf(group_sum<G>(dot(v, v)), n_inv, p.eps);
-                    inv = m >= 1.17549435e-38f ? rroot(m) : 0.f;   // a row of zeros without eps stays zero
+                    inv = m < 1.17549435e-38f ? 0.f : rroot(m);   // a row of zeros without eps stays zero, NaN stays NaN
                 }
                 const float2 inv2 = all2(inv);
                 Eight y;

@@ -44,3 +44,42 @@ def test_log_gates_below_the_normal_range(gdt, D):
     got, want = run(near), ref.recurrence_grads(x, near, dh, h0, dfinal, None, "log", "norm")
     for t, k in zip(got[2:5], ("dx", "dgate", "dh0")):
         ref.close(t, *want[k], 24 * 70 + 96, k)
+
+
+# ------------------------------------------------------------------ GPU: the norms
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", (torch.bfloat16, torch.float32))
+@pytest.mark.parametrize("width", (40, 64, 128, 256))
+@pytest.mark.parametrize("norm", ("l2", "rms"))
+def test_a_nan_fills_its_row(dt, width, norm):
+    """The norm divides by a sum over the row, so one NaN makes the whole row NaN, forward and backward, and
+    no other row."""
+    import preconditioned_delta_rule_token_b200 as pk
+    g = torch.Generator().manual_seed(2)
+    q, dq = (torch.randn(2, 9, 5, width, generator=g).to(dt).cuda() for _ in range(2))
+    bad = torch.zeros(2, 9, 5, dtype=torch.bool)
+    bad[0, 0, 0] = bad[0, 3, 4] = bad[1, 8, 2] = True
+    bad = bad.cuda()
+    x = q.clone()
+    x[..., 7][bad] = float("nan")
+    how = dict(freqs=ref.plain_freqs(16).cuda(), norm=norm)
+    out, want = pk.qk_norm(x, x, **how), pk.qk_norm(q, q, **how)
+    got, grad = pk.qk_norm_backward(x, x, dq, dq, **how), pk.qk_norm_backward(q, q, dq, dq, **how)
+    for a, b in ((out[0], want[0]), (out[1], want[1]), (got["dq"], grad["dq"]), (got["dk"], grad["dk"])):
+        assert bool(a[bad].isnan().all()) and torch.equal(a[~bad], b[~bad])
+
+
+@pytest.mark.gpu
+def test_an_infinity_keeps_to_its_row():
+    """x / sqrt(infinity): NaN in the infinity's place (without rotation), zeros beside it."""
+    import preconditioned_delta_rule_token_b200 as pk
+    q = torch.randn(1, 4, 2, 64, generator=torch.Generator().manual_seed(3)).cuda()
+    want = pk.qk_norm(q, None)[0]
+    q[0, 2, 1, 9] = float("inf")
+    out = pk.qk_norm(q, None)[0]
+    row = torch.zeros(64, device="cuda")
+    row[9] = float("nan")
+    assert torch.equal(out[0, 2, 1].isnan(), row.isnan()) and bool((out[0, 2, 1].nan_to_num() == 0).all())
+    want[0, 2, 1] = out[0, 2, 1] = 0
+    assert torch.equal(out, want)
