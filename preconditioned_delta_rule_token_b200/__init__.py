@@ -17,6 +17,8 @@ All tensors must be CUDA tensors; there is no CPU path.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from ._binding import (OSDN_BF16, OSDN_ERR_CUDA, OSDN_ERR_INVALID_ARG, OSDN_ERR_TIMEOUT, OSDN_ERR_UNSUPPORTED,
@@ -44,6 +46,12 @@ __all__ = ["forward", "backward", "step", "osdn_bwd", "osdn_bwd_gated", "osdn_bw
            "osdn_qk_bwd_workspace_size", "osdn_rope", "osdn_rope_freqs"]
 
 
+def _on(stream):
+    """For what a call drops when it returns (workspaces, gradients on the way): allocated on the stream that its
+    kernels run on, or the memory could go to the current stream's next allocation while they still use it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def forward(q, k, v, beta, r=None, d0=None, S0=None, eta=1e-2, chunk=64, workspace=None, stream=None,
             apf_anchor=False, alpha=None, qk=None, positions=None):
     """OSDN forward. q, k [B,T,H,dk]; v [B,T,H,dv]; beta, r [B,T,H] (bf16 or fp32,
@@ -64,7 +72,8 @@ def forward(q, k, v, beta, r=None, d0=None, S0=None, eta=1e-2, chunk=64, workspa
     final_S = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
     final_d = torch.empty((B, H, dk), dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = torch.empty(osdn_fwd_workspace_size(p), dtype=torch.uint8, device=dev)
+        with _on(stream):
+            workspace = torch.empty(osdn_fwd_workspace_size(p), dtype=torch.uint8, device=dev)
     if alpha is None:
         osdn_fwd(p, q, k, v, beta, r, d0, S0, out, final_S, final_d, workspace, stream)
     else:
@@ -86,7 +95,8 @@ def forward_host(q, k, v, beta, r=None, d0=None, S0=None, eta=1e-2, chunk=64, gr
     final_S = torch.empty((B, H, dv, dk), dtype=torch.float32, pin_memory=pin)
     final_d = torch.empty((B, H, dk), dtype=torch.float32, pin_memory=pin)
     if device_buffer is None:
-        device_buffer = torch.empty(osdn_fwd_host_buffer_size(p, groups), dtype=torch.uint8, device="cuda")
+        with _on(stream):
+            device_buffer = torch.empty(osdn_fwd_host_buffer_size(p, groups), dtype=torch.uint8, device="cuda")
     osdn_fwd_host(p, q, k, v, beta, r, d0, S0, out, final_S, final_d, device_buffer, groups, stream)
     return out, final_S, final_d
 
@@ -109,12 +119,15 @@ def backward(q, k, v, beta, dout, r=None, d0=None, S0=None, dS_final=None, dd_fi
     dv = v.shape[-1]
     p = make_params(B, T, H, dk, dv, k.dtype, eta, chunk, apf_anchor)
     dev, dt = k.device, k.dtype
-    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
-         "dbeta": torch.empty_like(beta), "dr": None if r is None else torch.empty_like(r),
-         "dd0": torch.empty((B, H, dk), dtype=torch.float32, device=dev),
-         "dS0": torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)}
+    with _on(None if qk is None else stream):   # with qk these two are on the way to the raw q's and k's
+        g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k)}
+    g.update({"dv": torch.empty_like(v),
+              "dbeta": torch.empty_like(beta), "dr": None if r is None else torch.empty_like(r),
+              "dd0": torch.empty((B, H, dk), dtype=torch.float32, device=dev),
+              "dS0": torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)})
     if workspace is None:
-        workspace = torch.empty(osdn_bwd_workspace_size(p), dtype=torch.uint8, device=dev)
+        with _on(stream):
+            workspace = torch.empty(osdn_bwd_workspace_size(p), dtype=torch.uint8, device=dev)
     if alpha is None:
         osdn_bwd(p, q, k, v, beta, r, d0, S0, dout, dS_final, dd_final, g["dq"], g["dk"], g["dv"], g["dbeta"],
                  g["dr"], g["dd0"], g["dS0"], workspace, stream)
@@ -138,7 +151,8 @@ def residual_ratio(k, beta, r=None, d0=None, eta=1e-2, stream=None, apf_anchor=F
     rho = torch.empty((B, T, H), dtype=torch.float32, device=k.device)
     q_geo = torch.empty((B, H), dtype=torch.float32, device=k.device)
     d = torch.empty((B, H, dk), dtype=torch.float32, device=k.device)
-    ws = torch.empty(max(osdn_fwd_workspace_size(p), 256), dtype=torch.uint8, device=k.device)
+    with _on(stream):
+        ws = torch.empty(max(osdn_fwd_workspace_size(p), 256), dtype=torch.uint8, device=k.device)
     osdn_fwd_scan_diag(p, k, beta, r, d0, d, rho, q_geo, ws, stream)
     return rho, q_geo, d
 

@@ -6,6 +6,73 @@ import pytest
 import torch
 
 from tests import _layer_ref as ref
+from tests._util import BF16_TOL
+
+
+# ------------------------------------------------------------------ CPU: what a call allocates on which stream
+
+def _fake_calls(pk, monkeypatch):
+    """The package's calls with the library, the streams and the norms replaced by fakes: a list of
+    (call, name, whether it was allocated on the call's stream) for every tensor that reaches the library."""
+    import contextlib
+    inside, where, seen = [0], {}, []
+
+    @contextlib.contextmanager
+    def stream(s):
+        inside[0] += 1
+        yield
+        inside[0] -= 1
+
+    def made(f):
+        def make(*a, **kw):
+            kw.pop("device", None), kw.pop("pin_memory", None)
+            t = f(*a, **kw)
+            where[id(t)] = (inside[0] > 0, t)
+            return t
+        return make
+
+    def raw(call, names):
+        def fake(p, *args):
+            seen.extend((call, n, where[id(t)][0]) for n, t in zip(names, args) if id(t) in where)
+        return fake
+
+    monkeypatch.setattr(pk.torch.cuda, "stream", stream)
+    monkeypatch.setattr(pk.torch, "empty", made(torch.empty))
+    monkeypatch.setattr(pk.torch, "empty_like", made(torch.empty_like))
+    for n in ("osdn_fwd_workspace_size", "osdn_bwd_workspace_size"):
+        monkeypatch.setattr(pk, n, lambda p: 256)
+    monkeypatch.setattr(pk, "osdn_fwd_host_buffer_size", lambda p, groups: 256)
+    fwd = "q k v beta r d0 S0 out final_S final_d workspace".split()
+    bwd = "q k v beta r d0 S0 dout dS_final dd_final dq dk dv dbeta dr dd0 dS0 workspace".split()
+    monkeypatch.setattr(pk, "osdn_fwd", raw("forward", fwd))
+    monkeypatch.setattr(pk, "osdn_fwd_host", raw("forward_host", fwd))
+    monkeypatch.setattr(pk, "osdn_bwd", raw("backward", bwd))
+    monkeypatch.setattr(pk, "osdn_fwd_scan_diag", raw("residual_ratio", "k beta r d0 d rho q_geo workspace".split()))
+    return seen
+
+
+class _FakeNorm:
+    def apply(self, q, k, positions=None, stream=None):
+        return q.clone(), k.clone()
+
+    def gradients(self, q, k, dq, dk, positions=None, stream=None):
+        return {"dq": dq.clone(), "dk": dk.clone(), "dwq": None, "dwk": None}
+
+
+def test_what_a_call_drops_is_allocated_on_its_stream(monkeypatch):
+    """Workspaces, and with qk the gradients of the normalised q and k, are dropped when the call returns, with its
+    kernels still ahead: they have to come from the pool of the stream that these run on."""
+    import preconditioned_delta_rule_token_b200 as pk
+    seen = _fake_calls(pk, monkeypatch)
+    q, b, s = torch.zeros(1, 4, 1, 64), torch.zeros(1, 4, 1), object()
+    pk.forward(q, q, q, b, stream=s, qk=_FakeNorm())
+    pk.backward(q, q, q, b, q, stream=s, qk=_FakeNorm())
+    pk.residual_ratio(q, b, stream=s)
+    pk.forward_host(q, q, q, b, stream=s)
+    dropped = [e for e in seen if e[1] == "workspace" or e[:2] in (("backward", "dq"), ("backward", "dk"))]
+    assert len(dropped) == 6 and all(e[2] for e in dropped), dropped
+    kept = [e for e in seen if e not in dropped]
+    assert kept and not any(e[2] for e in kept)      # results: on the caller's stream, as without qk
 
 
 # ------------------------------------------------------------------ GPU: the recurrence
@@ -83,3 +150,40 @@ def test_an_infinity_keeps_to_its_row():
     assert torch.equal(out[0, 2, 1].isnan(), row.isnan()) and bool((out[0, 2, 1].nan_to_num() == 0).all())
     want[0, 2, 1] = out[0, 2, 1] = 0
     assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------ GPU: the calls together
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gated", (False, True))
+def test_training_step_on_another_stream(gated):
+    """forward() and backward() with qk on a side stream that is still busy, while the current stream allocates and
+    writes: the results are those of the calls on the current stream. The forward's are bit for bit the same; the
+    delta rule's backward sums in an order that may change, so its gradients are compared as its own tests do."""
+    import preconditioned_delta_rule_token_b200 as pk
+    B, T, H, W = 2, 256, 4, 128
+    g = torch.Generator().manual_seed(5)
+    new = lambda *s: torch.randn(s, generator=g).bfloat16().cuda()  # noqa: E731
+    q, k, v, dout, beta = new(B, T, H, W), new(B, T, H, W), new(B, T, H, W), new(B, T, H, W), new(B, T, H).sigmoid()
+    alpha = torch.sigmoid(3 + new(B, T, H)) if gated else None
+    qk = pk.QkNorm(norm="rms", wq=torch.ones(W, device="cuda"), freqs=pk.rope_frequencies(W)[0], scale_k=W ** -0.5)
+
+    def run(stream):
+        out = pk.forward(q, k, v, beta, alpha=alpha, qk=qk, eta=0.1, stream=stream)
+        grads = pk.backward(q, k, v, beta, dout, alpha=alpha, qk=qk, eta=0.1, stream=stream)
+        return [*out, *(t for t in grads.values() if t is not None)]
+
+    want = run(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)            # about 10 ms
+        got = run(side)
+        junk = [torch.full((B, T, H, W), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+        junk += [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (1 << 20, 1 << 22, 1 << 24, 1 << 26)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[:3], got))
+        for a, b in zip(want[3:], got[3:]):
+            assert float((a.double() - b.double()).abs().max()) <= BF16_TOL * float(a.double().abs().max())
+        del junk
