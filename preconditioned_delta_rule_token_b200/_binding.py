@@ -422,9 +422,15 @@ def osdn_bwd_gated(params, q, k, v, beta, r, alpha, d0, S0, dout, dS_final, dd_f
                                 ctypes.c_size_t(_ws_bytes(workspace)), _stream(stream)))
 
 
-def _address(t):
-    """Device address of a tensor (None: NULL); its layout is in the parameter block."""
-    return None if t is None else t.data_ptr()
+def _ptr_rows(t):
+    """Address of a token tensor whose last dimension is contiguous; its other strides are in the parameter block."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise OsdnError(OSDN_ERR_INVALID_ARG, "tensor is not on a CUDA device (the library has no CPU path)")
+    if t.numel() > 0 and t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise OsdnError(OSDN_ERR_INVALID_ARG, "the last dimension of a token tensor must be contiguous")
+    return t.data_ptr()
 
 
 def _handle(stream):
@@ -434,8 +440,8 @@ def _handle(stream):
 
 def osdn_recur_fwd(params, x, gate, h0, lengths, h, final_h, checkpoints, stream=None):
     """Raw C-ABI call of the gated linear recurrence (every tensor preallocated; strides in params)."""
-    _check(lib().osdn_recur_fwd(params, x.data_ptr(), gate.data_ptr(), _address(h0), _address(lengths), _address(h),
-                                _address(final_h), _address(checkpoints), _handle(stream)))
+    _check(lib().osdn_recur_fwd(params, _ptr_rows(x), _ptr_rows(gate), _ptr(h0), _ptr(lengths), _ptr_rows(h),
+                                _ptr(final_h), _ptr(checkpoints), _handle(stream)))
 
 
 def osdn_recur_bwd_workspace_size(params: osdn_recur_params) -> int:
@@ -446,20 +452,20 @@ def osdn_recur_bwd_workspace_size(params: osdn_recur_params) -> int:
 
 def osdn_recur_bwd(params, x, gate, h0, lengths, dh, dfinal_h, checkpoints, dx, dgate, dh0, workspace, stream=None):
     """Raw C-ABI call of the recurrence's backward."""
-    _check(lib().osdn_recur_bwd(params, x.data_ptr(), gate.data_ptr(), _address(h0), _address(lengths), dh.data_ptr(),
-                                _address(dfinal_h), _address(checkpoints), dx.data_ptr(), dgate.data_ptr(),
-                                _address(dh0), _address(workspace), _ws_bytes(workspace), _handle(stream)))
+    _check(lib().osdn_recur_bwd(params, _ptr_rows(x), _ptr_rows(gate), _ptr(h0), _ptr(lengths), _ptr_rows(dh),
+                                _ptr(dfinal_h), _ptr(checkpoints), _ptr(dx), _ptr(dgate), _ptr(dh0), _ptr(workspace),
+                                _ws_bytes(workspace), _handle(stream)))
 
 
 def osdn_recur_step(params, x, gate, state, h, stream=None):
     """Raw C-ABI call: one token of the recurrence, state updated in place."""
-    _check(lib().osdn_recur_step(params, x.data_ptr(), gate.data_ptr(), state.data_ptr(), h.data_ptr(), _handle(stream)))
+    _check(lib().osdn_recur_step(params, _ptr_rows(x), _ptr_rows(gate), _ptr(state), _ptr_rows(h), _handle(stream)))
 
 
 def osdn_qk_fwd(params, q, k, wq, wk, positions, freqs, lengths, q_out, k_out, stream=None):
     """Raw C-ABI call of the query and key norms with the rotation (strides in params)."""
-    _check(lib().osdn_qk_fwd(params, q.data_ptr(), _address(k), _address(wq), _address(wk), _address(positions),
-                             _address(freqs), _address(lengths), q_out.data_ptr(), _address(k_out), _handle(stream)))
+    _check(lib().osdn_qk_fwd(params, _ptr_rows(q), _ptr_rows(k), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(freqs),
+                             _ptr(lengths), _ptr_rows(q_out), _ptr_rows(k_out), _handle(stream)))
 
 
 def osdn_qk_bwd_workspace_size(params: osdn_qk_params) -> int:
@@ -471,16 +477,15 @@ def osdn_qk_bwd_workspace_size(params: osdn_qk_params) -> int:
 def osdn_qk_bwd(params, q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
                 stream=None):
     """Raw C-ABI call of the backward of osdn_qk_fwd."""
-    _check(lib().osdn_qk_bwd(params, q.data_ptr(), _address(k), _address(wq), _address(wk), _address(positions),
-                             _address(freqs), _address(lengths), dq_out.data_ptr(), _address(dk_out), dq.data_ptr(),
-                             _address(dk), _address(dwq), _address(dwk), _address(workspace), _ws_bytes(workspace),
-                             _handle(stream)))
+    _check(lib().osdn_qk_bwd(params, _ptr_rows(q), _ptr_rows(k), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(freqs),
+                             _ptr(lengths), _ptr_rows(dq_out), _ptr_rows(dk_out), _ptr(dq), _ptr(dk), _ptr(dwq),
+                             _ptr(dwk), _ptr(workspace), _ws_bytes(workspace), _handle(stream)))
 
 
 def osdn_rope(params, x, positions, freqs, lengths, out, inverse=False, stream=None):
     """Raw C-ABI call of the rotation alone."""
-    _check(lib().osdn_rope(params, x.data_ptr(), _address(positions), _address(freqs), _address(lengths),
-                           out.data_ptr(), 1 if inverse else 0, _handle(stream)))
+    _check(lib().osdn_rope(params, _ptr_rows(x), _ptr(positions), _ptr(freqs), _ptr(lengths), _ptr_rows(out),
+                           1 if inverse else 0, _handle(stream)))
 
 
 def osdn_rope_freqs(rot_dim, base, scaling, factor, original_length, low_turns, high_turns):

@@ -75,6 +75,48 @@ def test_what_a_call_drops_is_allocated_on_its_stream(monkeypatch):
     assert kept and not any(e[2] for e in kept)      # results: on the caller's stream, as without qk
 
 
+
+_RAW = {
+    "osdn_recur_fwd": "x gate h0 lengths h final_h checkpoints",
+    "osdn_recur_bwd": "x gate h0 lengths dh dfinal_h checkpoints dx dgate dh0 workspace",
+    "osdn_recur_step": "x gate state h",
+    "osdn_qk_fwd": "q k wq wk positions freqs lengths q_out k_out",
+    "osdn_qk_bwd": "q k wq wk positions freqs lengths dq_out dk_out dq dk dwq dwk workspace",
+    "osdn_rope": "x positions freqs lengths out",
+}
+
+
+class _Fake(torch.Tensor):
+    """A host tensor that says it is on a CUDA device (its address never reaches the library here)."""
+    @property
+    def is_cuda(self):
+        return True
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, names in _RAW.items() for n in names.split()])
+def test_raw_calls_refuse_host_and_strided_tensors(osdn_lib, monkeypatch, call, name):
+    """Every tensor argument: a host tensor, and one whose last dimension is not contiguous, is refused before the
+    library sees an address; optional ones may be None."""
+    import preconditioned_delta_rule_token_b200 as pk
+    reached = []
+
+    class Library:
+        def __getattr__(self, n):
+            return lambda *a: reached.append(n) or 0
+
+    monkeypatch.setattr(osdn_lib, "lib", Library)
+    monkeypatch.setattr(osdn_lib, "_handle", lambda stream: 0)
+    names = _RAW[call].split()
+    good = lambda: torch.zeros(4, 6).as_subclass(_Fake)  # noqa: E731
+    getattr(pk, call)(None, *[good() for _ in names])
+    assert reached == [call]
+    for bad in (torch.zeros(4, 6), torch.zeros(6, 4).as_subclass(_Fake).t()):
+        with pytest.raises(pk.OsdnError):
+            getattr(pk, call)(None, *[bad if n == name else good() for n in names])
+    getattr(pk, call)(None, *[None if n == name else good() for n in names])   # NULL: the library's own check
+    assert reached == [call, call]
+
+
 # ------------------------------------------------------------------ GPU: the recurrence
 
 @pytest.mark.gpu
