@@ -97,6 +97,15 @@ def _held(dev, name, t, shape, dtype, dense=True):
         _bad("%s is not contiguous" % name)
 
 
+def _scratch(dev, workspace):
+    """Checks a workspace that the caller gave: dense memory of the tensors' device (its size is the library's check)."""
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_cuda:
+        _bad("workspace must be a tensor on %s (the library has no CPU path)" % dev)
+    if not workspace.is_contiguous():
+        _bad("workspace is not contiguous")
+    return workspace
+
+
 def _strides(name, t, n):
     """The first n strides of a token tensor whose last dimension is contiguous (zeros: dense)."""
     if t is None or t.is_contiguous():
@@ -190,7 +199,9 @@ def recurrence_backward(x, gate, dh, h0=None, dfinal_h=None, lengths=None, check
                                        workspace)
     g = {"dx": _C.like(x), "dgate": _C.like(gate),
          "dh0": _C.floats(x, x.shape[0], x.shape[2])}
-    if checkpoints is None and workspace is None:
+    if workspace is not None:
+        _scratch(x.device, workspace)
+    elif checkpoints is None:
         workspace = torch.empty(B.osdn_recur_bwd_workspace_size(kept[0]), dtype=torch.uint8, device=x.device)
     _done(_C.recur_bwd(kept[1], x, gate, h0, lengths, dh, dfinal_h, checkpoints, g["dx"], g["dgate"], g["dh0"],
                        workspace))
@@ -292,7 +303,9 @@ def qk_norm_backward(q, k, dq_out, dk_out, freqs=None, positions=None, norm="l2"
     g = {"dq": _C.like(q), "dk": None if k is None else _C.like(k),
          "dwq": None if wq is None else _C.like(wq),
          "dwk": None if wk is None or k is None else _C.like(wk)}
-    if workspace is None and (g["dwq"] is not None or g["dwk"] is not None):
+    if workspace is not None:
+        _scratch(q.device, workspace)
+    elif g["dwq"] is not None or g["dwk"] is not None:
         workspace = torch.empty(B.osdn_qk_bwd_workspace_size(kept[0]), dtype=torch.uint8, device=q.device)
     _done(_C.qk_bwd(kept[1], q, k, wq, wk, positions, freqs, lengths, dq_out, dk_out, g["dq"], g["dk"], g["dwq"],
                     g["dwk"], workspace))

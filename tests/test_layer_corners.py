@@ -117,6 +117,59 @@ def test_raw_calls_refuse_host_and_strided_tensors(osdn_lib, monkeypatch, call, 
     assert reached == [call, call]
 
 
+
+class _FakeCalls:
+    """The extension module's functions on fake tensors; `reached` lists the library's functions called."""
+    def __init__(self):
+        self.reached = []
+
+    def layouts(self, *ts):
+        return repr([None if t is None else (t.dtype, t.shape, t.stride()) for t in ts])
+
+    def here(self, t):
+        return True
+
+    def like(self, t):
+        return torch.empty(t.shape, dtype=t.dtype)
+
+    def floats(self, t, *sizes):
+        return torch.empty(sizes)
+
+    def __getattr__(self, name):
+        return lambda params, *a: self.reached.append((name, params, a)) or 0
+
+
+@pytest.fixture
+def fake_layer(monkeypatch):
+    """The layer's wrappers without a GPU: (module, its calls)."""
+    from preconditioned_delta_rule_token_b200 import _layer
+    calls = _FakeCalls()
+    monkeypatch.setattr(_layer, "_C", calls)
+    monkeypatch.setattr(_layer, "_RECUR", _layer._Kept())
+    monkeypatch.setattr(_layer, "_HEADS", _layer._Kept())
+    return _layer, calls
+
+
+def _fake(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(_Fake)
+
+
+def test_given_workspaces_are_checked(fake_layer):
+    """A workspace on the host, not dense (its elements are more than its memory) or no tensor is refused before the
+    call."""
+    import preconditioned_delta_rule_token_b200 as pk
+    layer, calls = fake_layer
+    x, q, w = _fake(2, 100, 16), _fake(2, 5, 1, 64), _fake(64)
+    for call, name in ((lambda ws: layer.recurrence_backward(x, x, x, workspace=ws), "recur_bwd"),
+                       (lambda ws: layer.qk_norm_backward(q, q, q, q, wq=w, workspace=ws), "qk_bwd")):
+        for ws in (torch.zeros(1 << 20), _fake(1).expand(1 << 20), _fake(64, 64).t(), 1 << 20):
+            with pytest.raises(pk.OsdnError):
+                call(ws)
+        assert not calls.reached
+        call(_fake(1 << 10))
+        assert calls.reached.pop()[0] == name
+
+
 # ------------------------------------------------------------------ GPU: the recurrence
 
 @pytest.mark.gpu
@@ -229,3 +282,22 @@ def test_training_step_on_another_stream(gated):
         for a, b in zip(want[3:], got[3:]):
             assert float((a.double() - b.double()).abs().max()) <= BF16_TOL * float(a.double().abs().max())
         del junk
+
+
+@pytest.mark.gpu
+def test_workspaces_of_the_caller():
+    """A given workspace gives what an own one gives; one that is too small is refused by the library."""
+    import preconditioned_delta_rule_token_b200 as pk
+    g = torch.Generator().manual_seed(6)
+    x, gate, dh = (torch.randn(2, 150, 40, generator=g).cuda() for _ in range(3))
+    q, w = torch.randn(2, 50, 4, 64, generator=g).cuda(), torch.ones(64, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    a = pk.recurrence_backward(x, gate, dh, gate_form="logit")
+    b = pk.recurrence_backward(x, gate, dh, gate_form="logit", workspace=ws)
+    c = pk.qk_norm_backward(q, q, q, q, wq=w, wk=w)
+    d = pk.qk_norm_backward(q, q, q, q, wq=w, wk=w, workspace=ws)
+    assert all(torch.equal(a[n], b[n]) for n in a) and all(torch.equal(c[n], d[n]) for n in c)
+    for call in (lambda: pk.recurrence_backward(x, gate, dh, gate_form="logit", workspace=ws[:64]),
+                 lambda: pk.qk_norm_backward(q, q, q, q, wq=w, workspace=ws[:64])):
+        with pytest.raises(pk.OsdnError, match="too small"):
+            call()
