@@ -52,6 +52,19 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _normed(qk, q, k, positions, stream):
+    """q and k through qk_norm where its options are given. It also takes fewer key heads than query heads; the
+    delta rule wants as many, and its kernels would read q by k's heads."""
+    if qk is None:
+        if positions is not None:
+            raise OsdnError(OSDN_ERR_INVALID_ARG, "positions need qk")
+        return q, k
+    if q.shape != k.shape:
+        raise OsdnError(OSDN_ERR_INVALID_ARG, "the delta rule takes q and k of one shape (got %s and %s)"
+                        % (tuple(q.shape), tuple(k.shape)))
+    return qk.apply(q, k, positions, stream)
+
+
 def forward(q, k, v, beta, r=None, d0=None, S0=None, eta=1e-2, chunk=64, workspace=None, stream=None,
             apf_anchor=False, alpha=None, qk=None, positions=None):
     """OSDN forward. q, k [B,T,H,dk]; v [B,T,H,dv]; beta, r [B,T,H] (bf16 or fp32,
@@ -60,10 +73,7 @@ def forward(q, k, v, beta, r=None, d0=None, S0=None, eta=1e-2, chunk=64, workspa
     S_t = alpha_t S_{t-1} (I - beta k kw^T) + beta v kw^T (bf16, dk = dv = 128). qk (a QkNorm): q and k
     first go through qk_norm with these options, at `positions` [B,T] int64 (None: 0, 1, ...).
     Returns (out [B,T,H,dv], final_S [B,H,dv,dk] fp32, final_d [B,H,dk] fp32)."""
-    if qk is not None:
-        q, k = qk.apply(q, k, positions, stream)
-    elif positions is not None:
-        raise OsdnError(OSDN_ERR_INVALID_ARG, "positions need qk")
+    q, k = _normed(qk, q, k, positions, stream)
     B, T, H, dk = k.shape
     dv = v.shape[-1]
     p = make_params(B, T, H, dk, dv, k.dtype, eta, chunk, apf_anchor)
@@ -110,11 +120,8 @@ def backward(q, k, v, beta, dout, r=None, d0=None, S0=None, dS_final=None, dd_fi
     input dtype and dd0 [B,H,dk], dS0 [B,H,dv,dk] fp32. With qk and positions as in forward(), dq and dk
     are of the q and k before qk_norm (which may be column slices of a projection), and dwq, dwk [dk]
     fp32 of its weights (None without) come too."""
-    if qk is not None:
-        given = q, k
-        q, k = qk.apply(q, k, positions, stream)
-    elif positions is not None:
-        raise OsdnError(OSDN_ERR_INVALID_ARG, "positions need qk")
+    given = q, k
+    q, k = _normed(qk, q, k, positions, stream)
     B, T, H, dk = k.shape
     dv = v.shape[-1]
     p = make_params(B, T, H, dk, dv, k.dtype, eta, chunk, apf_anchor)
@@ -164,11 +171,11 @@ def step(q, k, v, beta, S, d, r=None, eta=1e-2, stream=None, d_anchor=None, apf_
     d_anchor [B,H,dk] fp32 given) pulls d toward d_anchor (ones when None); alpha [B,H] decays S
     first (gated OSDN). qk (a QkNorm): q and k first go through qk_norm at `positions` [B] int64 (None: 0).
     Returns out [B,H,dv]."""
-    if qk is not None:
-        q, k = (t.squeeze(1) for t in qk.apply(q.unsqueeze(1), k.unsqueeze(1),
-                                               None if positions is None else positions.unsqueeze(1), stream))
-    elif positions is not None:
-        raise OsdnError(OSDN_ERR_INVALID_ARG, "positions need qk")
+    if qk is None:
+        _normed(qk, q, k, positions, stream)
+    else:
+        q, k = (t.squeeze(1) for t in _normed(qk, q.unsqueeze(1), k.unsqueeze(1),
+                                              None if positions is None else positions.unsqueeze(1), stream))
     B, H, dk = k.shape
     dv = v.shape[-1]
     p = make_params(B, 1, H, dk, dv, k.dtype, eta, apf_anchor=apf_anchor or d_anchor is not None)

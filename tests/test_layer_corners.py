@@ -76,6 +76,20 @@ def test_what_a_call_drops_is_allocated_on_its_stream(monkeypatch):
 
 
 
+@pytest.mark.parametrize("heads", ((4, 2), (2, 4)))
+def test_the_delta_rule_wants_as_many_key_heads(monkeypatch, heads):
+    """qk_norm takes shared key heads, forward, backward and step do not: they refuse them before any kernel."""
+    import preconditioned_delta_rule_token_b200 as pk
+    seen = _fake_calls(pk, monkeypatch)
+    (q, k), b = (torch.zeros(1, 4, n, 64) for n in heads), torch.zeros(1, 4, heads[1])
+    v, S, d = torch.zeros_like(k), torch.zeros(1, heads[1], 64, 64), torch.zeros(1, heads[1], 64)
+    for call in (lambda: pk.forward(q, k, v, b, qk=_FakeNorm()), lambda: pk.backward(q, k, v, b, v, qk=_FakeNorm()),
+                 lambda: pk.step(q[:, 0], k[:, 0], v[:, 0], b[:, 0], S, d, qk=_FakeNorm())):
+        with pytest.raises(pk.OsdnError, match="one shape"):
+            call()
+    assert not seen
+
+
 _RAW = {
     "osdn_recur_fwd": "x gate h0 lengths h final_h checkpoints",
     "osdn_recur_bwd": "x gate h0 lengths dh dfinal_h checkpoints dx dgate dh0 workspace",
