@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from dataclasses import dataclass, fields
 
 import torch
@@ -226,6 +227,16 @@ def recurrence_step(x, gate, state, gate_form="decay", input_scale="none", out=N
 _HEADS = _Kept()
 
 
+def _numbers(eps, amplitude, scale_q, scale_k, pos0):
+    """The numbers of a call by value: a block is kept by them, and a tensor in their place (a learned scale) would
+    be known by its identity while its value changes."""
+    try:
+        return float(eps), float(amplitude), float(scale_q), float(scale_k), operator.index(pos0)
+    except (TypeError, ValueError, RuntimeError):
+        _bad("eps, amplitude and the scales are numbers, pos0 is an integer (got %s)" %
+             ", ".join(type(v).__name__ for v in (eps, amplitude, scale_q, scale_k, pos0)))
+
+
 def _heads_params(q, k, freqs, positions, lengths, norm, layout, wq, wk, out_q, out_k, numbers, names):
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         _bad("%s [B, T, H, width]" % ("%s and %s are" % names[:2] if names[1] else "%s is" % names[0]))
@@ -267,7 +278,7 @@ def qk_norm(q, k, freqs=None, positions=None, norm="l2", eps=1e-6, wq=None, wk=N
     [B,T] int64 (None: pos0 + t). lengths [B] int32: tokens from a sequence's length on give zeros
     (rows of a given q_out, k_out stay as they were). q_out may be q, k_out may be k.
     Returns (q_out, k_out)."""
-    numbers = (eps, amplitude, scale_q, scale_k, pos0)
+    numbers = _numbers(eps, amplitude, scale_q, scale_k, pos0)
     key = (norm, layout, numbers, _C.layouts(q, k, freqs, positions, lengths, wq, wk, q_out, k_out))
     kept = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
         q, k, freqs, positions, lengths, norm, layout, wq, wk, q_out, k_out, numbers, ("q", "k", "q_out", "k_out")))
@@ -292,7 +303,7 @@ def qk_norm_backward(q, k, dq_out, dk_out, freqs=None, positions=None, norm="l2"
     [width] fp32 (None without the weight)."""
     if (k is None) != (dk_out is None):
         _bad("k and dk_out go together")
-    numbers = (eps, amplitude, scale_q, scale_k, pos0)
+    numbers = _numbers(eps, amplitude, scale_q, scale_k, pos0)
     key = ("bwd", norm, layout, numbers, _C.layouts(q, k, freqs, positions, lengths, wq, wk, dq_out, dk_out))
     kept = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
         q, k, freqs, positions, lengths, norm, layout, wq, wk, dq_out, dk_out, numbers, ("q", "k", "dq_out", "dk_out")))
@@ -341,7 +352,7 @@ def rope(x, freqs, positions=None, layout="half", amplitude=1.0, scale=1.0, pos0
     """The position rotation alone on x [B,T,H,width]: see qk_norm for freqs, positions, layout and lengths.
     inverse=True turns back with the same amplitude: it takes the gradient of the result to that of x.
     `out` may be x. Returns the rotated tensor."""
-    numbers = (0.0, amplitude, scale, 1.0, pos0)
+    numbers = _numbers(0.0, amplitude, scale, 1.0, pos0)
     key = ("rope", layout, numbers, _C.layouts(x, freqs, positions, lengths, out))
     kept = _HEADS.get(key)
     if kept is None:

@@ -184,6 +184,37 @@ def test_given_workspaces_are_checked(fake_layer):
         assert calls.reached.pop()[0] == name
 
 
+def test_numbers_are_taken_by_value(fake_layer):
+    """A scale, an eps or an amplitude held in a tensor that changes in place between two calls: each call has the
+    value of its time. What is no number is refused."""
+    import preconditioned_delta_rule_token_b200 as pk
+    layer, calls = fake_layer
+    q, f = _fake(2, 5, 1, 64), _fake(32, dtype=torch.float64)
+    field = {"scale": "scale_q"}
+
+    def params(call):
+        call()
+        address = calls.reached[-1][1]
+        return layer.B.osdn_qk_params.from_address(address)
+
+    for name, call in [(n, lambda **kw: layer.qk_norm(q, q, f, **kw)) for n in ("eps", "amplitude", "scale_q", "scale_k")] + \
+                      [(n, lambda **kw: layer.qk_norm_backward(q, q, q, q, f, **kw)) for n in ("eps", "scale_k")] + \
+                      [(n, lambda **kw: layer.rope(q, f, **kw)) for n in ("amplitude", "scale")]:
+        t = torch.tensor(0.5)
+        assert getattr(params(lambda: call(**{name: t})), field.get(name, name)) == 0.5
+        t.fill_(2.0)
+        assert getattr(params(lambda: call(**{name: t})), field.get(name, name)) == 2.0
+        for bad in ("x", torch.ones(2), None):
+            with pytest.raises(pk.OsdnError):
+                call(**{name: bad})
+    p = torch.tensor(3)
+    assert params(lambda: layer.rope(q, f, pos0=p)).pos0 == 3
+    p += 1
+    assert params(lambda: layer.rope(q, f, pos0=p)).pos0 == 4
+    with pytest.raises(pk.OsdnError):
+        layer.rope(q, f, pos0=1.5)
+
+
 # ------------------------------------------------------------------ GPU: the recurrence
 
 @pytest.mark.gpu
@@ -315,3 +346,13 @@ def test_workspaces_of_the_caller():
                  lambda: pk.qk_norm_backward(q, q, q, q, wq=w, workspace=ws[:64])):
         with pytest.raises(pk.OsdnError, match="too small"):
             call()
+
+
+@pytest.mark.gpu
+def test_a_scale_that_changes_in_place():
+    import preconditioned_delta_rule_token_b200 as pk
+    q = torch.randn(1, 3, 2, 64, generator=torch.Generator().manual_seed(7)).cuda()
+    s = torch.tensor(1.0)
+    a = pk.qk_norm(q, None, scale_q=s)[0]
+    s.fill_(2.0)
+    assert torch.equal(pk.qk_norm(q, None, scale_q=s)[0], 2 * a)
