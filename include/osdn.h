@@ -504,7 +504,7 @@ typedef struct {
     float scale_q, scale_k; /* factors on q and k */
     int32_t zero_rest;      /* rows from a sequence's length on: 0 left as they were, else written as zeros */
     int32_t reserved;       /* 0 */
-    int64_t pos0;           /* position of token 0 where positions is NULL */
+    int64_t pos0;           /* position of token 0 where positions is NULL (within +-2^53) */
     /* Element strides over (b, t, h), as in osdn_params: all zero for dense
      * [B, T, H, width], else non-negative multiples of 8; those of outputs keep
      * the rows apart. out_q and out_k: q_out and k_out in the forward, the

@@ -98,6 +98,13 @@ def _held(dev, name, t, shape, dtype, dense=True):
         _bad("%s is not contiguous" % name)
 
 
+def _fits(**sizes):
+    """The parameter blocks hold sizes in 32 bits: a larger one would come out as its remainder."""
+    for name, n in sizes.items():
+        if n >= 1 << 31:
+            _bad("%s must be below 2^31 (got %d)" % (name, n))
+
+
 def _scratch(dev, workspace):
     """Checks a workspace that the caller gave: dense memory of the tensors' device (its size is the library's check)."""
     if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_cuda:
@@ -138,6 +145,7 @@ def _recur_params(x, gate, gate_form, input_scale, named, token=True):
     _held(dev, "gate", gate, x.shape, gate.dtype, dense=False)
     p = B.osdn_recur_params()
     p.struct_size = ctypes.sizeof(p)
+    _fits(B=nB, T=T, D=D)
     p.B, p.T, p.D, p.dtype, p.gate_dtype = nB, T, D, code, gcode
     p.gate_form = _choice("gate_form", gate_form, B.GATE_FORMS)
     p.input_scale = _choice("input_scale", input_scale, B.INPUT_SCALES)
@@ -246,6 +254,9 @@ def _heads_params(q, k, freqs, positions, lengths, norm, layout, wq, wk, out_q, 
     Hk = 0 if k is None else k.shape[2]
     p = B.osdn_qk_params()
     p.struct_size = ctypes.sizeof(p)
+    _fits(B=nB, T=T, Hq=Hq, Hk=Hk, width=width, rot_dim=0 if freqs is None else 2 * freqs.numel())
+    if abs(numbers[-1]) > 1 << 53:
+        _bad("pos0 must lie within +-2^53 (got %d)" % numbers[-1])
     p.B, p.T, p.Hq, p.Hk, p.width, p.dtype = nB, T, Hq, Hk, width, _dtype(names[0], q)
     p.norm, p.layout = _choice("norm", norm, B.NORMS), _choice("layout", layout, B.ROPE_LAYOUTS)
     p.eps, p.amplitude, p.scale_q, p.scale_k, p.pos0 = numbers

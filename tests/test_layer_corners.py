@@ -215,6 +215,29 @@ def test_numbers_are_taken_by_value(fake_layer):
         layer.rope(q, f, pos0=1.5)
 
 
+def test_sizes_past_32_bits_are_refused(fake_layer):
+    """Sequences, tokens, channels and heads of 2^31 and more (of expanded tensors: no memory is needed), and a
+    position past 2^53: refused, not taken by their remainder."""
+    import preconditioned_delta_rule_token_b200 as pk
+    layer, calls = fake_layer
+    n = (1 << 32) + 5
+    x = lambda *s: _fake(1, 1, 8).expand(*s)  # noqa: E731
+    head = lambda *s: _fake(1, 1, 1, 8).expand(*s)  # noqa: E731
+    f = _fake(4, dtype=torch.float64)
+    for call in (lambda: layer.recurrence(x(1, n, 8), x(1, n, 8)), lambda: layer.recurrence(x(n, 1, 8), x(n, 1, 8)),
+                 lambda: layer.recurrence_backward(x(1, n, 8), x(1, n, 8), x(1, n, 8)),
+                 lambda: layer.recurrence_step(x(1, n, 8)[0], x(1, n, 8)[0], _fake(5, 8)),
+                 lambda: layer.qk_norm(head(1, n, 1, 8), None), lambda: layer.qk_norm(head(n, 1, 1, 8), None),
+                 lambda: layer.qk_norm(head(1, 2, 1, 8), head(1, 2, n, 8)), lambda: layer.rope(head(1, 2, n, 8), f),
+                 lambda: layer.rope(head(1, 2, 1, 8), _fake(1, dtype=torch.float64).expand(n))):
+        with pytest.raises(pk.OsdnError, match="below 2\\^31"):
+            call()
+    for pos0 in (1 << 64, (1 << 53) + 1, -(1 << 53) - 1):
+        with pytest.raises(pk.OsdnError, match="pos0"):
+            layer.rope(_fake(1, 2, 1, 8), f, pos0=pos0)
+    assert not calls.reached
+
+
 # ------------------------------------------------------------------ GPU: the recurrence
 
 @pytest.mark.gpu
