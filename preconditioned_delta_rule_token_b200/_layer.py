@@ -325,6 +325,8 @@ def qk_norm_backward(q, k, dq_out, dk_out, freqs=None, positions=None, norm="l2"
     g = {"dq": _C.like(q), "dk": None if k is None else _C.like(k),
          "dwq": None if wq is None else _C.like(wq),
          "dwk": None if wk is None or k is None else _C.like(wk)}
+    if g["dwk"] is not None and not k.shape[2]:   # no key heads: the library takes k, and so wk, as not given
+        g["dwk"].zero_()
     if workspace is not None:
         _scratch(q.device, workspace)
     elif g["dwq"] is not None or g["dwk"] is not None:

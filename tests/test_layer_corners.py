@@ -238,6 +238,15 @@ def test_sizes_past_32_bits_are_refused(fake_layer):
     assert not calls.reached
 
 
+def test_no_key_heads_leave_a_zero_weight_gradient(fake_layer, monkeypatch):
+    """k [B,T,0,width] with a weight: an empty dk, and dwk the sum over no rows."""
+    layer, calls = fake_layer
+    monkeypatch.setattr(calls, "like", lambda t: torch.full(t.shape, 7.0))
+    q, k, w = _fake(1, 2, 3, 64), _fake(1, 2, 0, 64), _fake(64)
+    g = layer.qk_norm_backward(q, k, q, k, wq=w, wk=w, workspace=_fake(1 << 12))
+    assert g["dk"].shape == (1, 2, 0, 64) and bool((g["dwk"] == 0).all())
+
+
 # ------------------------------------------------------------------ GPU: the recurrence
 
 @pytest.mark.gpu
@@ -379,3 +388,14 @@ def test_a_scale_that_changes_in_place():
     a = pk.qk_norm(q, None, scale_q=s)[0]
     s.fill_(2.0)
     assert torch.equal(pk.qk_norm(q, None, scale_q=s)[0], 2 * a)
+
+
+@pytest.mark.gpu
+def test_no_key_heads():
+    import preconditioned_delta_rule_token_b200 as pk
+    q, w = torch.randn(1, 3, 2, 64, generator=torch.Generator().manual_seed(8)).cuda(), torch.ones(64, device="cuda")
+    k = q[:, :, :0].contiguous()
+    out, got = pk.qk_norm(q, k, wq=w, wk=w), pk.qk_norm_backward(q, k, q, k, wq=w, wk=w)
+    want = pk.qk_norm_backward(q, None, q, None, wq=w)
+    assert torch.equal(out[0], pk.qk_norm(q, None, wq=w)[0]) and out[1].shape == got["dk"].shape == (1, 3, 0, 64)
+    assert torch.equal(got["dq"], want["dq"]) and torch.equal(got["dwq"], want["dwq"]) and bool((got["dwk"] == 0).all())
