@@ -440,8 +440,8 @@ typedef struct {
  * becomes of their rows of h.
  * h [B, T, D] (NULL: not written); final_h [B, D] fp32, the state after each
  * sequence's last token (h0 for length 0; nullable); checkpoints
- * [B, ceil(T / 64), D] fp32, the state before every 64th token, for the backward
- * (nullable). Any D, T and element-aligned x, gate and h are accepted (rows and D in
+ * [B, ceil(T / 64), D] fp32, the state before every 64th token (behind a sequence's
+ * length: its final state), for the backward (nullable). Any D, T and element-aligned x, gate and h are accepted (rows and D in
  * whole 16 bytes and no stride of 0 run fastest); fp32 states are 16-byte
  * aligned. h must not overlap x or gate. No workspace; bitwise reproducible.
  * Errors: OSDN_ERR_INVALID_ARG, OSDN_ERR_UNSUPPORTED, OSDN_ERR_CUDA. */

@@ -173,7 +173,8 @@ def recurrence(x, gate, h0=None, lengths=None, gate_form="decay", input_scale="n
     h0 [B,D] fp32 or None (zeros). lengths [B] int32 (None: T each): tokens from a sequence's length
     on do not count; their rows of h are zeros (left as they were when `h` is given).
     Returns (h [B,T,D] in x's type, final_h [B,D] fp32), and with checkpoints=True the states
-    [B,ceil(T/64),D] fp32 that recurrence_backward takes."""
+    [B,ceil(T/64),D] fp32 before every 64th token (behind a length: the final state) that
+    recurrence_backward takes."""
     key = ("fwd", gate_form, input_scale, _C.layouts(x, gate, h0, lengths, h))
     kept = _RECUR.get(key) or _RECUR.keep(key, _recur_params(
         x, gate, gate_form, input_scale, (("h0", h0, "state"), ("lengths", lengths, "lengths"), ("h", h, "token"))))

@@ -285,6 +285,27 @@ def test_log_gates_below_the_normal_range(gdt, D):
         ref.close(t, *want[k], 24 * 70 + 96, k)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("types", ((torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32), (torch.float32, torch.float32)))
+@pytest.mark.parametrize("B,T,D", ((7, 200, 24), (7, 200, 33), (7, 200, 34), (2, 2049, 72), (200, 70, 512)))
+def test_saved_states_behind_a_length(types, B, T, D):
+    """checkpoints[b, i] is the state before token 64 i, and behind the length the final state; the others are
+    those of the same sequence without lengths."""
+    import preconditioned_delta_rule_token_b200 as pk
+    g = torch.Generator().manual_seed(9)
+    dt, gdt = types
+    x, gate = torch.randn(B, T, D, generator=g).to(dt).cuda(), torch.rand(B, T, D, generator=g).to(gdt).cuda()
+    h0 = torch.randn(B, D, generator=g).cuda()
+    lengths = torch.tensor(([0, 1, 64, 65, 128, T, T + 9] * B)[:B], dtype=torch.int32)
+    for h in (None, torch.empty_like(x)):
+        _, final, marks = pk.recurrence(x, gate, h0=h0, lengths=lengths.cuda(), h=h, checkpoints=True)
+        whole = pk.recurrence(x, gate, h0=h0, checkpoints=True)[2]
+        for b in range(B):
+            first = (min(int(lengths[b]), T) + 63) // 64          # the first state behind the length
+            assert torch.equal(marks[b, :first], whole[b, :first])
+            assert torch.equal(marks[b, first:], final[b].expand_as(marks[b, first:]))
+
+
 # ------------------------------------------------------------------ GPU: the norms
 
 @pytest.mark.gpu
