@@ -428,7 +428,8 @@ typedef struct {
     /* Element strides of x, gate and h over (b, t); the channels are contiguous.
      * Both zero: dense [B, T, D]. Otherwise 0 .. 2^38; those of h keep its rows
      * apart. stride_h is also the stride of dh in the backward; dx and dgate are
-     * dense. osdn_recur_step reads the b strides alone. */
+     * dense. osdn_recur_step reads the b strides alone (0 beside a t stride that is not
+     * 0: one row of x or gate for all sequences). */
     int64_t stride_x[2];
     int64_t stride_gate[2];
     int64_t stride_h[2];

@@ -126,6 +126,14 @@ def _strides(name, t, n):
     return st[:n]
 
 
+def _rows(name, t, token):
+    """Strides over (b, t) of an input of the recurrence; without tokens, one row for all sequences is (0, not 0)."""
+    if token:
+        return _strides(name, t, 2)
+    one = t.shape[0] > 1 and t.stride(0) == 0 and (t.stride(1) == 1 or t.shape[1] == 1)
+    return (0, t.shape[1]) if one else (*_strides(name, t, 1), 0)
+
+
 def _saved(nB, T, D):
     return nB, (T + B.OSDN_RECUR_CHECKPOINT - 1) // B.OSDN_RECUR_CHECKPOINT, D
 
@@ -151,7 +159,7 @@ def _recur_params(x, gate, gate_form, input_scale, named, token=True):
     p.input_scale = _choice("input_scale", input_scale, B.INPUT_SCALES)
     p.zero_rest = not any(t is not None for name, t, _ in named if name == "h")   # our own outputs
     n = 2 if token else 1
-    p.stride_x[:n], p.stride_gate[:n] = _strides("x", x, n), _strides("gate", gate, n)
+    p.stride_x[:], p.stride_gate[:] = _rows("x", x, token), _rows("gate", gate, token)
     for name, t, kind in named:
         if kind == "token":
             _held(dev, name, t, x.shape, x.dtype, dense=False)
@@ -219,7 +227,8 @@ def recurrence_backward(x, gate, dh, h0=None, dfinal_h=None, lengths=None, check
 
 
 def recurrence_step(x, gate, state, gate_form="decay", input_scale="none", out=None, stream=None):
-    """One decode token of the recurrence: x, gate [B,D]; state [B,D] fp32, updated in place.
+    """One decode token of the recurrence: x, gate [B,D] (or one row of them expanded over the batch); state [B,D]
+    fp32, updated in place.
     Returns the new state in x's type [B,D] (`out` if given)."""
     key = ("step", gate_form, input_scale, _C.layouts(x, gate, state, out))
     kept = _RECUR.get(key) or _RECUR.keep(key, _recur_params(

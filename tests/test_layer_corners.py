@@ -247,6 +247,18 @@ def test_no_key_heads_leave_a_zero_weight_gradient(fake_layer, monkeypatch):
     assert g["dk"].shape == (1, 2, 0, 64) and bool((g["dwk"] == 0).all())
 
 
+def test_a_step_reads_one_row_for_the_batch(fake_layer):
+    """The strides that reach the library: 0 over the sequences, beside one that says that this is not the dense layout."""
+    layer, calls = fake_layer
+    x, one, state = _fake(3, 8), _fake(1, 8).expand(3, 8), _fake(3, 8)
+    for a, b in ((x, one), (one, x), (one, one)):
+        layer.recurrence_step(a, b, state)
+        p = layer.B.osdn_recur_params.from_address(calls.reached[-1][1])
+        for t, strides in ((a, p.stride_x), (b, p.stride_gate)):
+            assert tuple(strides) == ((0, 8) if t is one else (0, 0))
+        assert tuple(p.stride_h) == (0, 0)
+
+
 # ------------------------------------------------------------------ GPU: the recurrence
 
 @pytest.mark.gpu
@@ -304,6 +316,29 @@ def test_saved_states_behind_a_length(types, B, T, D):
             first = (min(int(lengths[b]), T) + 63) // 64          # the first state behind the length
             assert torch.equal(marks[b, :first], whole[b, :first])
             assert torch.equal(marks[b, first:], final[b].expand_as(marks[b, first:]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("types", ((torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32), (torch.float32, torch.float32)))
+@pytest.mark.parametrize("B,D", ((5, 64), (3, 33), (4, 1), (1, 8)))
+def test_a_step_with_one_row_for_the_batch(types, B, D):
+    """x or gate expanded over the sequences, as recurrence reads them: the values of the tensor in memory."""
+    import preconditioned_delta_rule_token_b200 as pk
+    g = torch.Generator().manual_seed(10)
+    dt, gdt = types
+    x, gate = torch.randn(B, D, generator=g).to(dt).cuda(), torch.randn(B, D, generator=g).to(gdt).cuda()
+    h0 = torch.randn(B, D, generator=g).cuda()
+    for a, b in ((x, gate[:1].expand(B, D)), (x[:1].expand(B, D), gate), (x[-1:].expand(B, D), gate[-1:].expand(B, D))):
+        s, t = h0.clone(), h0.clone()
+        got = pk.recurrence_step(a, b, s, gate_form="logit")
+        assert torch.equal(got, pk.recurrence_step(a.contiguous(), b.contiguous(), t, gate_form="logit"))
+        assert torch.equal(s, t)
+    if B > 1:
+        with pytest.raises(pk.OsdnError):        # a result for each sequence needs its own row
+            pk.recurrence_step(x, gate, h0.clone(), out=torch.empty_like(x[:1]).expand(B, D))
+        if D > 1:
+            with pytest.raises(pk.OsdnError):
+                pk.recurrence_step(x, gate[:1, :1].expand(B, D), h0.clone())
 
 
 # ------------------------------------------------------------------ GPU: the norms
