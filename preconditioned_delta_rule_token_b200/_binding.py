@@ -91,7 +91,8 @@ def build_if_missing() -> str:
     return build(force=False)
 
 
-CALL_PATH = os.path.join(_PKG, "_call" + sysconfig.get_config_var("EXT_SUFFIX"))
+# The extension module is compiled against torch's C++ headers: one file for each torch.
+CALL_PATH = os.path.join(_PKG, "_call." + torch.__version__ + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
 def build_call(force: bool = False) -> str:

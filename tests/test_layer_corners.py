@@ -259,6 +259,14 @@ def test_a_step_reads_one_row_for_the_batch(fake_layer):
         assert tuple(p.stride_h) == (0, 0)
 
 
+def test_the_extension_module_belongs_to_this_torch(osdn_lib):
+    """It is compiled against torch's C++ headers, so another torch has to get another file, and not load this one."""
+    import os
+    assert torch.__version__ in os.path.basename(osdn_lib.CALL_PATH)
+    osdn_lib.build_call()
+    assert os.path.exists(osdn_lib.CALL_PATH) and osdn_lib.call().layouts(None) == (-1).to_bytes(8, "little", signed=True)
+
+
 # ------------------------------------------------------------------ GPU: the recurrence
 
 @pytest.mark.gpu
