@@ -1753,7 +1753,7 @@ int osdn_recur_step(const osdn_recur_params* p, const void* x, const void* gate,
         const int64_t n = (int64_t)q.B * (q.D / v), blocks = (n + 255) / 256;
         const cudaError_t e =
             launch_chained(osdn::recur::step_kernel<v, decltype(tx), decltype(tg)>,
-                           dim3((unsigned)std::min<int64_t>(blocks, 148 * 8)), 256, 0,
+                           dim3((unsigned)std::min<int64_t>(blocks, 8LL * sm_count())), 256, 0,
                            reinterpret_cast<cudaStream_t>(cuda_stream), a);
         return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "recurrence step launch");
     };

@@ -463,3 +463,22 @@ def test_no_key_heads():
     want = pk.qk_norm_backward(q, None, q, None, wq=w)
     assert torch.equal(out[0], pk.qk_norm(q, None, wq=w)[0]) and out[1].shape == got["dk"].shape == (1, 3, 0, 64)
     assert torch.equal(got["dq"], want["dq"]) and torch.equal(got["dwq"], want["dwq"]) and bool((got["dwk"] == 0).all())
+
+
+@pytest.mark.gpu
+def test_a_step_larger_than_its_grid():
+    """More channels than threads at a time (eight blocks of 256 an SM, four channels or one a thread)."""
+    import preconditioned_delta_rule_token_b200 as pk
+    g = torch.Generator(device="cuda").manual_seed(11)
+    for B, D in ((700, 4096), (700, 1001)):
+        x, gate, state = (torch.randn(B, D, generator=g, device="cuda") for _ in range(3))
+        rows = state.clone()
+        out = pk.recurrence_step(x, gate, rows, gate_form="logit", input_scale="complement")
+        for i in (0, 1, B // 2, B - 1):              # each sequence alone gives the same bits
+            one = state[i:i + 1].clone()
+            want = pk.recurrence_step(x[i:i + 1], gate[i:i + 1], one, gate_form="logit", input_scale="complement")
+            assert torch.equal(out[i:i + 1], want) and torch.equal(rows[i:i + 1], one)
+        a = torch.sigmoid(gate.double())
+        h = a * state.double() + (1 - a) * x.double()
+        # 12 + 48 roundings of the terms, as for one token in test_recurrence.py
+        assert bool(((rows.double() - h).abs() <= 60 * 2.0 ** -24 * (a * state.double().abs() + x.double().abs())).all())
