@@ -246,8 +246,8 @@ _HEADS = _Kept()
 
 
 def _numbers(eps, amplitude, scale_q, scale_k, pos0):
-    """The numbers of a call by value: a block is kept by them, and a tensor in their place (a learned scale) would
-    be known by its identity while its value changes."""
+    """The numbers of a call by value: a block is kept by them alone, for a tensor in their place (a learned scale) is
+    known by its identity while its value changes. It meets no kept block, and is converted on every call."""
     try:
         return float(eps), float(amplitude), float(scale_q), float(scale_k), operator.index(pos0)
     except (TypeError, ValueError, RuntimeError):
@@ -299,10 +299,12 @@ def qk_norm(q, k, freqs=None, positions=None, norm="l2", eps=1e-6, wq=None, wk=N
     [B,T] int64 (None: pos0 + t). lengths [B] int32: tokens from a sequence's length on give zeros
     (rows of a given q_out, k_out stay as they were). q_out may be q, k_out may be k.
     Returns (q_out, k_out)."""
-    numbers = _numbers(eps, amplitude, scale_q, scale_k, pos0)
-    key = (norm, layout, numbers, _C.layouts(q, k, freqs, positions, lengths, wq, wk, q_out, k_out))
-    kept = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
-        q, k, freqs, positions, lengths, norm, layout, wq, wk, q_out, k_out, numbers, ("q", "k", "q_out", "k_out")))
+    layouts = _C.layouts(q, k, freqs, positions, lengths, wq, wk, q_out, k_out)
+    kept = _HEADS.get((norm, layout, (eps, amplitude, scale_q, scale_k, pos0), layouts))
+    if kept is None:
+        numbers = _numbers(eps, amplitude, scale_q, scale_k, pos0)
+        kept = _HEADS.keep((norm, layout, numbers, layouts), _heads_params(
+            q, k, freqs, positions, lengths, norm, layout, wq, wk, q_out, k_out, numbers, ("q", "k", "q_out", "k_out")))
     if stream is not None or not _C.here(q):
         with _scope(q.device, stream):
             return qk_norm(q, k, freqs, positions, norm, eps, wq, wk, layout, amplitude, scale_q, scale_k, pos0, lengths,
@@ -324,10 +326,13 @@ def qk_norm_backward(q, k, dq_out, dk_out, freqs=None, positions=None, norm="l2"
     [width] fp32 (None without the weight)."""
     if (k is None) != (dk_out is None):
         _bad("k and dk_out go together")
-    numbers = _numbers(eps, amplitude, scale_q, scale_k, pos0)
-    key = ("bwd", norm, layout, numbers, _C.layouts(q, k, freqs, positions, lengths, wq, wk, dq_out, dk_out))
-    kept = _HEADS.get(key) or _HEADS.keep(key, _heads_params(
-        q, k, freqs, positions, lengths, norm, layout, wq, wk, dq_out, dk_out, numbers, ("q", "k", "dq_out", "dk_out")))
+    layouts = _C.layouts(q, k, freqs, positions, lengths, wq, wk, dq_out, dk_out)
+    kept = _HEADS.get(("bwd", norm, layout, (eps, amplitude, scale_q, scale_k, pos0), layouts))
+    if kept is None:
+        numbers = _numbers(eps, amplitude, scale_q, scale_k, pos0)
+        kept = _HEADS.keep(("bwd", norm, layout, numbers, layouts), _heads_params(
+            q, k, freqs, positions, lengths, norm, layout, wq, wk, dq_out, dk_out, numbers,
+            ("q", "k", "dq_out", "dk_out")))
     if stream is not None or not _C.here(q):
         with _scope(q.device, stream):
             return qk_norm_backward(q, k, dq_out, dk_out, freqs, positions, norm, eps, wq, wk, layout, amplitude, scale_q,
@@ -375,14 +380,15 @@ def rope(x, freqs, positions=None, layout="half", amplitude=1.0, scale=1.0, pos0
     """The position rotation alone on x [B,T,H,width]: see qk_norm for freqs, positions, layout and lengths.
     inverse=True turns back with the same amplitude: it takes the gradient of the result to that of x.
     `out` may be x. Returns the rotated tensor."""
-    numbers = _numbers(0.0, amplitude, scale, 1.0, pos0)
-    key = ("rope", layout, numbers, _C.layouts(x, freqs, positions, lengths, out))
-    kept = _HEADS.get(key)
+    layouts = _C.layouts(x, freqs, positions, lengths, out)
+    kept = _HEADS.get(("rope", layout, (0.0, amplitude, scale, 1.0, pos0), layouts))
     if kept is None:
         if freqs is None:
             _bad("freqs is needed")
-        kept = _HEADS.keep(key, _heads_params(x, None, freqs, positions, lengths, "none", layout, None, None, out, None,
-                                              numbers, ("x", None, "out", None)))
+        numbers = _numbers(0.0, amplitude, scale, 1.0, pos0)
+        kept = _HEADS.keep(("rope", layout, numbers, layouts), _heads_params(
+            x, None, freqs, positions, lengths, "none", layout, None, None, out, None, numbers,
+            ("x", None, "out", None)))
     if stream is not None or not _C.here(x):
         with _scope(x.device, stream):
             return rope(x, freqs, positions, layout, amplitude, scale, pos0, inverse, lengths, out)
