@@ -1750,10 +1750,12 @@ int osdn_recur_step(const osdn_recur_params* p, const void* x, const void* gate,
     bool four = q.D % 4 == 0 && !((a.xb | a.gb | a.hb) % 4);   // four channels a thread where all rows allow it
     for (int i = 0; i < 3; ++i) four = four && element_aligned(ptrs[i], 4 * each[i]);
     auto go = [&](auto v, auto tx, auto tg) {
-        const int64_t n = (int64_t)q.B * (q.D / v), blocks = (n + 255) / 256;
+        const int64_t n = (int64_t)q.B * (q.D / v), needed = (n + 255) / 256;
+        // eight CTAs an SM; up to 128 SMs' worth none is cut, and the device is not asked (0.15 us a call)
+        const int64_t blocks = needed <= 8 * 128 ? needed : std::min<int64_t>(needed, 8LL * sm_count());
         const cudaError_t e =
             launch_chained(osdn::recur::step_kernel<v, decltype(tx), decltype(tg)>,
-                           dim3((unsigned)std::min<int64_t>(blocks, 8LL * sm_count())), 256, 0,
+                           dim3((unsigned)blocks), 256, 0,
                            reinterpret_cast<cudaStream_t>(cuda_stream), a);
         return e == cudaSuccess ? OSDN_OK : cuda_fail(e, "recurrence step launch");
     };
