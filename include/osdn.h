@@ -407,7 +407,9 @@ int osdn_fwd_host_buffer_size(const osdn_params *p, int groups, size_t *bytes);
  *           sqrt(1 - a_t^2) (OSDN_INPUT_NORM; a_t in [0, 1]).
  * a_t = 0 (gate 0, or -infinity in the other forms) starts a new document. 1 - a
  * is formed from the gate without cancellation; products, states and sums are
- * fp32. A non-finite state stays non-finite (0 times infinity is NaN). */
+ * fp32. A non-finite state stays non-finite (0 times infinity is NaN). Up to 128
+ * consecutive decays are multiplied before they meet a state, so decays above 1 whose
+ * product overflows give infinities or NaN even where the state before them is 0. */
 typedef enum { OSDN_GATE_DECAY = 0, OSDN_GATE_LOG = 1, OSDN_GATE_LOGIT = 2 } osdn_gate_form;
 typedef enum { OSDN_INPUT_NONE = 0, OSDN_INPUT_COMPLEMENT = 1, OSDN_INPUT_NORM = 2 } osdn_input_scale;
 

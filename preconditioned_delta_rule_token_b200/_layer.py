@@ -4,12 +4,15 @@ queries and keys with the position rotation, and the rotation alone.
 Wrappers that check shapes, types and devices, allocate the outputs and call the C ABI.
 `stream` is a torch.cuda.Stream of the tensors' device (default: that device's current
 stream); outputs and workspaces are allocated on it. All tensors must be on one CUDA
-device; there is no CPU path.
+device; there is no CPU path. Heads, weights, states and workspaces start on 16 bytes;
+x, gate and h of the recurrence start anywhere. An output that is given does not overlap
+an input, unless it is said that it may be one.
 
 A decode token's kernels take a few microseconds, so a call does little in Python: the
-checks and the parameter block depend on the tensors' layouts alone (shape, strides,
-type, device) and are kept by them, and addresses and stream go through an extension
-module (csrc/call.cpp).
+checks and the parameter block depend on the tensors' layouts (shape, strides, type,
+device), the options and the numbers alone and are kept by them, and addresses and stream
+go through an extension module (csrc/call.cpp). pos0 is one of the numbers: in a loop over
+tokens a positions tensor keeps its block, a pos0 that counts up makes one each time.
 """
 from __future__ import annotations
 
@@ -202,7 +205,7 @@ def recurrence_backward(x, gate, dh, h0=None, dfinal_h=None, lengths=None, check
                         input_scale="none", workspace=None, stream=None):
     """Gradients of L = sum(dh * h) + sum(dfinal_h * final_h) for the recurrence() of the same inputs.
 
-    dh [B,T,D] in x's type; dfinal_h [B,D] fp32 or None (= 0). checkpoints: the states that
+    dh [B,T,D] in x's type (the channels contiguous); dfinal_h [B,D] fp32 or None (= 0). checkpoints: the states that
     recurrence(..., checkpoints=True) returned for the same inputs; None runs the forward again for them.
     Returns a dict with dx (x's type), dgate (the gate's type; with respect to the gate as given) and
     dh0 [B,D] fp32. Rows from a sequence's length on are zeros."""

@@ -14,8 +14,10 @@
 // Measured, bf16, forward B8 T4096 16 + 16 heads of 128 (L2, rotation) / rotation alone B1 T32768 16 heads:
 // a table a CTA and partners by shuffles 188 / 98 us; a warp a token, pairs in one lane 148 / 69; rows by
 // stepped pointers and an approximate root 104 / 54; rows loaded ahead of the angles, CTAs that stay
-// 100 / 47; a group of lanes a token 95 / 46 us, 88% and 90% of the measured copy rate, bound by
-// instruction issue (2.6 of 4 a cycle) before memory. Backward at the first size 151 us (82%).
+// 100 / 47; a group of lanes a token 94 / 46 us, 88% and 90% of the measured copy rate. What is left is the
+// latency of the loads: 4.1 of the 9.5 warps that wait an issue wait for them, at 22 warps an SM (80 registers), and
+// issue takes 2.4 of 4 a cycle. Backward at the first size 151 us (82%). fp32, B8 T2048 16 + 16 heads of 128:
+// forward 93, with the backward 228 us (89% and 73%).
 #pragma once
 #include <type_traits>
 

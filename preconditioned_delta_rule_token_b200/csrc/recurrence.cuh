@@ -17,12 +17,15 @@
 // Measured on the way (bf16 forward, B8 T4096 D2048, log gate, norm scale / B1 T32768, fp32 log gate):
 // one CTA a walk with plain loads 648 / 3720 us; clusters with a hardware barrier each step 255 / 242;
 // packed arithmetic 114 / 165; tensor-map tiles and counted remote stores 107 / 108; 16 tokens a run instead
-// of 8 in the forward (half the joins) 83 / 95; unpacking bf16 by shifts 80 / 92 us, 78% and 90% of
-// the measured copy rate. The first is then bound by instruction issue (21 an element; 2.2 of 4 a
-// cycle with two CTAs on most SMs and one on the rest), the second by memory. The backward, B8 T4096 D2048:
-// 141 us (logit, complement), 156 us (log, norm), 74% and 67%: 43 instructions an element in two walks over a
+// of 8 in the forward (half the joins) 83 / 95; unpacking bf16 by shifts 79 / 92 us, 79% and 90% of
+// the measured copy rate. The second is bound by memory. The first puts 256 equal CTAs on 296 places: the 108 SMs
+// that hold two set the time and issue 2.6 of 4 a cycle (21 instructions an element), the 40 that hold one are
+// done after two thirds of it; over all SMs 2.2 of 4 and 4.4 TB/s. The backward, B8 T4096 D2048:
+// 141 us (logit, complement), 156 us (log, norm), 74% and 67%: 44 instructions an element in two walks over a
 // run, and two CTAs an SM by registers. What did not pay in the forward: 16 warps a CTA (111 us where 8 took
 // 102), two warps that join for all behind a second barrier (107), scalar arithmetic (34 instructions, 105).
+// Rows that are not whole 16 bytes, B8 T2048 D1001 against D1024 with the same bytes an element: fp32 forward 67
+// us against 35, with the backward 169 against 95; bf16 84 against 25, and 187 against 72 (kLoads has none ahead).
 #pragma once
 #include <type_traits>
 
