@@ -482,3 +482,69 @@ def test_a_step_larger_than_its_grid():
         h = a * state.double() + (1 - a) * x.double()
         # 12 + 48 roundings of the terms, as for one token in test_recurrence.py
         assert bool(((rows.double() - h).abs() <= 60 * 2.0 ** -24 * (a * state.double().abs() + x.double().abs())).all())
+
+
+@pytest.mark.gpu
+def test_captured_training_step_and_decode_token():
+    """forward(), backward() and step() with qk captured into a graph and replayed with new inputs."""
+    import preconditioned_delta_rule_token_b200 as pk
+    B, T, H, W = 2, 192, 3, 128
+    g = torch.Generator().manual_seed(12)
+    new = lambda *s: torch.randn(s, generator=g).bfloat16().cuda()  # noqa: E731
+    q, k, v, dout, beta = new(B, T, H, W), new(B, T, H, W), new(B, T, H, W), new(B, T, H, W), new(B, T, H).sigmoid()
+    q2, k2 = new(B, T, H, W), new(B, T, H, W)
+    qk = pk.QkNorm(norm="rms", wq=torch.ones(W, device="cuda"), wk=torch.ones(W, device="cuda"),
+                   freqs=pk.rope_frequencies(W)[0], scale_k=W ** -0.5)
+    at = torch.full((B,), T, device="cuda")
+
+    def run():
+        out, S, d = pk.forward(q, k, v, beta, qk=qk, eta=0.1)
+        grads = pk.backward(q, k, v, beta, dout, qk=qk, eta=0.1)
+        token = pk.step(*(t[:, 0].contiguous() for t in (q, k, v, beta)), S, d, eta=0.1, qk=qk, positions=at)
+        return [out, S, d, token], [t for t in grads.values() if t is not None]
+
+    first = [t.clone() for t in (q, k)]
+    want = run()
+    q.copy_(q2), k.copy_(k2)
+    want2 = run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for (a, b), exp in (((q2, k2), want2), (first, want)):
+        q.copy_(a), k.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(exp[0], got[0]))
+        for x, y in zip(exp[1], got[1]):
+            assert float((x.double() - y.double()).abs().max()) <= BF16_TOL * float(x.double().abs().max())
+
+
+@pytest.mark.gpu
+def test_two_training_steps_at_once():
+    """forward() and backward() with qk in flight on two streams at a time give what they give alone."""
+    import preconditioned_delta_rule_token_b200 as pk
+    B, T, H, W = 2, 192, 3, 128
+    qk = pk.QkNorm(wq=torch.ones(W, device="cuda"), freqs=pk.rope_frequencies(W)[0])
+    cases = []
+    for seed in (13, 14):
+        g = torch.Generator().manual_seed(seed)
+        cases.append([torch.randn(B, T, H, W, generator=g).bfloat16().cuda() for _ in range(4)] +
+                     [torch.rand(B, T, H, generator=g).bfloat16().cuda()])
+
+    def run(c, stream):
+        q, k, v, dout, beta = c
+        out = pk.forward(q, k, v, beta, qk=qk, eta=0.1, stream=stream)
+        grads = pk.backward(q, k, v, beta, dout, qk=qk, eta=0.1, stream=stream)
+        return list(out), [t for t in grads.values() if t is not None]
+
+    want = [run(c, None) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [run(c, s) for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a[0], b[0]))
+        for x, y in zip(a[1], b[1]):
+            assert float((x.double() - y.double()).abs().max()) <= BF16_TOL * float(x.double().abs().max())
